@@ -80,6 +80,9 @@ extern "C" {
 
 typedef void *sgemm_stream_t; /* hipStream_t; NULL = the default stream */
 
+/* Element types of the calls that take one (i8gemm.h, experts.h). */
+enum sgemm_type { SGEMM_F32 = 0, SGEMM_F16 = 1, SGEMM_BF16 = 2, SGEMM_I8 = 3 };
+
 /* C = alpha * op(A) @ op(B) + beta * C for one matrix triple (batch = 1). */
 int sgemm(int transA, int transB, int M, int N, int K,
           float alpha, const float *A, int lda,
@@ -391,6 +394,46 @@ int sgemm_strided_batched_noalloc(int transA, int transB, int M, int N, int K,
                                   int batch, long long strideA, long long strideB,
                                   long long strideC, int splits,
                                   sgemm_stream_t stream);
+
+/*
+ * Products over rows sorted by group (expert; experts.h sorts them), the
+ * ragged form next to the batched ones: `groups` products whose row counts
+ * only the device knows.
+ *
+ * sgemm_grouped: rows offsets[g] <= m < offsets[g+1] of A (M x K) and C
+ * (M x N) make
+ *     C[m, :] = alpha * A[m, :] @ op(B_g) + beta * C[m, :],  B_g = B + g*strideB,
+ * B_g stored K x N (transB = 0) or N x K (transB = 1). With C's gradient as A
+ * and the other transB it is the gradient of A.
+ *
+ * sgemm_grouped_outer: the gradient of B. K is ragged instead: over the rows
+ * offsets[g] <= k < offsets[g+1] of A (K x M) and B (K x N)
+ *     C_g = alpha * sum_k A[k, :]^T B[k, :] + beta * C_g,    C_g = C + g*strideC,
+ * M x N; an empty group gives beta * C_g.
+ *
+ * offsets is a DEVICE array of groups + 1 nondecreasing ints within [0, number
+ * of rows]; the host never reads it. Groups may be empty. Rows before
+ * offsets[0] and from offsets[groups] on are neither read nor written. Values
+ * outside the range are brought into it, and a group whose end lies before its
+ * start is empty. alpha == 0 or K == 0: as above, A and B are not read. C_g
+ * must not overlap each other, A or B.
+ *
+ * Status codes: minus (a base for the call + the position of the first invalid
+ * argument in its own list), base 800 for sgemm_grouped and 900 for
+ * sgemm_grouped_outer, or -22. Leading dimensions are below 2^21. Execution
+ * and accuracy are as above (K is a group's own row count in the outer form).
+ */
+int sgemm_grouped(int transB, int M, int N, int K, int groups, const int *offsets,
+                  float alpha, const float *A, int lda,
+                               const float *B, int ldb, long long strideB,
+                  float beta,        float *C, int ldc,
+                  sgemm_stream_t stream);
+
+int sgemm_grouped_outer(int M, int N, int K, int groups, const int *offsets,
+                        float alpha, const float *A, int lda,
+                                     const float *B, int ldb,
+                        float beta,        float *C, int ldc, long long strideC,
+                        sgemm_stream_t stream);
 
 /*
  * Host-side check of the buffer-range bookkeeping the tile and streaming

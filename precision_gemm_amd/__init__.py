@@ -1,13 +1,20 @@
 """precision_gemm_amd — single-precision GEMM on MI355X (gfx950).
 
-A thin ctypes binding over ``libsgemm.so`` (built from ``csrc/sgemm.hip``;
-its C ABI is declared in ``include/sgemm.h``). The functions have the C
+A thin ctypes binding over ``libsgemm.so`` (built from ``csrc/``; its C ABI is
+declared in ``include/sgemm.h``, ``include/i8gemm.h`` and
+``include/experts.h``). The functions have the C
 names and argument order; they only marshal arguments (tensor -> device
 pointer, torch's current stream -> hipStream_t) and raise on a nonzero
 status. All arithmetic runs in the library's HIP kernels; there is no CPU or
 PyTorch fallback, and a missing library is an error.
 
     C = alpha * op(A) @ op(B) + beta * C            (fp32, row-major)
+
+Next to it stand the products of a mixture layer's experts: rows sorted by
+expert and back (expert_sort, expert_gather, expert_combine and its gradient),
+their fp32 products (sgemm_grouped, sgemm_grouped_outer), and products in 8-bit
+integers with scales for each token and channel (i8_quantize_rows, i8gemm,
+i8gemm_grouped).
 """
 from __future__ import annotations
 
@@ -24,6 +31,9 @@ __all__ = [
     "sgemm_set_dispatch_overrides", "sgemm_dispatch_override_count", "load_dispatch_overrides",
     "MAX_DISPATCH_OVERRIDES",
     "library_path",
+    "i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "expert_sort",
+    "expert_sort_workspace_size", "expert_gather", "expert_combine", "expert_combine_grad",
+    "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped", "sgemm_grouped_outer",
     "VARIANT_AUTO", "VARIANT_L256x128", "VARIANT_M128x128", "VARIANT_S64x64",
     "VARIANT_S64x64_V1", "VARIANT_T64x64", "VARIANT_L256x256", "VARIANT_S64x64_K2",
     "VARIANT_M128x128_DMA", "VARIANT_T32x64", "VARIANT_T64x32", "VARIANT_GEMV",
@@ -88,9 +98,9 @@ def _load():
     # torch's, and its device calls then fail. So torch, when installed, is
     # imported first.
     try:
-        import torch  # noqa: F401
+        import torch
     except ImportError:
-        pass
+        torch = None
     lib = ctypes.CDLL(path)
     i, f, p, ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
     lib.sgemm.restype = i
@@ -135,6 +145,9 @@ def _load():
     lib.sgemm_set_dispatch_overrides.argtypes = [ctypes.POINTER(ctypes.c_int), i]
     lib.sgemm_dispatch_override_count.restype = i
     lib.sgemm_dispatch_override_count.argtypes = []
+    if torch is not None:
+        from . import _experts
+        _experts.declare(lib)
     _lib = lib
     return lib
 
@@ -414,3 +427,19 @@ def matmul(A, B, C, alpha=1.0, beta=0.0, transA=False, transB=False, stream=None
         sgemm_strided_batched(transA, transB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc,
                               batch, A.stride(0), B.stride(0), C.stride(0), stream)
     return C
+
+
+# The calls whose operands are always tensors come from their own module, loaded
+# on first use: it needs torch, which importing this package does not.
+_EXPERTS = ("i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "expert_sort",
+            "expert_sort_workspace_size", "expert_gather", "expert_combine",
+            "expert_combine_grad", "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped",
+            "sgemm_grouped_outer")
+
+
+def __getattr__(name):
+    if name in _EXPERTS:
+        from . import _experts
+        value = globals()[name] = getattr(_experts, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

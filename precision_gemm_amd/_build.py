@@ -14,7 +14,8 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "sgemm.hip")
+CSRC = os.path.join(PKG, "csrc")
+SOURCES = [os.path.join(CSRC, f) for f in ("sgemm.hip", "i8gemm.hip", "experts.hip")]
 LIB = os.path.join(PKG, "libsgemm.so")
 INCLUDE = os.path.join(ROOT, "include")
 ARCH = "gfx950"
@@ -37,10 +38,23 @@ def flags(save_temps_dir: str | None = None) -> list[str]:
 
 
 def build(out: str = LIB, save_temps_dir: str | None = None) -> str:
+    """Compile every source (side by side) and link the library."""
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *flags(save_temps_dir), SRC, "-o", tmp]
-    subprocess.run(cmd, check=True, cwd=save_temps_dir or PKG)
-    os.replace(tmp, out)
+    cc = [f for f in flags(save_temps_dir) if f != "-shared"]
+    objects = ["%s.%s.o" % (tmp, os.path.basename(s)) for s in SOURCES]
+    try:
+        jobs = [subprocess.Popen([hipcc(), *cc, "-c", s, "-o", o], cwd=save_temps_dir or PKG)
+                for s, o in zip(SOURCES, objects)]
+        failed = [s for s, j in zip(SOURCES, jobs) if j.wait() != 0]
+        if failed:
+            raise RuntimeError("hipcc failed on " + ", ".join(failed))
+        subprocess.run([hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", *objects, "-o", tmp],
+                       check=True, cwd=save_temps_dir or PKG)
+        os.replace(tmp, out)
+    finally:
+        for path in objects + [tmp]:
+            if os.path.exists(path):
+                os.remove(path)
     return out
 
 

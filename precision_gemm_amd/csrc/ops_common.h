@@ -1,0 +1,106 @@
+// What the kernels of i8gemm.hip and experts.hip share: element types, loads
+// of any alignment, and the search of the group a row tile belongs to.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+#include "sgemm.h"
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// Vectors at any address: one global_load_dwordx4 or store each (the hardware
+// takes unaligned addresses, at a lower rate).
+typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef int i32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef int i32_any __attribute__((aligned(1)));
+
+__device__ __forceinline__ i32x4 load16(const void *p)
+{
+    return *static_cast<const i32x4_any *>(p);
+}
+
+__device__ __forceinline__ void store16(void *p, i32x4 v)
+{
+    *static_cast<i32x4_any *>(p) = v;
+}
+
+__host__ __device__ __forceinline__ int type_bytes(int type)
+{
+    return type == SGEMM_F32 ? 4 : type == SGEMM_I8 ? 1 : 2;
+}
+
+// A group's rows [lo, hi), brought into [0, rows] whatever the device array
+// holds.
+__device__ __forceinline__ void group_rows(const int *offsets, int g, int rows, int &lo, int &hi)
+{
+    lo = min(max(offsets[g], 0), rows);
+    hi = min(max(offsets[g + 1], lo), rows);
+}
+
+// Row tile `slot` of a grouped product: tiles of `bm` rows are counted group
+// by group. Every lane of the wave returns the same group, its first row and
+// row count, and the tile's first row within the group; false if the groups
+// have fewer tiles. A wave's lanes take groups/64 consecutive groups each and
+// add up their tiles with a scan over the lanes.
+__device__ __forceinline__ bool find_tile(const int *offsets, int groups, int rows, int bm,
+                                          int slot, int &g_out, int &lo_out, int &n_out,
+                                          int &m_out)
+{
+    const int lane = __lane_id();
+    const int per = (groups + 63) >> 6;
+    const int g0 = lane * per, g1 = min(g0 + per, groups);
+    int tiles = 0;
+    for (int g = g0; g < g1; ++g) {
+        int lo, hi;
+        group_rows(offsets, g, rows, lo, hi);
+        tiles += (hi - lo + bm - 1) / bm;
+    }
+    int upto = tiles; // tiles of lanes 0..lane
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(upto, d);
+        if (lane >= d)
+            upto += v;
+    }
+    const int before = upto - tiles;
+    const bool mine = slot >= before && slot < upto;
+    const unsigned long long who = __ballot(mine);
+    if (who == 0)
+        return false;
+    int g_at = 0, lo_at = 0, n_at = 0, m_at = 0;
+    if (mine) {
+        int left = slot - before;
+        for (int g = g0; g < g1; ++g) {
+            int lo, hi;
+            group_rows(offsets, g, rows, lo, hi);
+            const int t = (hi - lo + bm - 1) / bm;
+            if (left < t) {
+                g_at = g;
+                lo_at = lo;
+                n_at = hi - lo;
+                m_at = left * bm;
+                break;
+            }
+            left -= t;
+        }
+    }
+    const int src = __builtin_ctzll(who);
+    g_out = __builtin_amdgcn_readfirstlane(__shfl(g_at, src));
+    lo_out = __builtin_amdgcn_readfirstlane(__shfl(lo_at, src));
+    n_out = __builtin_amdgcn_readfirstlane(__shfl(n_at, src));
+    m_out = __builtin_amdgcn_readfirstlane(__shfl(m_at, src));
+    return true;
+}
+
+// Most row tiles that `groups` groups over `rows` rows can have.
+inline long long most_tiles(int rows, int groups, int bm)
+{
+    return rows / bm + (groups < rows ? groups : rows);
+}
+
+inline long long ceil_div_ll(long long a, long long b) { return (a + b - 1) / b; }
+
+} // namespace

@@ -2923,6 +2923,268 @@ extern "C" int sgemm_strided_batched_noalloc(int transA, int transB, int M, int 
     return r == -21 ? -23 : r;
 }
 
+#include "ops_common.h"
+#include "status.h"
+
+// ---------------------------------------------------------------------------
+// Products over rows sorted by group.
+//
+// Row tiles are counted group by group on the device: a workgroup finds the
+// group its tile belongs to from the offsets (find_tile), and the grid has the
+// most tiles that any offsets can need; the others end at once. The tile
+// itself is sgemm_mfma_kernel's: the same staging (Operand), LDS layout, k
+// order and epilogue, so a group's rows get the bits of that tile kernel.
+// ---------------------------------------------------------------------------
+namespace {
+
+struct GroupedParams {
+    Params p;            // M, N, K: of the whole call; batch strides as needed
+    const int *offsets;
+    int groups;
+    long long stride;    // of B (rows product) or C (outer product)
+};
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, bool A_KC, bool B_KC, int VEC>
+__device__ __forceinline__ void grouped_tile(const Params &p, const float *Ab, const float *Bb,
+                                             float *Cb, int Kt, int m0, int n0, float *lds)
+{
+    constexpr int BK = kBK, NT = 64 * WAVES_M * WAVES_N;
+    constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 32, TN = WN / 32;
+    constexpr int NQ = BK / 8;
+    using OpA = Operand<A_KC, BM, BK, NT, VEC>;
+    using OpB = Operand<B_KC, BN, BK, NT, VEC>;
+    constexpr int STAGE = OpA::STAGE + OpB::STAGE;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm0 = (wave % WAVES_M) * WM, wn0 = (wave / WAVES_M) * WN;
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            acc[i][j] = f32x16{};
+
+    if (Kt > 0) {
+        const int kfirst = Kt % BK == 0 ? 0 : Kt % BK - BK;
+        OpA opa;
+        opa.X = Ab;
+        opa.ld = p.lda;
+        opa.total = A_KC ? (long long)(p.M - 1) * p.lda + Kt : (long long)(Kt - 1) * p.lda + p.M;
+        opa.O = p.M;
+        opa.K = Kt;
+        opa.o0 = m0;
+        opa.init(tid, kfirst);
+        OpB opb;
+        opb.X = Bb;
+        opb.ld = p.ldb;
+        opb.total = B_KC ? (long long)(p.N - 1) * p.ldb + Kt : (long long)(Kt - 1) * p.ldb + p.N;
+        opb.O = p.N;
+        opb.K = Kt;
+        opb.o0 = n0;
+        opb.init(tid, kfirst);
+
+        const int nsteps = (Kt + BK - 1) / BK;
+        f32x4 ra[OpA::SLOTS], rb[OpB::SLOTS];
+        opa.template load_next<true>(tid, ra);
+        opb.template load_next<true>(tid, rb);
+        for (int s = 0; s < nsteps; ++s) {
+            float *cur = lds + (s & 1) * STAGE;
+            OpA::store(cur, tid, ra);
+            OpB::store(cur + OpA::STAGE, tid, rb);
+            // (After the last step the window lies past K; what a lane reads
+            // there, inside the operand or zeros, is not used.)
+            opa.template load_next<false>(tid, ra);
+            opb.template load_next<false>(tid, rb);
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                float fa[TM][4], fb[TN][4];
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    OpA::frag(cur, wm0 + 32 * i, q, lane, fa[i]);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    OpB::frag(cur + OpA::STAGE, wn0 + 32 * j, q, lane, fb[j]);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int j = 0; j < TN; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                                fa[i][kk], fb[j][kk], acc[i][j], 0, 0, 0);
+            }
+        }
+    }
+    float res[TM][TN][16];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                res[i][j][v] = acc[i][j][v];
+    store_tile<TM, TN, 16>(p, Cb, m0, n0, wm0, wn0, 0, lane, res);
+}
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int MIN_WAVES_PER_EU, bool B_KC, int VEC>
+__global__ void
+__attribute__((amdgpu_flat_work_group_size(64 * WAVES_M * WAVES_N, 64 * WAVES_M * WAVES_N),
+               amdgpu_waves_per_eu(MIN_WAVES_PER_EU)))
+sgemm_grouped_kernel(GroupedParams gp)
+{
+    __shared__ __attribute__((aligned(16))) float lds[2 * (BM + BN) * kBK];
+    Params p = gp.p;
+    int g, lo, m0;
+    const int slot = blockIdx.x / p.tiles_n, n0 = blockIdx.x % p.tiles_n * BN;
+    if (!find_tile(gp.offsets, gp.groups, p.M, BM, slot, g, lo, p.M, m0))
+        return;
+    grouped_tile<BM, BN, WAVES_M, WAVES_N, true, B_KC, VEC>(
+        p, p.A + (long long)lo * p.lda, p.B + g * gp.stride, p.C + (long long)lo * p.ldc, p.K, m0,
+        n0, lds);
+}
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int MIN_WAVES_PER_EU, int VEC>
+__global__ void
+__attribute__((amdgpu_flat_work_group_size(64 * WAVES_M * WAVES_N, 64 * WAVES_M * WAVES_N),
+               amdgpu_waves_per_eu(MIN_WAVES_PER_EU)))
+sgemm_grouped_outer_kernel(GroupedParams gp)
+{
+    __shared__ __attribute__((aligned(16))) float lds[2 * (BM + BN) * kBK];
+    Params p = gp.p;
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int g = blockIdx.x / tiles, t = blockIdx.x % tiles;
+    int lo, hi;
+    group_rows(gp.offsets, g, p.K, lo, hi);
+    int n = __builtin_amdgcn_readfirstlane(hi - lo);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    if (p.alpha == 0.0f)
+        n = 0;
+    if (n == 0) {
+        if (p.beta == 1.0f)
+            return;
+        p.alpha = 0.0f;
+    }
+    grouped_tile<BM, BN, WAVES_M, WAVES_N, false, false, VEC>(
+        p, p.A + (long long)lo * p.lda, p.B + (long long)lo * p.ldb, p.C + g * gp.stride, n,
+        t / p.tiles_n * BM, t % p.tiles_n * BN, lds);
+}
+
+typedef void (*GroupedFn)(GroupedParams);
+
+int launch_grouped(GroupedFn fn, GroupedParams gp, long long blocks, int threads, hipStream_t s)
+{
+    if (blocks * threads > INT32_MAX)
+        return -22;
+    void *args[] = {&gp};
+    return (int)hipLaunchKernel((const void *)fn, dim3((unsigned)blocks), dim3(threads), args, 0,
+                                s);
+}
+
+} // namespace
+
+extern "C" int sgemm_grouped(int transB, int M, int N, int K, int groups, const int *offsets,
+                             float alpha, const float *A, int lda, const float *B, int ldb,
+                             long long strideB, float beta, float *C, int ldc,
+                             sgemm_stream_t stream)
+{
+    if (transB != 0 && transB != 1) return -801;
+    if (M < 0) return -802;
+    if (N < 0) return -803;
+    if (K < 0) return -804;
+    if (groups < 0) return -805;
+    const int rowB = transB ? K : N;
+    if (lda < (K > 1 ? K : 1) || lda > kMaxLd) return -809;
+    if (ldb < (rowB > 1 ? rowB : 1) || ldb > kMaxLd) return -811;
+    if (strideB < 0) return -812;
+    if (ldc < (N > 1 ? N : 1) || ldc > kMaxLd) return -815;
+    if (M == 0 || N == 0 || groups == 0)
+        return 0;
+    const bool product = K > 0 && alpha != 0.0f;
+    if (!product && beta == 1.0f)
+        return 0;
+    if (offsets == nullptr) return -806;
+    if (product && A == nullptr) return -808;
+    if (product && B == nullptr) return -810;
+    if (C == nullptr) return -814;
+    GroupedParams gp{};
+    gp.p.A = A;
+    gp.p.B = B;
+    gp.p.C = C;
+    gp.p.M = M;
+    gp.p.N = N;
+    gp.p.K = product ? K : 0;
+    gp.p.lda = lda;
+    gp.p.ldb = ldb;
+    gp.p.ldc = ldc;
+    gp.p.alpha = product ? alpha : 0.0f;
+    gp.p.beta = beta;
+    gp.offsets = offsets;
+    gp.groups = groups;
+    gp.stride = strideB;
+    const bool vec4 = aligned16(A) && aligned16(B) && lda % 4 == 0 && ldb % 4 == 0 &&
+                      strideB % 4 == 0 && K % 4 == 0 && (transB || N % 4 == 0);
+    const int bm = 64, bn = 64;
+    const GroupedFn fn = vec4 ? (transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 4>
+                                        : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 4>)
+                              : (transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 1>
+                                        : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>);
+    gp.p.tiles_n = (int)ceil_div(N, bn);
+    return launch_grouped(fn, gp, most_tiles(M, groups, bm) * gp.p.tiles_n, 256,
+                          reinterpret_cast<hipStream_t>(stream));
+}
+
+extern "C" int sgemm_grouped_outer(int M, int N, int K, int groups, const int *offsets,
+                                   float alpha, const float *A, int lda, const float *B, int ldb,
+                                   float beta, float *C, int ldc, long long strideC,
+                                   sgemm_stream_t stream)
+{
+    if (M < 0) return -901;
+    if (N < 0) return -902;
+    if (K < 0) return -903;
+    if (groups < 0) return -904;
+    if (lda < (M > 1 ? M : 1) || lda > kMaxLd) return -908;
+    if (ldb < (N > 1 ? N : 1) || ldb > kMaxLd) return -910;
+    if (ldc < (N > 1 ? N : 1) || ldc > kMaxLd) return -913;
+    if (strideC < 0) return -914;
+    if (M == 0 || N == 0 || groups == 0)
+        return 0;
+    const bool product = K > 0 && alpha != 0.0f;
+    if (!product && beta == 1.0f)
+        return 0;
+    if (offsets == nullptr) return -905;
+    if (product && A == nullptr) return -907;
+    if (product && B == nullptr) return -909;
+    if (C == nullptr) return -912;
+    GroupedParams gp{};
+    gp.p.A = A;
+    gp.p.B = B;
+    gp.p.C = C;
+    gp.p.M = M;
+    gp.p.N = N;
+    gp.p.K = K;
+    gp.p.lda = lda;
+    gp.p.ldb = ldb;
+    gp.p.ldc = ldc;
+    gp.p.alpha = product ? alpha : 0.0f;
+    gp.p.beta = beta;
+    gp.offsets = offsets;
+    gp.groups = groups;
+    gp.stride = strideC;
+    const bool vec4 = aligned16(A) && aligned16(B) && lda % 4 == 0 && ldb % 4 == 0 &&
+                      M % 4 == 0 && N % 4 == 0;
+    const int bm = 64, bn = 64;
+    const GroupedFn fn = vec4 ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 4>
+                              : sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 1>;
+    gp.p.tiles_m = (int)ceil_div(M, bm);
+    gp.p.tiles_n = (int)ceil_div(N, bn);
+    const long long per_group = (long long)gp.p.tiles_m * gp.p.tiles_n;
+    if (per_group > INT32_MAX / 256)
+        return -22;
+    return launch_grouped(fn, gp, per_group * groups, 256, reinterpret_cast<hipStream_t>(stream));
+}
+
 extern "C" const char *sgemm_status_string(int status)
 {
     switch (status) {
@@ -2952,7 +3214,9 @@ extern "C" const char *sgemm_status_string(int status)
     case -25: return "invalid dispatch override count: negative or above SGEMM_MAX_DISPATCH_OVERRIDES";
     default: break;
     }
-    if (status < 0)
-        return "invalid argument";
+    if (status < 0) {
+        const char *call = call_status_string(status);
+        return call ? call : "invalid argument";
+    }
     return hipGetErrorString(static_cast<hipError_t>(status));
 }

@@ -1,0 +1,169 @@
+"""The expert and 8-bit calls on the host: exported symbols, argument checks,
+quick returns and messages, and what the binding refuses. Nothing here launches
+a kernel, so it runs without a GPU."""
+import os
+import re
+import subprocess
+
+import pytest
+
+from conftest import ROOT
+
+FAKE = 1 << 20  # never dereferenced: every call below returns before any device work
+CALLS = {
+    "i8_quantize_rows": (100, dict(M=4, K=4, X=FAKE, x_type=0, ldx=4, Q=FAKE, ldq=4, scale=FAKE)),
+    "i8gemm": (200, dict(M=4, N=4, K=4, A=FAKE, lda=4, scaleA=FAKE, B=FAKE, ldb=4, scaleB=FAKE,
+                         bias=None, C=FAKE, c_type=0, ldc=4)),
+    "i8gemm_grouped": (300, dict(M=4, N=4, K=4, groups=2, offsets=FAKE, A=FAKE, lda=4,
+                                 scaleA=FAKE, B=FAKE, ldb=4, strideB=16, scaleB=FAKE, bias=None,
+                                 C=FAKE, c_type=0, ldc=4)),
+    "expert_sort": (400, dict(tokens=4, topk=2, experts=8, ids=FAKE, id_bytes=4, offsets=FAKE,
+                              row_of_slot=FAKE, workspace=None, workspace_bytes=0)),
+    "expert_gather": (500, dict(tokens=4, topk=2, cols=4, X=FAKE, type=0, ldx=4,
+                                row_of_slot=FAKE, Y=FAKE, ldy=4)),
+    "expert_combine": (600, dict(tokens=4, topk=2, cols=4, Y=FAKE, type=0, ldy=4,
+                                 row_of_slot=FAKE, weights=None, out=FAKE, ldo=4)),
+    "expert_combine_grad": (700, dict(tokens=4, topk=2, cols=4, dout=FAKE, type=0, ldo=4, Y=FAKE,
+                                      ldy=4, row_of_slot=FAKE, weights=FAKE, dY=FAKE, lddy=4,
+                                      dweights=FAKE)),
+    "sgemm_grouped": (800, dict(transB=0, M=4, N=4, K=4, groups=2, offsets=FAKE, alpha=1.0,
+                                A=FAKE, lda=4, B=FAKE, ldb=4, strideB=16, beta=0.0, C=FAKE,
+                                ldc=4)),
+    "sgemm_grouped_outer": (900, dict(M=4, N=4, K=4, groups=2, offsets=FAKE, alpha=1.0, A=FAKE,
+                                      lda=4, B=FAKE, ldb=4, beta=0.0, C=FAKE, ldc=4,
+                                      strideC=16)),
+}
+
+
+@pytest.fixture(scope="module")
+def pg():
+    import precision_gemm_amd as pg
+    if not os.path.exists(pg.library_path()):
+        from precision_gemm_amd import _build
+        _build.build()
+    pg._load()
+    return pg
+
+
+def call(pg, name, **over):
+    args = dict(CALLS[name][1])
+    assert set(over) <= set(args), over
+    args.update(over)
+    return getattr(pg._load(), name)(*args.values(), None)
+
+
+def position(name, arg):
+    return list(CALLS[name][1]).index(arg) + 1
+
+
+@pytest.mark.parametrize("header,prefix", [("i8gemm.h", "i8"), ("experts.h", "expert")])
+def test_headers(pg, header, prefix):
+    """The headers compile as C, and the library exports what they declare."""
+    path = os.path.join(ROOT, "include", header)
+    text = re.sub(r"/\*.*?\*/", "", open(path).read(), flags=re.S)
+    names = set(re.findall(r"^\s*(?:int|size_t)\s+(%s\w*)\s*\(" % prefix, text, re.M))
+    assert names >= {n for n in CALLS if n.startswith(prefix)}
+    for n in names:
+        assert hasattr(pg._load(), n)
+    subprocess.run(["gcc", "-x", "c", "-std=c99", "-Wall", "-Werror", "-I",
+                    os.path.join(ROOT, "include"), "-fsyntax-only", "-"],
+                   input='#include "%s"\nint main(void){return 0;}\n' % header, text=True,
+                   check=True)
+
+
+REFUSED = [
+    ("i8_quantize_rows", [("M", -1), ("K", -1), ("K", 2**31 - 1), ("X", None), ("x_type", 3),
+                          ("x_type", -1), ("ldx", 3), ("Q", None), ("ldq", 3), ("scale", None)]),
+    ("i8gemm", [("M", -1), ("N", -1), ("K", -1), ("K", 131072), ("A", None), ("lda", 3),
+                ("scaleA", None), ("B", None), ("ldb", 3), ("scaleB", None), ("C", None),
+                ("c_type", 3), ("ldc", 3)]),
+    ("i8gemm_grouped", [("M", -1), ("N", -1), ("K", -1), ("K", 131072), ("groups", -1),
+                        ("offsets", None), ("A", None), ("lda", 3), ("scaleA", None),
+                        ("B", None), ("ldb", 3), ("strideB", -1), ("scaleB", None), ("C", None),
+                        ("c_type", 4), ("ldc", 3)]),
+    ("expert_sort", [("tokens", -1), ("tokens", 2**30), ("topk", 0), ("experts", 0),
+                     ("experts", 1025), ("ids", None), ("id_bytes", 2), ("offsets", None),
+                     ("row_of_slot", None)]),
+    ("expert_gather", [("tokens", -1), ("tokens", 2**30), ("topk", 0), ("cols", -1), ("X", None),
+                       ("type", 4), ("ldx", 3), ("row_of_slot", None), ("Y", None), ("ldy", 3)]),
+    ("expert_combine", [("tokens", -1), ("tokens", 2**30), ("topk", 0), ("cols", -1), ("Y", None),
+                        ("type", 3), ("ldy", 3), ("row_of_slot", None), ("out", None),
+                        ("ldo", 3)]),
+    ("expert_combine_grad", [("tokens", -1), ("tokens", 2**30), ("topk", 0), ("cols", -1),
+                             ("dout", None), ("type", 3), ("ldo", 3), ("Y", None), ("ldy", 3),
+                             ("row_of_slot", None), ("dY", None), ("lddy", 3)]),
+    ("sgemm_grouped", [("transB", 2), ("M", -1), ("N", -1), ("K", -1), ("groups", -1),
+                       ("offsets", None), ("A", None), ("lda", 3), ("lda", 1 << 21), ("B", None),
+                       ("ldb", 3), ("ldb", 1 << 21), ("strideB", -1), ("C", None), ("ldc", 3),
+                       ("ldc", 1 << 21)]),
+    ("sgemm_grouped_outer", [("M", -1), ("N", -1), ("K", -1), ("groups", -1), ("offsets", None),
+                             ("A", None), ("lda", 3), ("lda", 1 << 21), ("B", None), ("ldb", 3),
+                             ("ldb", 1 << 21), ("C", None), ("ldc", 3), ("ldc", 1 << 21),
+                             ("strideC", -1)]),
+]
+
+
+@pytest.mark.parametrize("name,arg,value", [(n, a, v) for n, av in REFUSED for a, v in av])
+def test_argument_errors(pg, name, arg, value):
+    """Each bad argument gives minus (the call's base + its position), with a
+    message naming the call."""
+    status = call(pg, name, **{arg: value})
+    assert status == -(CALLS[name][0] + position(name, arg))
+    text = pg.sgemm_status_string(status)
+    assert text.startswith(name + ":") and str(position(name, arg)) in text
+
+
+@pytest.mark.parametrize("name,over", [
+    ("i8_quantize_rows", dict(M=0, X=None, Q=None, scale=None)),
+    ("i8gemm", dict(M=0, A=None, C=None)), ("i8gemm", dict(N=0, B=None, C=None)),
+    ("i8gemm_grouped", dict(groups=0, offsets=None)), ("i8gemm_grouped", dict(M=0, A=None)),
+    ("expert_gather", dict(tokens=0, X=None, row_of_slot=None)),
+    ("expert_gather", dict(cols=0, X=None, Y=None)),
+    ("expert_combine", dict(tokens=0)), ("expert_combine", dict(cols=0, Y=None)),
+    ("expert_combine_grad", dict(tokens=0)),
+    ("expert_combine_grad", dict(cols=0, dweights=None, dY=None)),
+    ("sgemm_grouped", dict(M=0)), ("sgemm_grouped", dict(groups=0, offsets=None)),
+    ("sgemm_grouped", dict(K=0, beta=1.0, A=None, B=None)),
+    ("sgemm_grouped", dict(alpha=0.0, beta=1.0)),
+    ("sgemm_grouped_outer", dict(N=0)), ("sgemm_grouped_outer", dict(K=0, beta=1.0, A=None)),
+])
+def test_quick_returns_launch_nothing(pg, name, over):
+    assert call(pg, name, **over) == 0
+
+
+def test_sort_workspace(pg):
+    size = pg.expert_sort_workspace_size
+    assert size(4, 2, 8) == 0  # a single run needs none
+    need = size(1 << 16, 8, 128)
+    assert 0 < need <= 256 * 129 * 4
+    big = size((1 << 28) - 1, 8, 1024)
+    assert 0 < big <= 256 * 1025 * 4
+    for bad in ((-1, 2, 8), (4, 0, 8), (4, 2, 0), (4, 2, 1025), (1 << 30, 2, 8)):
+        assert size(*bad) == 0
+    over = dict(tokens=1 << 16, topk=8, experts=128)
+    assert call(pg, "expert_sort", **over, workspace=None, workspace_bytes=need) == -408
+    assert call(pg, "expert_sort", **over, workspace=FAKE + 2, workspace_bytes=need) == -408
+    assert call(pg, "expert_sort", **over, workspace=FAKE, workspace_bytes=need - 1) == -409
+
+
+def test_oversize_grids_are_rejected(pg):
+    """More output tiles than a launch holds: -22 before any device work."""
+    n = 2**31 - 1
+    assert call(pg, "i8gemm", M=n, N=n, ldc=n) == -22
+    assert call(pg, "sgemm_grouped", M=n, N=(1 << 21) - 1, ldb=(1 << 21) - 1,
+                ldc=(1 << 21) - 1) == -22
+    assert call(pg, "sgemm_grouped_outer", groups=n, M=4096, N=4096, lda=4096, ldb=4096,
+                ldc=4096) == -22
+
+
+def test_binding_refuses_host_tensors(pg):
+    torch = pytest.importorskip("torch")
+    x, q, s = torch.zeros(4, 4), torch.zeros(4, 4, dtype=torch.int8), torch.zeros(4)
+    with pytest.raises(TypeError, match="X must be a GPU tensor"):
+        pg.i8_quantize_rows(4, 4, x, 4, q, 4, s)
+    with pytest.raises(TypeError, match="A must be a GPU tensor"):
+        pg.i8gemm(4, 4, 4, q, 4, s, q, 4, s, None, x, 4)
+    with pytest.raises(TypeError, match="ids must be a GPU tensor"):
+        pg.expert_sort(4, 1, 4, s, s, s, None)
+    with pytest.raises(TypeError, match="offsets must be a GPU tensor"):
+        pg.sgemm_grouped(0, 4, 4, 4, 1, s, 1.0, x, 4, x, 4, 16, 0.0, x, 4)
