@@ -9,7 +9,8 @@
  * contiguous in k:
  *   acc[m,n] = sum_k A[m*lda + k] * B[n*ldb + k]            (exact, 32-bit integers)
  *   C[m*ldc + n] = (float(acc) * scaleA[m]) * scaleB[n] + bias[n]
- * in fp32, rounded once to C's type. The integer sum is exact for every order
+ * in fp32 (the last product and sum with one rounding), rounded once to C's
+ * type. The integer sum is exact for every order
  * of its terms, so results do not depend on how a kernel splits K.
  *
  * Ownership, execution (asynchronous on `stream`, no host synchronisation, no

@@ -46,88 +46,96 @@ def declare(lib):
     lib.expert_sort_workspace_size.restype = sz
 
 
-class _Operands:
-    """Checks one call's tensors and hands out their addresses."""
+_INT8, _F32, _I32 = (torch.int8,), (torch.float32,), (torch.int32,)
+_ANY = _FLOATS + _INT8
+_IDS = (torch.int32, torch.int64)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
-    def __init__(self):
-        self.device = None
 
-    def at(self, name, t, dtypes, rows, cols=1, ld=None):
-        """Address of `rows` rows of `cols` elements, `ld` apart."""
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a GPU tensor")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the operands before it on {self.device}")
-        need = (rows - 1) * (cols if ld is None else ld) + cols if rows > 0 and cols > 0 else 0
+def _span(rows, cols, ld):
+    """Elements from the first to the last of `rows` rows, `ld` apart."""
+    return (rows - 1) * ld + cols if rows > 0 and cols > 0 else 0
+
+
+def _spans(groups, stride, rows, cols, ld):
+    """The same for `groups` matrices, `stride` apart."""
+    n = _span(rows, cols, ld)
+    return (groups - 1) * stride + n if groups > 0 and n > 0 else 0
+
+
+def _first(name, t):
+    """The device of a call's operands, from one of them."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    return t.get_device()
+
+
+def _at(name, t, dtypes, device, need):
+    """Address of an operand that the call takes `need` elements of."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other operands on cuda:{device}")
+    if need > t.numel() or not t.is_contiguous():
         have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
         if need > have:
             raise ValueError(f"{name} holds {have} elements from its first one on, "
                              f"the call needs {need}")
-        return t.data_ptr()
+    return t.data_ptr()
 
-    def groups(self, name, t, dtypes, groups, stride, rows, cols, ld):
-        """Address of `groups` matrices, `stride` apart."""
-        at = self.at(name, t, dtypes, rows, cols, ld)
-        if groups > 1 and rows > 0 and cols > 0:
-            need = (groups - 1) * stride + (rows - 1) * ld + cols
-            have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
-            if need > have:
-                raise ValueError(f"{name} holds {have} elements from its first one on, "
-                                 f"the call needs {need}")
-        return at
 
-    def call(self, name, stream, check, *args):
-        fn = getattr(_pg._load(), name)
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device).cuda_stream
-        elif not isinstance(stream, int):
-            stream = stream.cuda_stream
-        if torch.cuda.current_device() == self.device.index:
+def _call(fn, device, stream, check, *args):
+    if stream is None:
+        stream = _raw_stream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
             status = fn(*args, stream)
-        else:
-            with torch.cuda.device(self.device):
-                status = fn(*args, stream)
-        return _pg._check(status, check)
+    return status if status == 0 else _pg._check(status, check)
 
 
 def i8_quantize_rows(M, K, X, ldx, Q, ldq, scale, stream=None, check=True) -> int:
     """C ABI ``i8_quantize_rows``: rows of X (fp32, fp16 or bf16) to 8-bit
     integers Q with one fp32 scale a row."""
-    o = _Operands()
-    return o.call("i8_quantize_rows", stream, check, M, K, o.at("X", X, _FLOATS, M, K, ldx),
-                  _TYPES[X.dtype], ldx, o.at("Q", Q, (torch.int8,), M, K, ldq), ldq,
-                  o.at("scale", scale, (torch.float32,), M))
+    d = _first("X", X)
+    return _call(_pg._load().i8_quantize_rows, d, stream, check, M, K,
+                 _at("X", X, _FLOATS, d, _span(M, K, ldx)), _TYPES[X.dtype], ldx,
+                 _at("Q", Q, _INT8, d, _span(M, K, ldq)), ldq,
+                 _at("scale", scale, _F32, d, M))
 
 
 def i8gemm(M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, C, ldc, stream=None, check=True) -> int:
     """C ABI ``i8gemm``: C = (A B^T) * scaleA[m] * scaleB[n] + bias[n], A (M x
     K) and B (N x K) int8, bias fp32 or None, C fp32, fp16 or bf16."""
-    o = _Operands()
-    f32 = (torch.float32,)
-    return o.call("i8gemm", stream, check, M, N, K, o.at("A", A, (torch.int8,), M, K, lda), lda,
-                  o.at("scaleA", scaleA, f32, M), o.at("B", B, (torch.int8,), N, K, ldb), ldb,
-                  o.at("scaleB", scaleB, f32, N),
-                  None if bias is None else o.at("bias", bias, f32, N),
-                  o.at("C", C, _FLOATS, M, N, ldc), _TYPES[C.dtype], ldc)
+    d = _first("A", A)
+    return _call(_pg._load().i8gemm, d, stream, check, M, N, K,
+                 _at("A", A, _INT8, d, _span(M, K, lda)), lda,
+                 _at("scaleA", scaleA, _F32, d, M),
+                 _at("B", B, _INT8, d, _span(N, K, ldb)), ldb,
+                 _at("scaleB", scaleB, _F32, d, N),
+                 None if bias is None else _at("bias", bias, _F32, d, N),
+                 _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
 
 
 def i8gemm_grouped(M, N, K, groups, offsets, A, lda, scaleA, B, ldb, strideB, scaleB, bias, C,
                    ldc, stream=None, check=True) -> int:
     """C ABI ``i8gemm_grouped``: i8gemm over rows sorted by group; `offsets`
     holds groups + 1 int32, scaleB and bias groups x N."""
-    o = _Operands()
-    f32, i8 = (torch.float32,), (torch.int8,)
-    return o.call("i8gemm_grouped", stream, check, M, N, K, groups,
-                  o.at("offsets", offsets, (torch.int32,), groups + 1),
-                  o.at("A", A, i8, M, K, lda), lda, o.at("scaleA", scaleA, f32, M),
-                  o.groups("B", B, i8, groups, strideB, N if groups else 0, K, ldb), ldb, strideB,
-                  o.at("scaleB", scaleB, f32, groups, N),
-                  None if bias is None else o.at("bias", bias, f32, groups, N),
-                  o.at("C", C, _FLOATS, M, N, ldc), _TYPES[C.dtype], ldc)
+    d = _first("offsets", offsets)
+    return _call(_pg._load().i8gemm_grouped, d, stream, check, M, N, K, groups,
+                 _at("offsets", offsets, _I32, d, groups + 1),
+                 _at("A", A, _INT8, d, _span(M, K, lda)), lda,
+                 _at("scaleA", scaleA, _F32, d, M),
+                 _at("B", B, _INT8, d, _spans(groups, strideB, N, K, ldb)), ldb, strideB,
+                 _at("scaleB", scaleB, _F32, d, groups * N),
+                 None if bias is None else _at("bias", bias, _F32, d, groups * N),
+                 _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
 
 
 def expert_sort_workspace_size(tokens, topk, experts) -> int:
@@ -140,83 +148,79 @@ def expert_sort(tokens, topk, experts, ids, offsets, row_of_slot, workspace, str
     """C ABI ``expert_sort``: ids (int32 or int64, contiguous) to offsets and
     row_of_slot (int32); workspace: a GPU tensor of any type, or None where
     expert_sort_workspace_size() is 0."""
-    o = _Operands()
-    p_ids = o.at("ids", ids, (torch.int32, torch.int64), tokens * topk)
+    d = _first("ids", ids)
+    slots = tokens * topk
+    p_ids = _at("ids", ids, _IDS, d, slots)
     ws, ws_bytes = None, 0
     if workspace is not None:
-        if not isinstance(workspace, torch.Tensor) or workspace.device != o.device:
-            raise TypeError("workspace must be a GPU tensor on the operands' device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+        ws = _at("workspace", workspace, (workspace.dtype,), d, 0)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    return o.call("expert_sort", stream, check, tokens, topk, experts, p_ids, ids.element_size(),
-                  o.at("offsets", offsets, (torch.int32,), experts + 1),
-                  o.at("row_of_slot", row_of_slot, (torch.int32,), tokens * topk), ws, ws_bytes)
+    return _call(_pg._load().expert_sort, d, stream, check, tokens, topk, experts, p_ids,
+                 ids.element_size(), _at("offsets", offsets, _I32, d, experts + 1),
+                 _at("row_of_slot", row_of_slot, _I32, d, slots), ws, ws_bytes)
 
 
 def expert_gather(tokens, topk, cols, X, ldx, row_of_slot, Y, ldy, stream=None, check=True) -> int:
     """C ABI ``expert_gather``: Y[row_of_slot[t, j]] = X[t]; X and Y of one
     type, fp32, fp16, bf16 or int8."""
-    o = _Operands()
-    any_type = _FLOATS + (torch.int8,)
+    d = _first("X", X)
     slots = tokens * topk
-    return o.call("expert_gather", stream, check, tokens, topk, cols,
-                  o.at("X", X, any_type, tokens, cols, ldx), _TYPES[X.dtype], ldx,
-                  o.at("row_of_slot", row_of_slot, (torch.int32,), slots),
-                  o.at("Y", Y, (X.dtype,), slots, cols, ldy), ldy)
+    return _call(_pg._load().expert_gather, d, stream, check, tokens, topk, cols,
+                 _at("X", X, _ANY, d, _span(tokens, cols, ldx)), _TYPES[X.dtype], ldx,
+                 _at("row_of_slot", row_of_slot, _I32, d, slots),
+                 _at("Y", Y, (X.dtype,), d, _span(slots, cols, ldy)), ldy)
 
 
 def expert_combine(tokens, topk, cols, Y, ldy, row_of_slot, weights, out, ldo, stream=None,
                    check=True) -> int:
     """C ABI ``expert_combine``: out[t] = sum_j weights[t, j] Y[row_of_slot[t,
     j]]; weights fp32, or None for 1 (the gradient of expert_gather)."""
-    o = _Operands()
+    d = _first("Y", Y)
     slots = tokens * topk
-    return o.call("expert_combine", stream, check, tokens, topk, cols,
-                  o.at("Y", Y, _FLOATS, slots, cols, ldy), _TYPES[Y.dtype], ldy,
-                  o.at("row_of_slot", row_of_slot, (torch.int32,), slots),
-                  None if weights is None else o.at("weights", weights, (torch.float32,), slots),
-                  o.at("out", out, (Y.dtype,), tokens, cols, ldo), ldo)
+    return _call(_pg._load().expert_combine, d, stream, check, tokens, topk, cols,
+                 _at("Y", Y, _FLOATS, d, _span(slots, cols, ldy)), _TYPES[Y.dtype], ldy,
+                 _at("row_of_slot", row_of_slot, _I32, d, slots),
+                 None if weights is None else _at("weights", weights, _F32, d, slots),
+                 _at("out", out, (Y.dtype,), d, _span(tokens, cols, ldo)), ldo)
 
 
 def expert_combine_grad(tokens, topk, cols, dout, ldo, Y, ldy, row_of_slot, weights, dY, lddy,
                         dweights, stream=None, check=True) -> int:
     """C ABI ``expert_combine_grad``: dY and dweights (fp32, or None: then Y
     may be None too) from dout."""
-    o = _Operands()
+    d = _first("dout", dout)
     slots = tokens * topk
-    f32 = (torch.float32,)
-    return o.call("expert_combine_grad", stream, check, tokens, topk, cols,
-                  o.at("dout", dout, _FLOATS, tokens, cols, ldo), _TYPES[dout.dtype], ldo,
-                  None if Y is None else o.at("Y", Y, (dout.dtype,), slots, cols, ldy), ldy,
-                  o.at("row_of_slot", row_of_slot, (torch.int32,), slots),
-                  None if weights is None else o.at("weights", weights, f32, slots),
-                  o.at("dY", dY, (dout.dtype,), slots, cols, lddy), lddy,
-                  None if dweights is None else o.at("dweights", dweights, f32, slots))
+    return _call(_pg._load().expert_combine_grad, d, stream, check, tokens, topk, cols,
+                 _at("dout", dout, _FLOATS, d, _span(tokens, cols, ldo)), _TYPES[dout.dtype], ldo,
+                 None if Y is None else _at("Y", Y, (dout.dtype,), d, _span(slots, cols, ldy)),
+                 ldy, _at("row_of_slot", row_of_slot, _I32, d, slots),
+                 None if weights is None else _at("weights", weights, _F32, d, slots),
+                 _at("dY", dY, (dout.dtype,), d, _span(slots, cols, lddy)), lddy,
+                 None if dweights is None else _at("dweights", dweights, _F32, d, slots))
 
 
 def sgemm_grouped(transB, M, N, K, groups, offsets, alpha, A, lda, B, ldb, strideB, beta, C, ldc,
                   stream=None, check=True) -> int:
     """C ABI ``sgemm_grouped``: C[m] = alpha A[m] op(B_g) + beta C[m] for the
     rows offsets[g] <= m < offsets[g + 1] of every group."""
-    o = _Operands()
-    f32 = (torch.float32,)
+    d = _first("offsets", offsets)
     rows, cols = (N, K) if transB else (K, N)
-    return o.call("sgemm_grouped", stream, check, int(transB), M, N, K, groups,
-                  o.at("offsets", offsets, (torch.int32,), groups + 1), float(alpha),
-                  o.at("A", A, f32, M, K, lda), lda,
-                  o.groups("B", B, f32, groups, strideB, rows if groups else 0, cols, ldb), ldb,
-                  strideB, float(beta), o.at("C", C, f32, M, N, ldc), ldc)
+    return _call(_pg._load().sgemm_grouped, d, stream, check, int(transB), M, N, K, groups,
+                 _at("offsets", offsets, _I32, d, groups + 1), alpha,
+                 _at("A", A, _F32, d, _span(M, K, lda)), lda,
+                 _at("B", B, _F32, d, _spans(groups, strideB, rows, cols, ldb)), ldb, strideB,
+                 beta, _at("C", C, _F32, d, _span(M, N, ldc)), ldc)
 
 
 def sgemm_grouped_outer(M, N, K, groups, offsets, alpha, A, lda, B, ldb, beta, C, ldc, strideC,
                         stream=None, check=True) -> int:
     """C ABI ``sgemm_grouped_outer``: C_g = alpha A_g^T B_g + beta C_g over the
     rows offsets[g] <= k < offsets[g + 1] of A (K x M) and B (K x N)."""
-    o = _Operands()
-    f32 = (torch.float32,)
-    return o.call("sgemm_grouped_outer", stream, check, M, N, K, groups,
-                  o.at("offsets", offsets, (torch.int32,), groups + 1), float(alpha),
-                  o.at("A", A, f32, K, M, lda), lda, o.at("B", B, f32, K, N, ldb), ldb,
-                  float(beta), o.groups("C", C, f32, groups, strideC, M if groups else 0, N, ldc),
-                  ldc, strideC)
+    d = _first("offsets", offsets)
+    return _call(_pg._load().sgemm_grouped_outer, d, stream, check, M, N, K, groups,
+                 _at("offsets", offsets, _I32, d, groups + 1), alpha,
+                 _at("A", A, _F32, d, _span(K, M, lda)), lda,
+                 _at("B", B, _F32, d, _span(K, N, ldb)), ldb, beta,
+                 _at("C", C, _F32, d, _spans(groups, strideC, M, N, ldc)), ldc, strideC)

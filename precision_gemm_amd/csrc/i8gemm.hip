@@ -5,6 +5,7 @@
 
 #include "i8gemm.h"
 
+#include <atomic>
 #include <type_traits>
 
 namespace {
@@ -204,8 +205,8 @@ struct I8Params {
     int M, N, K;
     int lda, ldb, ldc;
     int type;
-    int groups;  // 0: one product
-    int tiles_n; // grid: row tiles x tiles_n
+    int groups;           // 0: one product
+    int tiles_m, tiles_n; // the grid
 };
 
 // Where a workgroup stands: its group's operands and its rows [m0, M) of
@@ -252,6 +253,52 @@ __device__ __forceinline__ void store_c(const I8Params &p, long long at, float v
         static_cast<_Float16 *>(p.C)[at] = (_Float16)v;
     else
         static_cast<__bf16 *>(p.C)[at] = (__bf16)v;
+}
+
+// One output: every kernel rounds in this order.
+__device__ __forceinline__ float scaled(float acc, float sa, float sb, float bias)
+{
+    return __builtin_fmaf(acc * sa, sb, bias);
+}
+
+// Four neighbouring outputs from column n of the row at `row` on.
+__device__ __forceinline__ void store_c4(const I8Params &p, long long row, int n, f32x4 x)
+{
+    if (n + 4 > p.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.N)
+                store_c(p, row + n + i, x[i]);
+        return;
+    }
+    if (p.type == SGEMM_F32) {
+        store16(static_cast<float *>(p.C) + row + n, __builtin_bit_cast(i32x4, x));
+        return;
+    }
+    i32x2_any h;
+    if (p.type == SGEMM_F16) {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        h = __builtin_bit_cast(i32x2, h4{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2],
+                                         (_Float16)x[3]});
+    } else {
+        typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+        h = __builtin_bit_cast(i32x2, b4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]});
+    }
+    *reinterpret_cast<i32x2_any *>(static_cast<short *>(p.C) + row + n) = h;
+}
+
+// Workgroup -> (row tile, column tile): consecutive workgroups go round the 8
+// XCDs, each of which gets a contiguous run of the tiles, ordered in bands of 8
+// row tiles so that the rows and weights in use stay in its L2.
+__device__ __forceinline__ void i8_order(const I8Params &p, int &slot, int &tn)
+{
+    const int num = gridDim.x, pid = blockIdx.x;
+    const int xcd = pid & 7, local = pid >> 3, q = num >> 3, r = num & 7;
+    const int at = xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
+    const int band = 8 * p.tiles_n, first = at / band * 8;
+    const int rows = min(p.tiles_m - first, 8);
+    slot = first + at % band % rows;
+    tn = at % band / rows;
 }
 
 // 16 bytes of a row from its byte k on, zeros from byte K on; nothing outside
@@ -326,21 +373,369 @@ __global__ void __launch_bounds__(256) i8_tile_kernel(I8Params p)
     for (int v = 0; v < 16; ++v) {
         const int m = t.m0 + wm + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
         if (m < t.M)
-            store_c(p, (t.row0 + m) * p.ldc + n, (float)acc[v] * t.sA[m] * sb + bias);
+            store_c(p, (t.row0 + m) * p.ldc + n, scaled((float)acc[v], t.sA[m], sb, bias));
     }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the weights' bytes bound the call, so they go from memory straight
+// into the matrix instructions' registers, once, and no LDS stage stands
+// between. A workgroup owns 16 * NT channels and up to 16 * MT rows; its WAVES
+// waves take every WAVES-th block of 64 * U of k, so all of a short K is in
+// flight at once, and their exact integer sums are added in LDS.
+// v_mfma_i32_16x16x64_i8: lane l supplies 16 bytes of row l % 16 from k =
+// 16 (l / 16) on; register v of lane l holds row 4 (l / 16) + v, column l % 16.
+// Rows behind the last repeat it and are not stored.
+// ---------------------------------------------------------------------------
+template <int MT, int NT, int WAVES, int U>
+__global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
+{
+    constexpr int BM = 16 * MT, BN = 16 * NT;
+    __shared__ int sums[WAVES][BM][BN];
+    I8Tile t;
+    if (!i8_tile_of<BM, BN>(p, blockIdx.x / p.tiles_n, blockIdx.x % p.tiles_n, t))
+        return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, kq = 16 * (lane >> 4);
+    const signed char *ra[MT], *rb[NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        ra[i] = t.A + (long long)min(t.m0 + 16 * i + r, t.M - 1) * p.lda + kq;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        rb[j] = t.B + (long long)min(t.n0 + 16 * j + r, p.N - 1) * p.ldb + kq;
+
+    i32x4 acc[MT][NT] = {};
+    auto products = [&](const i32x4 (&fa)[MT], const i32x4 (&fb)[NT]) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    };
+    int k = wave * 64 * U;
+    for (; k + 64 * U <= p.K; k += WAVES * 64 * U) {
+        i32x4 fb[U][NT], fa[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                fb[u][j] = load16(rb[j] + k + 64 * u);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                fa[u][i] = load16(ra[i] + k + 64 * u);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            products(fa[u], fb[u]);
+    }
+    // The block that K ends in (one wave's).
+    for (int q = k; q < p.K && q < k + 64 * U; q += 64) {
+        i32x4 fb[NT], fa[MT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            fb[j] = row_chunk(rb[j] + q, 0, p.K - q - kq);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            fa[i] = row_chunk(ra[i] + q, 0, p.K - q - kq);
+        products(fa, fb);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                sums[wave][16 * i + 4 * (lane >> 4) + v][16 * j + r] = acc[i][j][v];
+    __syncthreads();
+    const int rows = min(BM, t.M - t.m0);
+    for (int e = tid; e < rows * BN; e += 64 * WAVES) {
+        const int m = e / BN, n = t.n0 + e % BN;
+        if (n >= p.N)
+            continue;
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            sum += sums[w][m][e % BN];
+        store_c(p, (t.row0 + t.m0 + m) * p.ldc + n,
+                scaled((float)sum, t.sA[t.m0 + m], t.sB[n], t.bias ? t.bias[n] : 0.0f));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Large products: BM x BN of C by WAVES_M x WAVES_N waves, K in steps of 64
+// bytes that go straight from memory to LDS (buffer_load_dwordx4 ... lds)
+// through a ring of STAGES stages, STAGES - 1 steps ahead. Lane l of a load
+// fills the l-th 16 bytes of a 1 KiB block, 16 rows of 64 bytes; which chunk of
+// its row it fetches carries the XOR that makes the reads conflict-free (as in
+// i8_tile_kernel). A lane whose chunk lies behind K fetches zeros from a
+// 2^31 byte offset, outside the buffer. Loads are issued for steps past the
+// last too (of zeros), so that the number in flight is the same at every wait.
+// Needs 16-byte-aligned rows, K a multiple of 16 and leading dimensions below
+// 2^22 (32-bit offsets within a tile).
+// ---------------------------------------------------------------------------
+constexpr uint32_t kOutside = 0x80000000u;
+constexpr int kMaxTileLd = 1 << 22;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const signed char *base, long long bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<signed char *>(base), (short)0,
+                                             (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff),
+                                             0x00020000);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    // vmcnt <= N, lgkmcnt and expcnt as they are
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+__device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *lds)
+{
+    constexpr int BK = 64, NW = WAVES_M * WAVES_N;
+    constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 32, TN = WN / 32;
+    constexpr int STAGE = (BM + BN) * BK;
+    constexpr int NA = BM * BK / 1024 / NW, NB = BN * BK / 1024 / NW; // blocks a wave loads
+    static_assert(NA >= 1 && NB >= 1 && (STAGES - 2) * (NA + NB) <= 63, "loads in flight");
+
+    I8Tile t;
+    int slot, tn;
+    i8_order(p, slot, tn);
+    if (!i8_tile_of<BM, BN>(p, slot, tn, t))
+        return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = (wave % WAVES_M) * WM, wn = (wave / WAVES_M) * WN;
+
+    const __amdgpu_buffer_rsrc_t rsA = rows_rsrc(
+        t.A + (long long)t.m0 * p.lda, (long long)(t.M - t.m0 - 1) * p.lda + p.K);
+    const __amdgpu_buffer_rsrc_t rsB = rows_rsrc(
+        t.B + (long long)t.n0 * p.ldb, (long long)(p.N - t.n0 - 1) * p.ldb + p.K);
+    const int chunk = 16 * ((lane & 3) ^ (lane >> 4));
+    uint32_t offA[NA], offB[NB];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+        offA[i] = (uint32_t)(min(16 * (wave + NW * i) + (lane >> 2), t.M - t.m0 - 1) * p.lda + chunk);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+        offB[i] = (uint32_t)(min(16 * (wave + NW * i) + (lane >> 2), p.N - t.n0 - 1) * p.ldb + chunk);
+
+    typedef __attribute__((address_space(3))) void lds_void;
+    auto issue = [&](int step, int stage) {
+        const int k = step * BK;
+        const uint32_t off = k + chunk < p.K ? 0u : kOutside;
+        signed char *to = lds + stage * STAGE;
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsA, (lds_void *)(to + 1024 * (wave + NW * i)), 16, offA[i] | off, k, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsB, (lds_void *)(to + BM * BK + 1024 * (wave + NW * i)), 16, offB[i] | off, k, 0, 0);
+    };
+
+    // This lane's 16 bytes of k-half q (32 bytes of the step) in row 32 i + l %
+    // 32 of the wave's part; 32 rows on is a fixed distance.
+    const int o = lane & 31;
+    int at[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        at[q] = o * BK + 16 * ((2 * q + (lane >> 5)) ^ ((o >> 2) & 3));
+
+    i32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            acc[i][j] = i32x16{};
+    i32x4 fa[2][TM], fb[2][TN];
+    auto read = [&](const signed char *stage, int q) {
+        const signed char *a = stage + wm * BK + at[q], *b = stage + (BM + wn) * BK + at[q];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa[q][i] = *reinterpret_cast<const i32x4 *>(a + 32 * BK * i);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            fb[q][j] = *reinterpret_cast<const i32x4 *>(b + 32 * BK * j);
+    };
+    auto products = [&](int q) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[q][i], fb[q][j], acc[i][j], 0,
+                                                                  0, 0);
+    };
+    auto meet = [&]() { // every wave's loads of the next step are in LDS
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        wait_loads<(STAGES - 2) * (NA + NB)>();
+        __builtin_amdgcn_s_waitcnt(0xc07f); // lgkmcnt(0): this step's reads are done
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    const int steps = (p.K + BK - 1) / BK;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        issue(s, s);
+    meet();
+    read(lds, 0);
+    int cur = 0, ahead = STAGES - 1; // stages of this step and of step + STAGES - 1
+    for (int s = 0; s < steps; ++s) {
+        read(lds + cur * STAGE, 1);
+        issue(s + STAGES - 1, ahead);
+        products(0);
+        // The reads of the second half, products with the loads between them.
+        __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+#pragma unroll
+        for (int i = 0; i < NA + NB; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+        cur = cur + 1 == STAGES ? 0 : cur + 1;
+        ahead = ahead + 1 == STAGES ? 0 : ahead + 1;
+        meet();
+        // (After the last step this reads zeros that are not used.)
+        read(lds + cur * STAGE, 0);
+        products(1);
+        __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_loads<0>();
+    __syncthreads();
+
+    // Each wave turns its part over in an LDS patch of its own, 32 rows at a
+    // time, so that a row's outputs leave as 16-byte (fp32) or 8-byte pieces.
+    constexpr int ROW = WN + 4; // floats; the pad keeps a row's lanes off the next row's banks
+    static_assert(NW * 32 * ROW * 4 <= STAGES * STAGE, "the patches must fit in the stages");
+    float *patch = reinterpret_cast<float *>(lds) + wave * 32 * ROW;
+    constexpr int PER = WN / 4; // lanes a row, four columns each
+    const int c = 4 * (lane % PER), n = t.n0 + wn + c;
+    float sb[4], bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sb[e] = t.sB[min(n + e, p.N - 1)];
+        bias[e] = t.bias ? t.bias[min(n + e, p.N - 1)] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int mb = t.m0 + wm + 32 * i;
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                patch[(8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * ROW + 32 * j + o] =
+                    (float)acc[i][j][v];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 64 / PER) {
+            const int row = r0 + lane / PER;
+            f32x4 x = *reinterpret_cast<const f32x4 *>(patch + row * ROW + c);
+            if (mb + row < t.M) {
+                const float sa = t.sA[mb + row];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = scaled(x[e], sa, sb[e], bias[e]);
+                store_c4(p, (t.row0 + mb + row) * p.ldc, n, x);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+__global__ void
+__attribute__((amdgpu_flat_work_group_size(64 * WAVES_M * WAVES_N, 64 * WAVES_M * WAVES_N)))
+i8_large_kernel(I8Params p)
+{
+    __shared__ __attribute__((aligned(1024))) signed char lds[STAGES * (BM + BN) * 64];
+    i8_large_tile<BM, BN, WAVES_M, WAVES_N, STAGES>(p, lds);
+}
+
+int current_cus(int *out)
+{
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess)
+        return (int)e;
+    const bool cached = dev >= 0 && dev < 64;
+    int cus = cached ? cache[dev].load(std::memory_order_relaxed) : 0;
+    if (cus == 0) {
+        e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+        if (e != hipSuccess)
+            return (int)e;
+        if (cached)
+            cache[dev].store(cus, std::memory_order_relaxed);
+    }
+    *out = cus;
+    return 0;
+}
+
+typedef void (*I8Fn)(I8Params);
+
+struct I8Variant {
+    I8Fn fn;
+    int bm, bn, threads;
+};
+
+// The tile of a call. `rows` is the row count of one product, or for groups
+// their average.
+I8Variant choose_i8(const I8Params &p, int cus)
+{
+    const bool aligned = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.lda % 16 == 0 &&
+                         p.ldb % 16 == 0 && p.strideB % 16 == 0 && p.K % 16 == 0 &&
+                         p.lda < kMaxTileLd && p.ldb < kMaxTileLd && p.K > 0;
+    const long long rows = p.groups ? ceil_div_ll(p.M, p.groups) : p.M;
+    if (rows <= 16) {
+        if (p.K >= 1536)
+            return {i8_stream_kernel<1, 1, 8, 4>, 16, 16, 512};
+        return {i8_stream_kernel<1, 1, 4, 2>, 16, 16, 256};
+    }
+    if (rows <= 32)
+        return {i8_stream_kernel<2, 2, 8, 2>, 32, 32, 512};
+    if (aligned) {
+        const long long t256 = (p.groups ? most_tiles(p.M, p.groups, 256) : ceil_div_ll(p.M, 256)) *
+                               ceil_div_ll(p.N, 256);
+        if (t256 >= cus)
+            return {i8_large_kernel<256, 256, 2, 2, 4>, 256, 256, 256};
+        return {i8_large_kernel<128, 128, 2, 2, 4>, 128, 128, 256};
+    }
+    return {i8_tile_kernel, 64, 64, 256};
 }
 
 int launch_i8(I8Params p, hipStream_t s)
 {
-    const long long tiles_m =
-        p.groups ? most_tiles(p.M, p.groups, 64) : ceil_div_ll(p.M, 64);
-    const long long tiles_n = ceil_div_ll(p.N, 64);
-    if (tiles_m * tiles_n > (1 << 23))
+    int cus = 0;
+    I8Variant v{i8_tile_kernel, 64, 64, 256};
+    // (Every kernel's tiles are at least 16 x 16: more of those than a launch
+    // can hold are refused before the device is asked.)
+    if ((p.groups ? most_tiles(p.M, p.groups, 256) : ceil_div_ll(p.M, 256)) *
+            ceil_div_ll(p.N, 256) > (1 << 22))
         return -22;
+    const int st = current_cus(&cus);
+    if (st != 0)
+        return st;
+    v = choose_i8(p, cus);
+    const long long tiles_m =
+        p.groups ? most_tiles(p.M, p.groups, v.bm) : ceil_div_ll(p.M, v.bm);
+    const long long tiles_n = ceil_div_ll(p.N, v.bn);
+    if (tiles_m * tiles_n * v.threads > 0xffffffffLL)
+        return -22;
+    p.tiles_m = (int)tiles_m;
     p.tiles_n = (int)tiles_n;
     void *args[] = {&p};
-    return (int)hipLaunchKernel((const void *)i8_tile_kernel, dim3((unsigned)(tiles_m * tiles_n)),
-                                dim3(256), args, 0, s);
+    return (int)hipLaunchKernel((const void *)v.fn, dim3((unsigned)(tiles_m * tiles_n)),
+                                dim3(v.threads), args, 0, s);
 }
 
 bool c_type_ok(int type) { return type == SGEMM_F32 || type == SGEMM_F16 || type == SGEMM_BF16; }
@@ -388,7 +783,7 @@ extern "C" int i8gemm(int M, int N, int K, const signed char *A, int lda, const 
     if (K > 0 && B == nullptr) return -207;
     if (scaleB == nullptr) return -209;
     if (C == nullptr) return -211;
-    I8Params p{A, B, scaleA, scaleB, bias, C, nullptr, 0, M, N, K, lda, ldb, ldc, c_type, 0, 0};
+    I8Params p{A, B, scaleA, scaleB, bias, C, nullptr, 0, M, N, K, lda, ldb, ldc, c_type, 0, 0, 0};
     return launch_i8(p, static_cast<hipStream_t>(stream));
 }
 
@@ -417,6 +812,6 @@ extern "C" int i8gemm_grouped(int M, int N, int K, int groups, const int *offset
     if (scaleB == nullptr) return -312;
     if (C == nullptr) return -314;
     I8Params p{A,   B,   scaleA, scaleB, bias,   C,      offsets, strideB, M,
-               N,   K,   lda,    ldb,    ldc,    c_type, groups,  0};
+               N,   K,   lda,    ldb,    ldc,    c_type, groups, 0, 0};
     return launch_i8(p, static_cast<hipStream_t>(stream));
 }

@@ -9,8 +9,10 @@
 
 namespace {
 
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // Vectors at any address: one global_load_dwordx4 or store each (the hardware
 // takes unaligned addresses, at a lower rate).
