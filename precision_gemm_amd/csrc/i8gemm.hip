@@ -207,6 +207,7 @@ struct I8Params {
     int type;
     int groups;           // 0: one product
     int tiles_m, tiles_n; // the grid
+    int band;             // row tiles of a band of the grid's order
 };
 
 // Where a workgroup stands: its group's operands and its rows [m0, M) of
@@ -219,9 +220,9 @@ struct I8Tile {
 };
 
 template <int BM, int BN>
-__device__ __forceinline__ bool i8_tile_of(const I8Params &p, int slot, int tn, I8Tile &t)
+__device__ __forceinline__ bool i8_tile_of(const I8Params &p, I8Tile &t)
 {
-    t.n0 = tn * BN;
+    int tm = 0, tn = 0;
     t.A = p.A;
     t.B = p.B;
     t.sA = p.sA;
@@ -229,30 +230,43 @@ __device__ __forceinline__ bool i8_tile_of(const I8Params &p, int slot, int tn, 
     t.bias = p.bias;
     t.row0 = 0;
     t.M = p.M;
-    t.m0 = slot * BM;
-    if (p.groups == 0)
-        return true;
-    int g, lo;
-    if (!find_tile(p.offsets, p.groups, p.M, BM, slot, g, lo, t.M, t.m0))
-        return false;
-    t.row0 = lo;
-    t.A += (long long)lo * p.lda;
-    t.sA += lo;
-    t.B += g * p.strideB;
-    t.sB += (long long)g * p.N;
-    if (t.bias)
-        t.bias += (long long)g * p.N;
+    if (p.groups == 0) {
+        if (!tile_order(p.tiles_m, p.tiles_n, p.band, tm, tn))
+            return false;
+        t.m0 = tm * BM;
+    } else {
+        auto pick = [&](int tiles) {
+            return tile_order(tiles, p.tiles_n, p.band, tm, tn) ? tm : -1;
+        };
+        int g, lo;
+        if (!find_tile(p.offsets, p.groups, p.M, BM, pick, g, lo, t.M, t.m0))
+            return false;
+        t.row0 = lo;
+        t.A += (long long)lo * p.lda;
+        t.sA += lo;
+        t.B += g * p.strideB;
+        t.sB += (long long)g * p.N;
+        if (t.bias)
+            t.bias += (long long)g * p.N;
+    }
+    t.n0 = tn * BN;
     return true;
+}
+
+template <typename F>
+__device__ __forceinline__ void with_type(int type, F f)
+{
+    if (type == SGEMM_F32)
+        f(float{});
+    else if (type == SGEMM_F16)
+        f(_Float16{});
+    else
+        f(__bf16{});
 }
 
 __device__ __forceinline__ void store_c(const I8Params &p, long long at, float v)
 {
-    if (p.type == SGEMM_F32)
-        static_cast<float *>(p.C)[at] = v;
-    else if (p.type == SGEMM_F16)
-        static_cast<_Float16 *>(p.C)[at] = (_Float16)v;
-    else
-        static_cast<__bf16 *>(p.C)[at] = (__bf16)v;
+    with_type(p.type, [&](auto t) { static_cast<decltype(t) *>(p.C)[at] = (decltype(t))v; });
 }
 
 // One output: every kernel rounds in this order.
@@ -261,44 +275,16 @@ __device__ __forceinline__ float scaled(float acc, float sa, float sb, float bia
     return __builtin_fmaf(acc * sa, sb, bias);
 }
 
-// Four neighbouring outputs from column n of the row at `row` on.
-__device__ __forceinline__ void store_c4(const I8Params &p, long long row, int n, f32x4 x)
+// Four neighbouring outputs at any address.
+template <typename T>
+__device__ __forceinline__ void store4(T *c, f32x4 x)
 {
-    if (n + 4 > p.N) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < p.N)
-                store_c(p, row + n + i, x[i]);
-        return;
-    }
-    if (p.type == SGEMM_F32) {
-        store16(static_cast<float *>(p.C) + row + n, __builtin_bit_cast(i32x4, x));
-        return;
-    }
-    i32x2_any h;
-    if (p.type == SGEMM_F16) {
-        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-        h = __builtin_bit_cast(i32x2, h4{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2],
-                                         (_Float16)x[3]});
-    } else {
-        typedef __bf16 b4 __attribute__((ext_vector_type(4)));
-        h = __builtin_bit_cast(i32x2, b4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]});
-    }
-    *reinterpret_cast<i32x2_any *>(static_cast<short *>(p.C) + row + n) = h;
-}
-
-// Workgroup -> (row tile, column tile): consecutive workgroups go round the 8
-// XCDs, each of which gets a contiguous run of the tiles, ordered in bands of 8
-// row tiles so that the rows and weights in use stay in its L2.
-__device__ __forceinline__ void i8_order(const I8Params &p, int &slot, int &tn)
-{
-    const int num = gridDim.x, pid = blockIdx.x;
-    const int xcd = pid & 7, local = pid >> 3, q = num >> 3, r = num & 7;
-    const int at = xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
-    const int band = 8 * p.tiles_n, first = at / band * 8;
-    const int rows = min(p.tiles_m - first, 8);
-    slot = first + at % band % rows;
-    tn = at % band / rows;
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    const t4 h = {(T)x[0], (T)x[1], (T)x[2], (T)x[3]};
+    if constexpr (sizeof(T) == 4)
+        store16(c, __builtin_bit_cast(i32x4, h));
+    else
+        *reinterpret_cast<i32x2_any *>(c) = __builtin_bit_cast(i32x2, h);
 }
 
 // 16 bytes of a row from its byte k on, zeros from byte K on; nothing outside
@@ -328,7 +314,7 @@ __global__ void __launch_bounds__(256) i8_tile_kernel(I8Params p)
     constexpr int BM = 64, BN = 64, BK = 64;
     __shared__ __attribute__((aligned(16))) signed char lds[2][2][64 * BK];
     I8Tile t;
-    if (!i8_tile_of<BM, BN>(p, blockIdx.x / p.tiles_n, blockIdx.x % p.tiles_n, t))
+    if (!i8_tile_of<BM, BN>(p, t))
         return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int r = tid >> 2, c = tid & 3;
@@ -393,7 +379,7 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
     constexpr int BM = 16 * MT, BN = 16 * NT;
     __shared__ int sums[WAVES][BM][BN];
     I8Tile t;
-    if (!i8_tile_of<BM, BN>(p, blockIdx.x / p.tiles_n, blockIdx.x % p.tiles_n, t))
+    if (!i8_tile_of<BM, BN>(p, t))
         return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -503,13 +489,12 @@ __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *ld
     static_assert(NA >= 1 && NB >= 1 && (STAGES - 2) * (NA + NB) <= 63, "loads in flight");
 
     I8Tile t;
-    int slot, tn;
-    i8_order(p, slot, tn);
-    if (!i8_tile_of<BM, BN>(p, slot, tn, t))
+    if (!i8_tile_of<BM, BN>(p, t))
         return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = (wave % WAVES_M) * WM, wn = (wave / WAVES_M) * WN;
+    // (Waves that share a SIMD, four apart, lie above one another in M.)
+    const int wm = (wave / WAVES_N) * WM, wn = (wave % WAVES_N) * WN;
 
     const __amdgpu_buffer_rsrc_t rsA = rows_rsrc(
         t.A + (long long)t.m0 * p.lda, (long long)(t.M - t.m0 - 1) * p.lda + p.K);
@@ -588,27 +573,37 @@ __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *ld
     meet();
     read(lds, 0);
     int cur = 0, ahead = STAGES - 1; // stages of this step and of step + STAGES - 1
-    for (int s = 0; s < steps; ++s) {
-        read(lds + cur * STAGE, 1);
-        issue(s + STAGES - 1, ahead);
-        products(0);
-        // The reads of the second half, products with the loads between them.
-        __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+    if (t.m0 + wm < t.M) {
+        for (int s = 0; s < steps; ++s) {
+            read(lds + cur * STAGE, 1);
+            issue(s + STAGES - 1, ahead);
+            products(0);
+            // The reads of the second half, products with the loads between them.
+            __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
 #pragma unroll
-        for (int i = 0; i < NA + NB; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            for (int i = 0; i < NA + NB; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
+            ahead = ahead + 1 == STAGES ? 0 : ahead + 1;
+            meet();
+            // (After the last step this reads zeros that are not used.)
+            read(lds + cur * STAGE, 0);
+            products(1);
+            __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
-        cur = cur + 1 == STAGES ? 0 : cur + 1;
-        ahead = ahead + 1 == STAGES ? 0 : ahead + 1;
-        meet();
-        // (After the last step this reads zeros that are not used.)
-        read(lds + cur * STAGE, 0);
-        products(1);
-        __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
-        __builtin_amdgcn_sched_barrier(0);
+    } else {
+        // A wave whose rows all lie behind the group's last only loads, and
+        // leaves the matrix unit to the other wave of its SIMD.
+        for (int s = 0; s < steps; ++s) {
+            issue(s + STAGES - 1, ahead);
+            ahead = ahead + 1 == STAGES ? 0 : ahead + 1;
+            meet();
+        }
     }
     wait_loads<0>();
     __syncthreads();
@@ -626,30 +621,54 @@ __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *ld
         sb[e] = t.sB[min(n + e, p.N - 1)];
         bias[e] = t.bias ? t.bias[min(n + e, p.N - 1)] : 0.0f;
     }
+    const int r = lane / PER;
+    // EDGE: the tile reaches past M or N.
+    auto turn_over = [&](auto type, auto edge) {
+        typedef decltype(type) T;
+        constexpr bool EDGE = decltype(edge)::value;
+        T *out = static_cast<T *>(p.C) + (t.row0 + t.m0 + wm + r) * p.ldc + n;
+        const float *sa = t.sA + t.m0 + wm + r;
+        const int left = t.M - (t.m0 + wm + r); // rows from this lane's first one on
+        const long long step = (long long)(64 / PER) * p.ldc;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int mb = t.m0 + wm + 32 * i;
+        for (int i = 0; i < TM; ++i) {
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
+            for (int v = 0; v < 16; ++v)
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-                patch[(8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * ROW + 32 * j + o] =
-                    (float)acc[i][j][v];
-        __builtin_amdgcn_wave_barrier();
+                for (int j = 0; j < TN; ++j)
+                    patch[(8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * ROW + 32 * j + o] =
+                        (float)acc[i][j][v];
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += 64 / PER) {
-            const int row = r0 + lane / PER;
-            f32x4 x = *reinterpret_cast<const f32x4 *>(patch + row * ROW + c);
-            if (mb + row < t.M) {
-                const float sa = t.sA[mb + row];
+            for (int r0 = 0; r0 < 32; r0 += 64 / PER) {
+                const int m = 32 * i + r0;
+                f32x4 x = *reinterpret_cast<const f32x4 *>(patch + (r0 + r) * ROW + c);
+                if (!EDGE || m < left) {
+                    const float s = sa[m];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[e] = scaled(x[e], sa, sb[e], bias[e]);
-                store_c4(p, (t.row0 + mb + row) * p.ldc, n, x);
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = scaled(x[e], s, sb[e], bias[e]);
+                    if (!EDGE || n + 4 <= p.N) {
+                        store4(out, x);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n + e < p.N)
+                                out[e] = (T)x[e];
+                    }
+                }
+                out += step;
             }
+            __builtin_amdgcn_wave_barrier();
         }
-        __builtin_amdgcn_wave_barrier();
-    }
+    };
+    const bool whole = t.m0 + BM <= t.M && t.n0 + BN <= p.N;
+    with_type(p.type, [&](auto type) {
+        if (whole)
+            turn_over(type, std::false_type{});
+        else
+            turn_over(type, std::true_type{});
+    });
 }
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
@@ -707,7 +726,7 @@ I8Variant choose_i8(const I8Params &p, int cus)
         const long long t256 = (p.groups ? most_tiles(p.M, p.groups, 256) : ceil_div_ll(p.M, 256)) *
                                ceil_div_ll(p.N, 256);
         if (t256 >= cus)
-            return {i8_large_kernel<256, 256, 2, 2, 4>, 256, 256, 256};
+            return {i8_large_kernel<256, 256, 2, 4, 4>, 256, 256, 512};
         return {i8_large_kernel<128, 128, 2, 2, 4>, 128, 128, 256};
     }
     return {i8_tile_kernel, 64, 64, 256};
@@ -733,6 +752,7 @@ int launch_i8(I8Params p, hipStream_t s)
         return -22;
     p.tiles_m = (int)tiles_m;
     p.tiles_n = (int)tiles_n;
+    p.band = p.groups ? group_band(p.M, p.groups, v.bm) : 8;
     void *args[] = {&p};
     return (int)hipLaunchKernel((const void *)v.fn, dim3((unsigned)(tiles_m * tiles_n)),
                                 dim3(v.threads), args, 0, s);
@@ -783,7 +803,7 @@ extern "C" int i8gemm(int M, int N, int K, const signed char *A, int lda, const 
     if (K > 0 && B == nullptr) return -207;
     if (scaleB == nullptr) return -209;
     if (C == nullptr) return -211;
-    I8Params p{A, B, scaleA, scaleB, bias, C, nullptr, 0, M, N, K, lda, ldb, ldc, c_type, 0, 0, 0};
+    I8Params p{A, B, scaleA, scaleB, bias, C, nullptr, 0, M, N, K, lda, ldb, ldc, c_type, 0, 0, 0, 0};
     return launch_i8(p, static_cast<hipStream_t>(stream));
 }
 
@@ -812,6 +832,6 @@ extern "C" int i8gemm_grouped(int M, int N, int K, int groups, const int *offset
     if (scaleB == nullptr) return -312;
     if (C == nullptr) return -314;
     I8Params p{A,   B,   scaleA, scaleB, bias,   C,      offsets, strideB, M,
-               N,   K,   lda,    ldb,    ldc,    c_type, groups, 0, 0};
+               N,   K,   lda,    ldb,    ldc,    c_type, groups, 0, 0, 0};
     return launch_i8(p, static_cast<hipStream_t>(stream));
 }

@@ -43,13 +43,15 @@ __device__ __forceinline__ void group_rows(const int *offsets, int g, int rows, 
     hi = min(max(offsets[g + 1], lo), rows);
 }
 
-// Row tile `slot` of a grouped product: tiles of `bm` rows are counted group
-// by group. Every lane of the wave returns the same group, its first row and
-// row count, and the tile's first row within the group; false if the groups
-// have fewer tiles. A wave's lanes take groups/64 consecutive groups each and
-// add up their tiles with a scan over the lanes.
+// A tile of a grouped product. Row tiles of `bm` rows are counted group by
+// group; `pick` is told how many there are and returns the number of the one
+// wanted, or -1 for none. Every lane of the wave returns the same group, its
+// first row and row count, and the tile's first row within the group; false if
+// there is no such tile. A wave's lanes take groups/64 consecutive groups each
+// and add up their tiles with a scan over the lanes.
+template <typename Pick>
 __device__ __forceinline__ bool find_tile(const int *offsets, int groups, int rows, int bm,
-                                          int slot, int &g_out, int &lo_out, int &n_out,
+                                          Pick pick, int &g_out, int &lo_out, int &n_out,
                                           int &m_out)
 {
     const int lane = __lane_id();
@@ -62,11 +64,13 @@ __device__ __forceinline__ bool find_tile(const int *offsets, int groups, int ro
         tiles += (hi - lo + bm - 1) / bm;
     }
     int upto = tiles; // tiles of lanes 0..lane
+#pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int v = __shfl_up(upto, d);
         if (lane >= d)
             upto += v;
     }
+    const int slot = pick(__builtin_amdgcn_readlane(upto, 63));
     const int before = upto - tiles;
     const bool mine = slot >= before && slot < upto;
     const unsigned long long who = __ballot(mine);
@@ -90,10 +94,28 @@ __device__ __forceinline__ bool find_tile(const int *offsets, int groups, int ro
         }
     }
     const int src = __builtin_ctzll(who);
-    g_out = __builtin_amdgcn_readfirstlane(__shfl(g_at, src));
-    lo_out = __builtin_amdgcn_readfirstlane(__shfl(lo_at, src));
-    n_out = __builtin_amdgcn_readfirstlane(__shfl(n_at, src));
-    m_out = __builtin_amdgcn_readfirstlane(__shfl(m_at, src));
+    g_out = __builtin_amdgcn_readlane(g_at, src);
+    lo_out = __builtin_amdgcn_readlane(lo_at, src);
+    n_out = __builtin_amdgcn_readlane(n_at, src);
+    m_out = __builtin_amdgcn_readlane(m_at, src);
+    return true;
+}
+
+// Workgroup -> (row tile, column tile) of `tiles_m` x `tiles_n`, or false for
+// one too many: consecutive workgroups go round the 8 XCDs, each of which gets
+// a contiguous run of the tiles, ordered in bands of `band` row tiles so that
+// the rows and weights in use stay in its L2.
+__device__ __forceinline__ bool tile_order(int tiles_m, int tiles_n, int band, int &tm, int &tn)
+{
+    const int num = tiles_m * tiles_n, pid = blockIdx.x;
+    const int xcd = pid & 7, local = pid >> 3, q = num >> 3, r = num & 7;
+    if (local >= q + (xcd < r))
+        return false;
+    const int at = xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
+    const int each = band * tiles_n, first = at / each * band;
+    const int rows = min(tiles_m - first, band);
+    tm = first + at % each % rows;
+    tn = at % each / rows;
     return true;
 }
 
@@ -101,6 +123,13 @@ __device__ __forceinline__ bool find_tile(const int *offsets, int groups, int ro
 inline long long most_tiles(int rows, int groups, int bm)
 {
     return rows / bm + (groups < rows ? groups : rows);
+}
+
+// Row tiles of a band of the tile order: as many as a group has on average.
+inline int group_band(long long rows, long long groups, int bm)
+{
+    const long long each = (rows + groups * (bm / 2)) / (groups * bm);
+    return each < 1 ? 1 : each > 8 ? 8 : (int)each;
 }
 
 inline long long ceil_div_ll(long long a, long long b) { return (a + b - 1) / b; }

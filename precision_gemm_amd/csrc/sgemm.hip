@@ -2942,6 +2942,7 @@ struct GroupedParams {
     const int *offsets;
     int groups;
     long long stride;    // of B (rows product) or C (outer product)
+    int band;            // row tiles of a band of the tile order
 };
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, bool A_KC, bool B_KC, int VEC>
@@ -3036,10 +3037,13 @@ sgemm_grouped_kernel(GroupedParams gp)
 {
     __shared__ __attribute__((aligned(16))) float lds[2 * (BM + BN) * kBK];
     Params p = gp.p;
-    int g, lo, m0;
-    const int slot = blockIdx.x / p.tiles_n, n0 = blockIdx.x % p.tiles_n * BN;
-    if (!find_tile(gp.offsets, gp.groups, p.M, BM, slot, g, lo, p.M, m0))
+    int g, lo, m0, tm = 0, tn = 0;
+    auto pick = [&](int tiles) {
+        return tile_order(tiles, p.tiles_n, gp.band, tm, tn) ? tm : -1;
+    };
+    if (!find_tile(gp.offsets, gp.groups, p.M, BM, pick, g, lo, p.M, m0))
         return;
+    const int n0 = tn * BN;
     grouped_tile<BM, BN, WAVES_M, WAVES_N, true, B_KC, VEC>(
         p, p.A + (long long)lo * p.lda, p.B + g * gp.stride, p.C + (long long)lo * p.ldc, p.K, m0,
         n0, lds);
@@ -3131,6 +3135,7 @@ extern "C" int sgemm_grouped(int transB, int M, int N, int K, int groups, const 
                               : (transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 1>
                                         : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>);
     gp.p.tiles_n = (int)ceil_div(N, bn);
+    gp.band = group_band(M, groups, bm);
     return launch_grouped(fn, gp, most_tiles(M, groups, bm) * gp.p.tiles_n, 256,
                           reinterpret_cast<hipStream_t>(stream));
 }
