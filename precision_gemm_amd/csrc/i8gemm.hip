@@ -451,16 +451,24 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
 }
 
 // ---------------------------------------------------------------------------
-// Large products: BM x BN of C by WAVES_M x WAVES_N waves, K in steps of 64
+// Larger products: BM x BN of C by WAVES_M x WAVES_N waves, K in steps of 128
 // bytes that go straight from memory to LDS (buffer_load_dwordx4 ... lds)
-// through a ring of STAGES stages, STAGES - 1 steps ahead. Lane l of a load
-// fills the l-th 16 bytes of a 1 KiB block, 16 rows of 64 bytes; which chunk of
-// its row it fetches carries the XOR that makes the reads conflict-free (as in
-// i8_tile_kernel). A lane whose chunk lies behind K fetches zeros from a
-// 2^31 byte offset, outside the buffer. Loads are issued for steps past the
-// last too (of zeros), so that the number in flight is the same at every wait.
-// Needs 16-byte-aligned rows, K a multiple of 16 and leading dimensions below
-// 2^22 (32-bit offsets within a tile).
+// through a ring of STAGES stages. Lane l of a load fills the l-th 16 bytes of
+// a 1 KiB block, 8 rows of 128 bytes: whole cache lines, so half the requests
+// of 64-byte steps (which measured the same on cached operands, and 577 us
+// against 474 on 4096 x 4096 x 32768). LDS rows are 128 bytes, two of them one
+// sweep of the 64 banks: the 16-byte chunk index is XORed with row / 2, on the
+// memory side, for conflict-free reads. A lane whose chunk lies behind K
+// fetches zeros from a 2^31 byte offset, outside the buffer. Loads are issued
+// for steps past the last too (of zeros), so that the number in flight is the
+// same at every wait. Needs 16-byte-aligned rows, K a multiple of 16 and
+// leading dimensions below 2^22 (32-bit offsets within a tile).
+//
+// What bounds the 256 x 256 tile: power. On 8192^3 it runs at 2.33 POP/s where
+// the library product makes 2.11; without its loads the loop takes 17 % less,
+// without its LDS reads 18 %, on operands of zeros 30 %, and the clock stands
+// at 1.8 GHz. Eight waves of 128 x 64 each beat four of 128 x 128 (4001 x 8192
+// x 4096: 132 us against 144), whose outputs leave one wave a SIMD idle.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kOutside = 0x80000000u;
 constexpr int kMaxTileLd = 1 << 22;
@@ -482,11 +490,11 @@ __device__ __forceinline__ void wait_loads()
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
 __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *lds)
 {
-    constexpr int BK = 64, NW = WAVES_M * WAVES_N;
+    constexpr int BK = 128, KH = BK / 32, NW = WAVES_M * WAVES_N;
     constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 32, TN = WN / 32;
     constexpr int STAGE = (BM + BN) * BK;
     constexpr int NA = BM * BK / 1024 / NW, NB = BN * BK / 1024 / NW; // blocks a wave loads
-    static_assert(NA >= 1 && NB >= 1 && (STAGES - 2) * (NA + NB) <= 63, "loads in flight");
+    static_assert(NA >= 1 && NB >= 1 && STAGES >= 2 && (STAGES - 1) * (NA + NB) <= 63, "loads in flight");
 
     I8Tile t;
     if (!i8_tile_of<BM, BN>(p, t))
@@ -500,14 +508,14 @@ __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *ld
         t.A + (long long)t.m0 * p.lda, (long long)(t.M - t.m0 - 1) * p.lda + p.K);
     const __amdgpu_buffer_rsrc_t rsB = rows_rsrc(
         t.B + (long long)t.n0 * p.ldb, (long long)(p.N - t.n0 - 1) * p.ldb + p.K);
-    const int chunk = 16 * ((lane & 3) ^ (lane >> 4));
+    const int chunk = 16 * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
     uint32_t offA[NA], offB[NB];
 #pragma unroll
     for (int i = 0; i < NA; ++i)
-        offA[i] = (uint32_t)(min(16 * (wave + NW * i) + (lane >> 2), t.M - t.m0 - 1) * p.lda + chunk);
+        offA[i] = (uint32_t)(min(8 * (wave + NW * i) + (lane >> 3), t.M - t.m0 - 1) * p.lda + chunk);
 #pragma unroll
     for (int i = 0; i < NB; ++i)
-        offB[i] = (uint32_t)(min(16 * (wave + NW * i) + (lane >> 2), p.N - t.n0 - 1) * p.ldb + chunk);
+        offB[i] = (uint32_t)(min(8 * (wave + NW * i) + (lane >> 3), p.N - t.n0 - 1) * p.ldb + chunk);
 
     typedef __attribute__((address_space(3))) void lds_void;
     auto issue = [&](int step, int stage) {
@@ -524,13 +532,13 @@ __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *ld
                 rsB, (lds_void *)(to + BM * BK + 1024 * (wave + NW * i)), 16, offB[i] | off, k, 0, 0);
     };
 
-    // This lane's 16 bytes of k-half q (32 bytes of the step) in row 32 i + l %
+    // This lane's 16 bytes of k-group q (32 bytes of the step) in row 32 i + l %
     // 32 of the wave's part; 32 rows on is a fixed distance.
     const int o = lane & 31;
-    int at[2];
+    int at[KH];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-        at[q] = o * BK + 16 * ((2 * q + (lane >> 5)) ^ ((o >> 2) & 3));
+    for (int q = 0; q < KH; ++q)
+        at[q] = o * BK + 16 * ((2 * q + (lane >> 5)) ^ ((o >> 1) & 7));
 
     i32x16 acc[TM][TN];
 #pragma unroll
@@ -538,61 +546,70 @@ __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *ld
 #pragma unroll
         for (int j = 0; j < TN; ++j)
             acc[i][j] = i32x16{};
-    i32x4 fa[2][TM], fb[2][TN];
+    i32x4 fa[2][TM], fb[2][TN]; // of k-groups by parity
     auto read = [&](const signed char *stage, int q) {
         const signed char *a = stage + wm * BK + at[q], *b = stage + (BM + wn) * BK + at[q];
 #pragma unroll
         for (int i = 0; i < TM; ++i)
-            fa[q][i] = *reinterpret_cast<const i32x4 *>(a + 32 * BK * i);
+            fa[q & 1][i] = *reinterpret_cast<const i32x4 *>(a + 32 * BK * i);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-            fb[q][j] = *reinterpret_cast<const i32x4 *>(b + 32 * BK * j);
+            fb[q & 1][j] = *reinterpret_cast<const i32x4 *>(b + 32 * BK * j);
     };
     auto products = [&](int q) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[q][i], fb[q][j], acc[i][j], 0,
-                                                                  0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[q & 1][i], fb[q & 1][j],
+                                                                  acc[i][j], 0, 0, 0);
     };
-    auto meet = [&]() { // every wave's loads of the next step are in LDS
+    auto meet = [&]() { // every wave's loads of the next step are in LDS, its reads of this one done
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
         wait_loads<(STAGES - 2) * (NA + NB)>();
-        __builtin_amdgcn_s_waitcnt(0xc07f); // lgkmcnt(0): this step's reads are done
+        __builtin_amdgcn_s_waitcnt(0xc07f); // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
 
+    // Step s in stage s % STAGES: each k-group is read under the products of
+    // the one before. Once the last one is read, all meet: the loads of step
+    // s + 1 have to be there, those of step s + STAGES take the stage just
+    // read, and the first k-group of s + 1 is read under the last products of
+    // s. (After the last step this reads zeros.)
     const int steps = (p.K + BK - 1) / BK;
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s)
         issue(s, s);
     meet();
-    read(lds, 0);
-    int cur = 0, ahead = STAGES - 1; // stages of this step and of step + STAGES - 1
+    issue(STAGES - 1, STAGES - 1);
+    int cur = 0;
     if (t.m0 + wm < t.M) {
+        read(lds, 0);
         for (int s = 0; s < steps; ++s) {
-            read(lds + cur * STAGE, 1);
-            issue(s + STAGES - 1, ahead);
-            products(0);
-            // The reads of the second half, products with the loads between them.
+            const signed char *stage = lds + cur * STAGE;
+#pragma unroll
+            for (int q = 0; q + 1 < KH; ++q) {
+                read(stage, q + 1);
+                products(q);
+                __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+            }
+            meet();
+            const int next = cur + 1 == STAGES ? 0 : cur + 1;
+            read(lds + next * STAGE, 0);
+            issue(s + STAGES, cur);
+            cur = next;
+            products(KH - 1);
+            constexpr int GAP = TM * TN / (NA + NB) > 0 ? TM * TN / (NA + NB) : 1;
             __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
 #pragma unroll
             for (int i = 0; i < NA + NB; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, GAP, 0);
                 __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
-            cur = cur + 1 == STAGES ? 0 : cur + 1;
-            ahead = ahead + 1 == STAGES ? 0 : ahead + 1;
-            meet();
-            // (After the last step this reads zeros that are not used.)
-            read(lds + cur * STAGE, 0);
-            products(1);
-            __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
             __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -600,9 +617,9 @@ __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *ld
         // A wave whose rows all lie behind the group's last only loads, and
         // leaves the matrix unit to the other wave of its SIMD.
         for (int s = 0; s < steps; ++s) {
-            issue(s + STAGES - 1, ahead);
-            ahead = ahead + 1 == STAGES ? 0 : ahead + 1;
             meet();
+            issue(s + STAGES, cur);
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
         }
     }
     wait_loads<0>();
@@ -676,7 +693,7 @@ __global__ void
 __attribute__((amdgpu_flat_work_group_size(64 * WAVES_M * WAVES_N, 64 * WAVES_M * WAVES_N)))
 i8_large_kernel(I8Params p)
 {
-    __shared__ __attribute__((aligned(1024))) signed char lds[STAGES * (BM + BN) * 64];
+    __shared__ __attribute__((aligned(1024))) signed char lds[STAGES * (BM + BN) * 128];
     i8_large_tile<BM, BN, WAVES_M, WAVES_N, STAGES>(p, lds);
 }
 
@@ -707,48 +724,108 @@ struct I8Variant {
     int bm, bn, threads;
 };
 
-// The tile of a call. `rows` is the row count of one product, or for groups
-// their average.
+// The tiles that load straight into LDS, with what they cost on 256 CUs
+// (measured, us): `step` for 128 bytes of K of one tile a CU, `fixed` for the
+// launch, the first loads and the outputs. `one_round`: only where every CU
+// gets at most one tile, as its four stages leave room for few workgroups.
+struct I8Large {
+    I8Variant v;
+    float step, fixed;
+    bool one_round;
+};
+const I8Large kLarge[] = {
+    {{i8_large_kernel<32, 64, 1, 2, 4>, 32, 64, 128}, 0.22f, 4.0f, false},
+    {{i8_large_kernel<64, 64, 2, 2, 4>, 64, 64, 256}, 0.28f, 4.0f, true},
+    {{i8_large_kernel<64, 64, 2, 2, 3>, 64, 64, 256}, 0.33f, 4.0f, false},
+    {{i8_large_kernel<64, 128, 2, 2, 3>, 64, 128, 256}, 0.45f, 4.5f, false},
+    {{i8_large_kernel<128, 128, 2, 4, 4>, 128, 128, 512}, 0.70f, 5.0f, false},
+    {{i8_large_kernel<128, 256, 2, 4, 3>, 128, 256, 512}, 1.10f, 7.0f, false},
+    {{i8_large_kernel<256, 256, 2, 4, 2>, 256, 256, 512}, 1.85f, 10.0f, false},
+};
+
+// The kernel of a call. Times below are graph replays over weights that no
+// cache holds.
 I8Variant choose_i8(const I8Params &p, int cus)
 {
-    const bool aligned = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.lda % 16 == 0 &&
-                         p.ldb % 16 == 0 && p.strideB % 16 == 0 && p.K % 16 == 0 &&
-                         p.lda < kMaxTileLd && p.ldb < kMaxTileLd && p.K > 0;
-    const long long rows = p.groups ? ceil_div_ll(p.M, p.groups) : p.M;
-    if (rows <= 16) {
-        if (p.K >= 1536)
-            return {i8_stream_kernel<1, 1, 8, 4>, 16, 16, 512};
-        return {i8_stream_kernel<1, 1, 4, 2>, 16, 16, 256};
+    const bool direct = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.lda % 16 == 0 &&
+                        p.ldb % 16 == 0 && p.strideB % 16 == 0 && p.K % 16 == 0 &&
+                        p.lda < kMaxTileLd && p.ldb < kMaxTileLd && p.K > 0;
+    const long long n16 = ceil_div_ll(p.N, 16);
+    if (p.groups) {
+        // Up to 8 rows a group on average: the weights stream (256 rows over
+        // 64 groups, 2048 x 2048: 48.5 us against 51.5 with the 32 x 64 tile;
+        // 512 over 128, 4096 x 1024: 96 against 102; with 16 rows a group 76
+        // against 58).
+        if (p.M <= 8LL * p.groups || (!direct && p.M <= 16LL * p.groups))
+            return {i8_stream_kernel<1, 2, 4, 2>, 16, 32, 256};
+    } else if (p.M <= 16) {
+        // One row tile: 16 channels a workgroup, K over 8 waves, or 16 for a
+        // token or a few over a deep K (1 x 4096 x 16384: 14.7 us against
+        // 16.5; with 16 rows 18.9 against 17.6). With many workgroups, 32
+        // channels for as many rows as make A's bytes count (16 x 16384 x 4096:
+        // 17.9 us against 19.1; one row 17.0 against 17.1, 28672 channels 26.8
+        // against 23.7).
+        if (p.M <= 4)
+            return p.K >= 4096 && n16 <= 2LL * cus
+                       ? I8Variant{i8_stream_kernel<1, 1, 16, 2>, 16, 16, 1024}
+                       : I8Variant{i8_stream_kernel<1, 1, 8, 2>, 16, 16, 512};
+        if (n16 >= 4LL * cus)
+            return {i8_stream_kernel<1, 2, 4, 2>, 16, 32, 256};
+        return {i8_stream_kernel<1, 1, 8, 2>, 16, 16, 512};
+    } else {
+        // Row tiles of 32 as long as every CU gets one workgroup at most: 16,
+        // 32 or 64 channels (64 x 1024 x 4096: 7.9 us, the 32 x 64 tile 10.0;
+        // 64 x 4096 x 4096: 10.9 and 11.7; 32 x 16384 x 4096: 20.7 and 28 with
+        // the 64 x 64 tile; 128 x 4096 x 4096, two a CU: 17.8 and 11.8).
+        const long long m32 = ceil_div_ll(p.M, 32);
+        if (m32 * n16 <= cus)
+            return {i8_stream_kernel<2, 1, 8, 2>, 32, 16, 512};
+        if (m32 * ceil_div_ll(p.N, 32) <= cus)
+            return {i8_stream_kernel<2, 2, 8, 2>, 32, 32, 512};
+        if (m32 * ceil_div_ll(p.N, 64) <= cus && p.M <= 32)
+            return {i8_stream_kernel<2, 4, 4, 2>, 32, 64, 256};
     }
-    if (rows <= 32)
-        return {i8_stream_kernel<2, 2, 8, 2>, 32, 32, 512};
-    if (aligned) {
-        const long long t256 = (p.groups ? most_tiles(p.M, p.groups, 256) : ceil_div_ll(p.M, 256)) *
-                               ceil_div_ll(p.N, 256);
-        if (t256 >= cus)
-            return {i8_large_kernel<256, 256, 2, 4, 4>, 256, 256, 512};
-        return {i8_large_kernel<128, 128, 2, 2, 4>, 128, 128, 256};
+    if (!direct)
+        return {i8_tile_kernel, 64, 64, 256};
+    const I8Large *best = nullptr;
+    float least = 0.0f;
+    for (const I8Large &l : kLarge) {
+        // Row tiles: of groups, every one's own and half a tile more, since
+        // only the device knows their rows.
+        double rows = (double)ceil_div_ll(p.M, l.v.bm);
+        if (p.groups) {
+            const double each = (double)p.M / p.groups / l.v.bm + 0.5;
+            rows = (p.groups < p.M ? p.groups : p.M) * (each > 1.0 ? each : 1.0);
+        }
+        const double tiles = rows * (double)ceil_div_ll(p.N, l.v.bn);
+        if (l.one_round && tiles > cus)
+            continue;
+        const float rounds = (float)ceil_div_ll((long long)(tiles + 0.999), cus);
+        const float cost = l.fixed + rounds * (float)ceil_div_ll(p.K, 128) * l.step;
+        if (best == nullptr || cost < least) {
+            best = &l;
+            least = cost;
+        }
     }
-    return {i8_tile_kernel, 64, 64, 256};
+    return best->v;
 }
 
 int launch_i8(I8Params p, hipStream_t s)
 {
-    int cus = 0;
-    I8Variant v{i8_tile_kernel, 64, 64, 256};
-    // (Every kernel's tiles are at least 16 x 16: more of those than a launch
-    // can hold are refused before the device is asked.)
+    // (Every tile is at most 256 x 256: more of those than a launch can hold
+    // are refused before the device is asked.)
     if ((p.groups ? most_tiles(p.M, p.groups, 256) : ceil_div_ll(p.M, 256)) *
             ceil_div_ll(p.N, 256) > (1 << 22))
         return -22;
+    int cus = 0;
     const int st = current_cus(&cus);
     if (st != 0)
         return st;
-    v = choose_i8(p, cus);
+    const I8Variant v = choose_i8(p, cus);
     const long long tiles_m =
         p.groups ? most_tiles(p.M, p.groups, v.bm) : ceil_div_ll(p.M, v.bm);
     const long long tiles_n = ceil_div_ll(p.N, v.bn);
-    if (tiles_m * tiles_n * v.threads > 0xffffffffLL)
+    if (tiles_m * tiles_n * v.threads > 0xffffffffLL || tiles_m * tiles_n > INT32_MAX)
         return -22;
     p.tiles_m = (int)tiles_m;
     p.tiles_n = (int)tiles_n;

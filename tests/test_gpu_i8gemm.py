@@ -412,3 +412,53 @@ def test_other_stream_and_graph(env):
         work(*eager)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(eager, captured)), rep
+
+
+# --- large products: every tile of the dispatch, against 64-bit products on the GPU -------------
+
+
+def large_case(env, M, N, K, dtype, counts=None, first=0, extra=0, bias=True, ldc_pad=0):
+    torch, pg = env
+    log(f"[i8gemm large] {M}x{N}x{K} {dtype} counts={counts}")
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    dt, G = getattr(torch, dtype), 1 if counts is None else len(counts)
+    i8 = lambda *s: torch.randint(-128, 128, s, generator=g, device="cuda",  # noqa: E731
+                                  dtype=torch.int8)
+    A, B = i8(M, K), i8(G, N, K)
+    sA = torch.rand(M, generator=g, device="cuda") / 64
+    sB = torch.rand(G, N, generator=g, device="cuda") / 64
+    bs = torch.randn(G, N, generator=g, device="cuda") if bias else None
+    ldc = N + ldc_pad
+    C = torch.full((M, ldc), 7.0, dtype=dt, device="cuda")
+    if counts is None:
+        pg.i8gemm(M, N, K, A, K, sA, B, K, sB, bs, C, ldc)
+        ends = [0, M]
+    else:
+        ends = [int(e) for e in np.concatenate([[0], np.cumsum(counts)]) + first]
+        off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+        pg.i8gemm_grouped(M, N, K, G, off, A, K, sA, B, K, N * K, sB, bs, C, ldc)
+    for e in range(G):
+        lo, hi = ends[e], ends[e + 1]
+        p = (A[lo:hi].double() @ B[e].double().t().contiguous()) * sA[lo:hi, None].double() * \
+            sB[e].double()
+        b = bs[e].double().expand_as(p) if bias else torch.zeros_like(p)
+        err = (C[lo:hi, :N].double() - p - b).abs()
+        assert (err <= tolerance(torch, dt, p, b)).all(), (e, err.max().item())
+    assert (C[:, N:] == 7).all() and (C[:ends[0]] == 7).all() and (C[ends[-1]:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [
+    (200, 2048, 1024), (250, 4093, 272), (5000, 512, 512), (500, 4096, 2048), (1001, 4090, 2064),
+    (2000, 4095, 2032), (4000, 4090, 2064), (4001, 8192, 144), (700, 16384, 1008),
+    (33, 16384, 528), (16, 16400, 272), (3, 5000, 4112), (1, 4100, 4096), (64, 4096, 1040)])
+def test_product_large(env, M, N, K, dtype):
+    large_case(env, M, N, K, dtype, bias=M % 2 == 0, ldc_pad=M % 3)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("counts,N,K", [
+    ([1990, 0, 2010], 3800, 2064), ([300] * 16, 2048, 528), ([129, 7, 0, 255, 256, 257, 1] * 4, 2050, 1040),
+    ([16] * 50 + [0] * 14, 2048, 512), ([2, 9, 0, 31, 1] * 20, 1030, 272), ([1] * 300, 520, 144)])
+def test_grouped_large(env, counts, N, K, dtype):
+    large_case(env, sum(counts) + 9, N, K, dtype, counts=counts, first=4, bias=len(counts) % 2 == 0)
