@@ -28,6 +28,7 @@ _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
 
 def declare(lib):
     """Argument types of the library's calls."""
+    global _lib
     i, f, p, ll, sz = (ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong,
                        ctypes.c_size_t)
     lib.i8_quantize_rows.argtypes = [i, i, p, i, i, p, i, p, p]
@@ -44,6 +45,7 @@ def declare(lib):
                  "expert_combine", "expert_combine_grad", "sgemm_grouped", "sgemm_grouped_outer"):
         getattr(lib, name).restype = i
     lib.expert_sort_workspace_size.restype = sz
+    _lib = lib
 
 
 _INT8, _F32, _I32 = (torch.int8,), (torch.float32,), (torch.int32,)
@@ -51,6 +53,7 @@ _ANY = _FLOATS + _INT8
 _IDS = (torch.int32, torch.int64)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_lib = None  # the loaded library, set by declare()
 
 
 def _span(rows, cols, ld):
@@ -65,7 +68,9 @@ def _spans(groups, stride, rows, cols, ld):
 
 
 def _first(name, t):
-    """The device of a call's operands, from one of them."""
+    """The device of a call's operands, from one of them, with the library loaded."""
+    if _lib is None:
+        _pg._load()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor")
     return t.get_device()
@@ -73,17 +78,23 @@ def _first(name, t):
 
 def _at(name, t, dtypes, device, need):
     """Address of an operand that the call takes `need` elements of."""
+    try:
+        if t.get_device() == device and t.dtype in dtypes and need <= t.numel() and \
+                t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    # not the plain case: a view, or a mistake
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, the call's other operands on cuda:{device}")
-    if need > t.numel() or not t.is_contiguous():
-        have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
-        if need > have:
-            raise ValueError(f"{name} holds {have} elements from its first one on, "
-                             f"the call needs {need}")
+    have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if need > have:
+        raise ValueError(f"{name} holds {have} elements from its first one on, "
+                         f"the call needs {need}")
     return t.data_ptr()
 
 
@@ -92,7 +103,7 @@ def _call(fn, device, stream, check, *args):
         stream = _raw_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -104,7 +115,7 @@ def i8_quantize_rows(M, K, X, ldx, Q, ldq, scale, stream=None, check=True) -> in
     """C ABI ``i8_quantize_rows``: rows of X (fp32, fp16 or bf16) to 8-bit
     integers Q with one fp32 scale a row."""
     d = _first("X", X)
-    return _call(_pg._load().i8_quantize_rows, d, stream, check, M, K,
+    return _call(_lib.i8_quantize_rows, d, stream, check, M, K,
                  _at("X", X, _FLOATS, d, _span(M, K, ldx)), _TYPES[X.dtype], ldx,
                  _at("Q", Q, _INT8, d, _span(M, K, ldq)), ldq,
                  _at("scale", scale, _F32, d, M))
@@ -114,7 +125,7 @@ def i8gemm(M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, C, ldc, stream=None, c
     """C ABI ``i8gemm``: C = (A B^T) * scaleA[m] * scaleB[n] + bias[n], A (M x
     K) and B (N x K) int8, bias fp32 or None, C fp32, fp16 or bf16."""
     d = _first("A", A)
-    return _call(_pg._load().i8gemm, d, stream, check, M, N, K,
+    return _call(_lib.i8gemm, d, stream, check, M, N, K,
                  _at("A", A, _INT8, d, _span(M, K, lda)), lda,
                  _at("scaleA", scaleA, _F32, d, M),
                  _at("B", B, _INT8, d, _span(N, K, ldb)), ldb,
@@ -128,7 +139,7 @@ def i8gemm_grouped(M, N, K, groups, offsets, A, lda, scaleA, B, ldb, strideB, sc
     """C ABI ``i8gemm_grouped``: i8gemm over rows sorted by group; `offsets`
     holds groups + 1 int32, scaleB and bias groups x N."""
     d = _first("offsets", offsets)
-    return _call(_pg._load().i8gemm_grouped, d, stream, check, M, N, K, groups,
+    return _call(_lib.i8gemm_grouped, d, stream, check, M, N, K, groups,
                  _at("offsets", offsets, _I32, d, groups + 1),
                  _at("A", A, _INT8, d, _span(M, K, lda)), lda,
                  _at("scaleA", scaleA, _F32, d, M),
@@ -157,7 +168,7 @@ def expert_sort(tokens, topk, experts, ids, offsets, row_of_slot, workspace, str
         ws = _at("workspace", workspace, (workspace.dtype,), d, 0)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    return _call(_pg._load().expert_sort, d, stream, check, tokens, topk, experts, p_ids,
+    return _call(_lib.expert_sort, d, stream, check, tokens, topk, experts, p_ids,
                  ids.element_size(), _at("offsets", offsets, _I32, d, experts + 1),
                  _at("row_of_slot", row_of_slot, _I32, d, slots), ws, ws_bytes)
 
@@ -167,7 +178,7 @@ def expert_gather(tokens, topk, cols, X, ldx, row_of_slot, Y, ldy, stream=None, 
     type, fp32, fp16, bf16 or int8."""
     d = _first("X", X)
     slots = tokens * topk
-    return _call(_pg._load().expert_gather, d, stream, check, tokens, topk, cols,
+    return _call(_lib.expert_gather, d, stream, check, tokens, topk, cols,
                  _at("X", X, _ANY, d, _span(tokens, cols, ldx)), _TYPES[X.dtype], ldx,
                  _at("row_of_slot", row_of_slot, _I32, d, slots),
                  _at("Y", Y, (X.dtype,), d, _span(slots, cols, ldy)), ldy)
@@ -179,7 +190,7 @@ def expert_combine(tokens, topk, cols, Y, ldy, row_of_slot, weights, out, ldo, s
     j]]; weights fp32, or None for 1 (the gradient of expert_gather)."""
     d = _first("Y", Y)
     slots = tokens * topk
-    return _call(_pg._load().expert_combine, d, stream, check, tokens, topk, cols,
+    return _call(_lib.expert_combine, d, stream, check, tokens, topk, cols,
                  _at("Y", Y, _FLOATS, d, _span(slots, cols, ldy)), _TYPES[Y.dtype], ldy,
                  _at("row_of_slot", row_of_slot, _I32, d, slots),
                  None if weights is None else _at("weights", weights, _F32, d, slots),
@@ -192,7 +203,7 @@ def expert_combine_grad(tokens, topk, cols, dout, ldo, Y, ldy, row_of_slot, weig
     may be None too) from dout."""
     d = _first("dout", dout)
     slots = tokens * topk
-    return _call(_pg._load().expert_combine_grad, d, stream, check, tokens, topk, cols,
+    return _call(_lib.expert_combine_grad, d, stream, check, tokens, topk, cols,
                  _at("dout", dout, _FLOATS, d, _span(tokens, cols, ldo)), _TYPES[dout.dtype], ldo,
                  None if Y is None else _at("Y", Y, (dout.dtype,), d, _span(slots, cols, ldy)),
                  ldy, _at("row_of_slot", row_of_slot, _I32, d, slots),
@@ -207,7 +218,7 @@ def sgemm_grouped(transB, M, N, K, groups, offsets, alpha, A, lda, B, ldb, strid
     rows offsets[g] <= m < offsets[g + 1] of every group."""
     d = _first("offsets", offsets)
     rows, cols = (N, K) if transB else (K, N)
-    return _call(_pg._load().sgemm_grouped, d, stream, check, int(transB), M, N, K, groups,
+    return _call(_lib.sgemm_grouped, d, stream, check, int(transB), M, N, K, groups,
                  _at("offsets", offsets, _I32, d, groups + 1), alpha,
                  _at("A", A, _F32, d, _span(M, K, lda)), lda,
                  _at("B", B, _F32, d, _spans(groups, strideB, rows, cols, ldb)), ldb, strideB,
@@ -219,7 +230,7 @@ def sgemm_grouped_outer(M, N, K, groups, offsets, alpha, A, lda, B, ldb, beta, C
     """C ABI ``sgemm_grouped_outer``: C_g = alpha A_g^T B_g + beta C_g over the
     rows offsets[g] <= k < offsets[g + 1] of A (K x M) and B (K x N)."""
     d = _first("offsets", offsets)
-    return _call(_pg._load().sgemm_grouped_outer, d, stream, check, M, N, K, groups,
+    return _call(_lib.sgemm_grouped_outer, d, stream, check, M, N, K, groups,
                  _at("offsets", offsets, _I32, d, groups + 1), alpha,
                  _at("A", A, _F32, d, _span(K, M, lda)), lda,
                  _at("B", B, _F32, d, _span(K, N, ldb)), ldb, beta,

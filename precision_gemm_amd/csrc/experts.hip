@@ -73,7 +73,7 @@ expert_place_kernel(const Id *ids, int slots, int experts, int run, const int *c
                     int *offsets, int *row_of_slot)
 {
     __shared__ int next[kSortWaves * kMaxKeys]; // each wave's next row of every key
-    __shared__ int total[kMaxKeys];
+    __shared__ int total[kMaxKeys], before[kMaxKeys];
     __shared__ int wave_sum[kSortWaves];
     const int keys = experts + 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -91,31 +91,40 @@ expert_place_kernel(const Id *ids, int slots, int experts, int run, const int *c
         atomicAdd(&mine[key_of(ids, i, experts)], 1);
     __syncthreads();
 
-    // Each key: all runs' slots, and those of the runs before this one.
-    constexpr int PER = (kMaxKeys + kSortThreads - 1) / kSortThreads;
-    int before[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int e = tid + j * kSortThreads;
-        int all = 0, bef = 0;
-        if (e < keys) {
-            if (counts == nullptr) { // a single run: its own counts are all
-                for (int w = 0; w < kSortWaves; ++w)
-                    all += next[w * keys + e];
-            } else {
-                for (int b = 0; b < (int)gridDim.x; ++b) {
-                    const int n = counts[(long long)b * keys + e];
-                    all += n;
-                    bef += b < (int)blockIdx.x ? n : 0;
-                }
-            }
+    // Each key: all runs' slots, and those of the runs before this one. A
+    // single run's own counts are all; otherwise the threads share out the runs
+    // of the keys, so that all counts are in flight at once.
+    if (counts == nullptr) {
+        for (int e = tid; e < keys; e += kSortThreads) {
+            int all = 0;
+            for (int w = 0; w < kSortWaves; ++w)
+                all += next[w * keys + e];
             total[e] = all;
+            before[e] = 0;
         }
-        before[j] = bef;
+    } else {
+        for (int e = tid; e < keys; e += kSortThreads)
+            total[e] = before[e] = 0;
+        __syncthreads();
+        int width = 64; // threads along the keys
+        while (width < keys && width < kSortThreads)
+            width *= 2;
+        for (int e = tid & (width - 1); e < keys; e += width) {
+            int all = 0, bef = 0;
+#pragma unroll 8
+            for (int b = tid / width; b < (int)gridDim.x; b += kSortThreads / width) {
+                const int n = counts[(long long)b * keys + e];
+                all += n;
+                bef += b < (int)blockIdx.x ? n : 0;
+            }
+            atomicAdd(&total[e], all);
+            atomicAdd(&before[e], bef);
+        }
     }
     __syncthreads();
 
     // The rows before each key: an exclusive scan of the totals, 512 at a time.
+    constexpr int PER = (kMaxKeys + kSortThreads - 1) / kSortThreads;
     int carry = 0;
     int start[PER];
 #pragma unroll
@@ -147,7 +156,7 @@ expert_place_kernel(const Id *ids, int slots, int experts, int run, const int *c
             continue;
         if (blockIdx.x == 0)
             offsets[e] = start[j];
-        int at = start[j] + before[j];
+        int at = start[j] + before[e];
         for (int w = 0; w < kSortWaves; ++w) {
             const int n = next[w * keys + e];
             next[w * keys + e] = at;
@@ -182,11 +191,47 @@ expert_place_kernel(const Id *ids, int slots, int experts, int run, const int *c
     }
 }
 
+// Few slots, in one workgroup and without counts: a slot's row is the number of
+// slots that come before it, which are those with a smaller (key, slot) pair,
+// and an expert's offset is the number of pairs below (expert, 0). Each thread
+// compares its pair with all of them, read from LDS four at a time.
+constexpr int kFewSlots = 256;
+
+template <typename Id>
+__global__ void __launch_bounds__(512)
+expert_few_kernel(const Id *ids, int slots, int experts, int *offsets, int *row_of_slot)
+{
+    __shared__ __attribute__((aligned(16))) int pairs[kFewSlots];
+    const int tid = threadIdx.x;
+    if (tid < kFewSlots)
+        pairs[tid] = tid < slots ? key_of(ids, tid, experts) << 8 | tid : INT32_MAX;
+    __syncthreads();
+    // (The slots first, then experts + 1 offsets.)
+    for (int q = tid; q < slots + experts + 1; q += 512) {
+        const int own = q < slots ? pairs[q] : (q - slots) << 8;
+        int below = 0;
+#pragma unroll 8
+        for (int i = 0; i < slots; i += 4) {
+            const i32x4 v = *reinterpret_cast<const i32x4 *>(pairs + i);
+            below += (v.x < own) + (v.y < own) + (v.z < own) + (v.w < own);
+        }
+        if (q >= slots)
+            offsets[q - slots] = below;
+        else
+            row_of_slot[q] = own >> 8 < experts ? below : -1;
+    }
+}
+
 template <typename Id>
 int launch_sort(int slots, int experts, const void *ids_, int *offsets, int *row_of_slot,
                 int *counts, hipStream_t s)
 {
     const Id *ids = static_cast<const Id *>(ids_);
+    if (slots <= kFewSlots) {
+        void *args[] = {&ids, &slots, &experts, &offsets, &row_of_slot};
+        return (int)hipLaunchKernel((const void *)expert_few_kernel<Id>, dim3(1), dim3(512), args,
+                                    0, s);
+    }
     SortPlan plan = sort_plan(slots);
     if (plan.blocks == 1)
         counts = nullptr;
@@ -205,7 +250,10 @@ int launch_sort(int slots, int experts, const void *ids_, int *offsets, int *row
 // ---------------------------------------------------------------------------
 // Rows to and from the sorted order. `lanes` (a power of two up to 256)
 // neighbouring threads take one token's row, 16 bytes each at a time, so 256 /
-// lanes tokens share a workgroup. Rows need no alignment.
+// lanes tokens share a workgroup. SLOTS slots (a power of two up to 8, as many
+// as topk needs) go together, so that their rows are in flight at once. Rows
+// need no alignment. With WAVE, a token has whole waves, and its slots' rows
+// and weights are scalars.
 // ---------------------------------------------------------------------------
 struct RowParams {
     const char *in;      // X or dout, or Y of the sum
@@ -219,40 +267,80 @@ struct RowParams {
     int bytes; // of a row
 };
 
-__device__ __forceinline__ bool valid_row(const RowParams &p, int r)
+template <bool WAVE>
+__device__ __forceinline__ int token_of(const RowParams &p)
 {
-    return (unsigned)r < (unsigned)p.tokens * (unsigned)p.topk;
+    const int in_block = threadIdx.x / p.lanes;
+    return blockIdx.x * (256 / p.lanes) +
+           (WAVE ? __builtin_amdgcn_readfirstlane(in_block) : in_block);
 }
 
-template <int ES>
+// The sorted rows of slots j0.. of the token whose first slot is `at`, -1 for
+// none.
+template <int SLOTS>
+__device__ __forceinline__ void slot_rows(const RowParams &p, long long at, int j0, int (&r)[SLOTS])
+{
+    const unsigned all = (unsigned)p.tokens * (unsigned)p.topk;
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+        r[j] = j0 + j < p.topk ? p.row_of_slot[at + j0 + j] : -1;
+        r[j] = (unsigned)r[j] < all ? r[j] : -1;
+    }
+}
+
+template <int SLOTS>
+__device__ __forceinline__ void slot_weights(const RowParams &p, long long at, int j0,
+                                             float (&w)[SLOTS])
+{
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j)
+        w[j] = p.weights && j0 + j < p.topk ? p.weights[at + j0 + j] : 1.0f;
+}
+
+template <int ES, int SLOTS, bool WAVE>
 __global__ void __launch_bounds__(256) expert_gather_kernel(RowParams p)
 {
     const int lane = threadIdx.x & (p.lanes - 1);
-    const long long t = (long long)blockIdx.x * (256 / p.lanes) + threadIdx.x / p.lanes;
+    const int t = token_of<WAVE>(p);
     if (t >= p.tokens)
         return;
     const char *x = p.in + t * p.ld_in;
-    const int *rows = p.row_of_slot + t * p.topk;
+    const long long at = (long long)t * p.topk;
     for (int b = 16 * lane; b < p.bytes; b += 16 * p.lanes) {
-        if (b + 16 <= p.bytes) {
-            const i32x4 v = load16(x + b);
-            for (int j = 0; j < p.topk; ++j) {
-                const int r = rows[j];
-                if (valid_row(p, r))
-                    store16(p.out + r * p.ld_out + b, v);
-            }
-        } else {
-            typedef std::conditional_t<ES == 4, int, std::conditional_t<ES == 2, short, char>> E;
-            const int n = (p.bytes - b) / ES;
-            for (int j = 0; j < p.topk; ++j) {
-                const int r = rows[j];
-                if (valid_row(p, r))
+        const bool whole = b + 16 <= p.bytes;
+        i32x4 v = {};
+        if (whole)
+            v = load16(x + b);
+        for (int j0 = 0; j0 < p.topk; j0 += SLOTS) {
+            int r[SLOTS];
+            slot_rows(p, at, j0, r);
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) {
+                if (r[j] < 0)
+                    continue;
+                char *y = p.out + r[j] * p.ld_out + b;
+                if (whole) {
+                    store16(y, v);
+                } else {
+                    typedef std::conditional_t<
+                        ES == 4, int, std::conditional_t<ES == 2, short, char>> E;
+                    const int n = (p.bytes - b) / ES;
                     for (int i = 0; i < n; ++i)
-                        reinterpret_cast<E *>(p.out + r * p.ld_out + b)[i] =
-                            reinterpret_cast<const E *>(x + b)[i];
+                        reinterpret_cast<E *>(y)[i] = reinterpret_cast<const E *>(x + b)[i];
+                }
             }
         }
     }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(i32x4 v, float (&x)[16 / sizeof(T)])
+{
+    typedef T tv __attribute__((ext_vector_type(16 / sizeof(T))));
+    const tv h = __builtin_bit_cast(tv, v);
+#pragma unroll
+    for (int i = 0; i < (int)(16 / sizeof(T)); ++i)
+        x[i] = (float)h[i];
 }
 
 // 16 bytes of a row from byte b on as floats, zeros behind the row's end.
@@ -260,20 +348,15 @@ template <typename T>
 __device__ __forceinline__ void load_chunk(const char *row, int b, int bytes,
                                            float (&x)[16 / sizeof(T)])
 {
-    constexpr int VEC = 16 / sizeof(T);
     if (b + 16 <= bytes) {
-        typedef T tv __attribute__((ext_vector_type(VEC)));
-        const tv h = __builtin_bit_cast(tv, load16(row + b));
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            x[i] = (float)h[i];
-    } else {
-        const T *e = reinterpret_cast<const T *>(row + b);
-        const int n = (bytes - b) / (int)sizeof(T);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            x[i] = i < n ? (float)e[i] : 0.0f;
+        unpack<T>(load16(row + b), x);
+        return;
     }
+    const T *e = reinterpret_cast<const T *>(row + b);
+    const int n = (bytes - b) / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < (int)(16 / sizeof(T)); ++i)
+        x[i] = i < n ? (float)e[i] : 0.0f;
 }
 
 template <typename T>
@@ -298,28 +381,49 @@ __device__ __forceinline__ void store_chunk(char *row, int b, int bytes,
     }
 }
 
-template <typename T>
+// A chunk of the rows of SLOTS slots. A slot without a row fetches row 0 (which
+// there always is); its values are not used.
+template <typename T, int SLOTS>
+__device__ __forceinline__ void load_slots(const char *y, long long ld, const int (&r)[SLOTS], int b,
+                                           int bytes, float (&v)[SLOTS][16 / sizeof(T)])
+{
+    if (b + 16 <= bytes) {
+        i32x4 raw[SLOTS];
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j)
+            raw[j] = load16(y + max(r[j], 0) * ld + b);
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j)
+            unpack<T>(raw[j], v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j)
+            load_chunk<T>(y + max(r[j], 0) * ld, b, bytes, v[j]);
+    }
+}
+
+template <typename T, int SLOTS, bool WAVE>
 __global__ void __launch_bounds__(256) expert_combine_kernel(RowParams p)
 {
     constexpr int VEC = 16 / sizeof(T);
     const int lane = threadIdx.x & (p.lanes - 1);
-    const long long t = (long long)blockIdx.x * (256 / p.lanes) + threadIdx.x / p.lanes;
+    const int t = token_of<WAVE>(p);
     if (t >= p.tokens)
         return;
-    const int *rows = p.row_of_slot + t * p.topk;
-    const float *w = p.weights ? p.weights + t * p.topk : nullptr;
+    const long long at = (long long)t * p.topk;
     for (int b = 16 * lane; b < p.bytes; b += 16 * p.lanes) {
         float sum[VEC] = {};
-        for (int j = 0; j < p.topk; ++j) {
-            const int r = rows[j];
-            if (!valid_row(p, r))
-                continue;
-            float y[VEC];
-            load_chunk<T>(p.in + r * p.ld_in, b, p.bytes, y);
-            const float wj = w ? w[j] : 1.0f;
+        for (int j0 = 0; j0 < p.topk; j0 += SLOTS) {
+            int r[SLOTS];
+            float w[SLOTS], y[SLOTS][VEC];
+            slot_rows(p, at, j0, r);
+            slot_weights(p, at, j0, w);
+            load_slots<T>(p.in, p.ld_in, r, b, p.bytes, y);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                sum[i] = __builtin_fmaf(wj, y[i], sum[i]);
+            for (int j = 0; j < SLOTS; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    sum[i] = r[j] < 0 ? sum[i] : __builtin_fmaf(w[j], y[j][i], sum[i]);
         }
         store_chunk<T>(p.out + t * p.ld_out, b, p.bytes, sum);
     }
@@ -327,45 +431,43 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(RowParams p)
 
 // A token's lanes hold a part of dout's row; each slot's partial dot products
 // are added over the lanes by exchanges within a wave and through LDS across
-// the waves of a 256-lane token, always in the same order.
-template <typename T>
+// the waves of a token, always in the same order.
+template <typename T, int SLOTS, bool WAVE>
 __global__ void __launch_bounds__(256) expert_combine_grad_kernel(RowParams p)
 {
     constexpr int VEC = 16 / sizeof(T);
-    constexpr int SLOTS = 8; // slots taken together
     __shared__ float part[4][SLOTS];
     const int lane = threadIdx.x & (p.lanes - 1);
-    const long long t = (long long)blockIdx.x * (256 / p.lanes) + threadIdx.x / p.lanes;
-    const bool live = t < p.tokens; // (all threads reach the barriers)
-    const long long at = live ? t * p.topk : 0;
-    const char *g = p.in + (live ? t : 0) * p.ld_in;
+    const int token = token_of<WAVE>(p);
+    const bool live = token < p.tokens; // (all threads reach the barriers)
+    const int t = live ? token : 0;
+    const long long at = (long long)t * p.topk;
+    const char *g = p.in + t * p.ld_in;
     for (int j0 = 0; j0 < p.topk; j0 += SLOTS) {
-        float dot[SLOTS] = {};
+        float dot[SLOTS] = {}, w[SLOTS];
         int r[SLOTS];
-        float w[SLOTS];
-#pragma unroll
-        for (int j = 0; j < SLOTS; ++j) {
-            const bool in = live && j0 + j < p.topk;
-            r[j] = in ? p.row_of_slot[at + j0 + j] : -1;
-            if (!valid_row(p, r[j]))
-                r[j] = -1;
-            w[j] = in && p.weights ? p.weights[at + j0 + j] : 1.0f;
-        }
+        slot_rows(p, at, j0, r);
+        slot_weights(p, at, j0, w);
         if (live) {
             for (int b = 16 * lane; b < p.bytes; b += 16 * p.lanes) {
                 float d[VEC];
-                load_chunk<T>(g, b, p.bytes, d);
+                if (p.dweights) {
+                    float y[SLOTS][VEC];
+                    load_slots<T>(p.in2, p.ld_in2, r, b, p.bytes, y);
+                    load_chunk<T>(g, b, p.bytes, d);
+#pragma unroll
+                    for (int j = 0; j < SLOTS; ++j)
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i)
+                            dot[j] = __builtin_fmaf(d[i], y[j][i], dot[j]);
+                } else {
+                    load_chunk<T>(g, b, p.bytes, d);
+                }
 #pragma unroll
                 for (int j = 0; j < SLOTS; ++j) {
                     if (r[j] < 0)
                         continue;
                     float v[VEC];
-                    if (p.dweights) {
-                        load_chunk<T>(p.in2 + r[j] * p.ld_in2, b, p.bytes, v);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i)
-                            dot[j] = __builtin_fmaf(d[i], v[i], dot[j]);
-                    }
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
                         v[i] = w[j] * d[i];
@@ -403,19 +505,34 @@ __global__ void __launch_bounds__(256) expert_combine_grad_kernel(RowParams p)
     }
 }
 
-int launch_rows(const void *fn, RowParams p, hipStream_t s)
+typedef void (*RowFn)(RowParams);
+
+// A kernel by slots taken together (1, 2, 4, 8) and by WAVE.
+struct RowKernels {
+    RowFn fn[4][2];
+};
+
+#define ROW_KERNELS(kernel, type)                                      \
+    RowKernels                                                         \
+    {                                                                  \
+        {{kernel<type, 1, false>, kernel<type, 1, true>},              \
+         {kernel<type, 2, false>, kernel<type, 2, true>},              \
+         {kernel<type, 4, false>, kernel<type, 4, true>},              \
+         {kernel<type, 8, false>, kernel<type, 8, true>}},             \
+    }
+
+int launch_rows(const RowKernels &k, RowParams p, hipStream_t s)
 {
     p.lanes = 1;
     while (p.lanes < 256 && 16LL * p.lanes < p.bytes)
         p.lanes *= 2;
-    const int per = 256 / p.lanes;
-    // A launch holds fewer than 2^32 work-items. A later one starts at the
-    // token it is given; the rows it names stay those of all tokens.
-    const long long blocks = ceil_div_ll(p.tokens, per);
-    if (blocks > (1 << 23))
+    const long long blocks = ceil_div_ll(p.tokens, 256 / p.lanes);
+    if (blocks > (1 << 23)) // a launch holds fewer than 2^32 work-items
         return -22;
+    const int slots = p.topk <= 1 ? 0 : p.topk <= 2 ? 1 : p.topk <= 4 ? 2 : 3;
     void *args[] = {&p};
-    return (int)hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, s);
+    return (int)hipLaunchKernel((const void *)k.fn[slots][p.lanes >= 64], dim3((unsigned)blocks),
+                                dim3(256), args, 0, s);
 }
 
 bool float_type(int type) { return type == SGEMM_F32 || type == SGEMM_F16 || type == SGEMM_BF16; }
@@ -483,10 +600,10 @@ extern "C" int expert_gather(int tokens, int topk, int cols, const void *X, int 
     p.tokens = tokens;
     p.topk = topk;
     p.bytes = cols * es;
-    const void *fn = es == 4   ? (const void *)expert_gather_kernel<4>
-                     : es == 2 ? (const void *)expert_gather_kernel<2>
-                               : (const void *)expert_gather_kernel<1>;
-    return launch_rows(fn, p, static_cast<hipStream_t>(stream));
+    static const RowKernels kernels[] = {ROW_KERNELS(expert_gather_kernel, 4),
+                                         ROW_KERNELS(expert_gather_kernel, 2),
+                                         ROW_KERNELS(expert_gather_kernel, 1)};
+    return launch_rows(kernels[es == 4 ? 0 : es == 2 ? 1 : 2], p, static_cast<hipStream_t>(stream));
 }
 
 extern "C" int expert_combine(int tokens, int topk, int cols, const void *Y, int type, int ldy,
@@ -517,10 +634,10 @@ extern "C" int expert_combine(int tokens, int topk, int cols, const void *Y, int
     p.tokens = tokens;
     p.topk = topk;
     p.bytes = cols * es;
-    const void *fn = type == SGEMM_F32   ? (const void *)expert_combine_kernel<float>
-                     : type == SGEMM_F16 ? (const void *)expert_combine_kernel<_Float16>
-                                         : (const void *)expert_combine_kernel<__bf16>;
-    return launch_rows(fn, p, static_cast<hipStream_t>(stream));
+    static const RowKernels kernels[] = {ROW_KERNELS(expert_combine_kernel, float),
+                                         ROW_KERNELS(expert_combine_kernel, _Float16),
+                                         ROW_KERNELS(expert_combine_kernel, __bf16)};
+    return launch_rows(kernels[type], p, static_cast<hipStream_t>(stream));
 }
 
 extern "C" int expert_combine_grad(int tokens, int topk, int cols, const void *dout, int type,
@@ -558,8 +675,8 @@ extern "C" int expert_combine_grad(int tokens, int topk, int cols, const void *d
     p.tokens = tokens;
     p.topk = topk;
     p.bytes = cols * es;
-    const void *fn = type == SGEMM_F32   ? (const void *)expert_combine_grad_kernel<float>
-                     : type == SGEMM_F16 ? (const void *)expert_combine_grad_kernel<_Float16>
-                                         : (const void *)expert_combine_grad_kernel<__bf16>;
-    return launch_rows(fn, p, static_cast<hipStream_t>(stream));
+    static const RowKernels kernels[] = {ROW_KERNELS(expert_combine_grad_kernel, float),
+                                         ROW_KERNELS(expert_combine_grad_kernel, _Float16),
+                                         ROW_KERNELS(expert_combine_grad_kernel, __bf16)};
+    return launch_rows(kernels[type], p, static_cast<hipStream_t>(stream));
 }
