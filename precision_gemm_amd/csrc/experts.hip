@@ -263,38 +263,55 @@ struct RowParams {
     const float *weights;
     float *dweights;
     long long ld_in, ld_in2, ld_out; // bytes
-    int tokens, topk, lanes;
+    int tokens, topk;
+    int lanes, log_lanes;
     int bytes; // of a row
 };
 
 template <bool WAVE>
 __device__ __forceinline__ int token_of(const RowParams &p)
 {
-    const int in_block = threadIdx.x / p.lanes;
-    return blockIdx.x * (256 / p.lanes) +
+    const int in_block = threadIdx.x >> p.log_lanes;
+    return blockIdx.x * (256 >> p.log_lanes) +
            (WAVE ? __builtin_amdgcn_readfirstlane(in_block) : in_block);
+}
+
+// Through the constant address space a wave's common value is a scalar load
+// (no kernel here writes what it reads so).
+template <bool WAVE, typename T>
+__device__ __forceinline__ T slot_value(const T *x, long long i)
+{
+    if constexpr (WAVE)
+        return ((const __attribute__((address_space(4))) T *)(uintptr_t)x)[i];
+    else
+        return x[i];
 }
 
 // The sorted rows of slots j0.. of the token whose first slot is `at`, -1 for
 // none.
-template <int SLOTS>
+template <bool WAVE, int SLOTS>
 __device__ __forceinline__ void slot_rows(const RowParams &p, long long at, int j0, int (&r)[SLOTS])
 {
     const unsigned all = (unsigned)p.tokens * (unsigned)p.topk;
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j) {
-        r[j] = j0 + j < p.topk ? p.row_of_slot[at + j0 + j] : -1;
-        r[j] = (unsigned)r[j] < all ? r[j] : -1;
+        // (Behind the last slot: the last one's again, and then -1.)
+        r[j] = slot_value<WAVE>(p.row_of_slot, at + min(j0 + j, p.topk - 1));
+        r[j] = j0 + j < p.topk && (unsigned)r[j] < all ? r[j] : -1;
     }
 }
 
-template <int SLOTS>
+template <bool WAVE, int SLOTS>
 __device__ __forceinline__ void slot_weights(const RowParams &p, long long at, int j0,
                                              float (&w)[SLOTS])
 {
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j)
-        w[j] = p.weights && j0 + j < p.topk ? p.weights[at + j0 + j] : 1.0f;
+        w[j] = 1.0f;
+    if (p.weights)
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j)
+            w[j] = slot_value<WAVE>(p.weights, at + min(j0 + j, p.topk - 1));
 }
 
 template <int ES, int SLOTS, bool WAVE>
@@ -313,7 +330,7 @@ __global__ void __launch_bounds__(256) expert_gather_kernel(RowParams p)
             v = load16(x + b);
         for (int j0 = 0; j0 < p.topk; j0 += SLOTS) {
             int r[SLOTS];
-            slot_rows(p, at, j0, r);
+            slot_rows<WAVE>(p, at, j0, r);
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
                 if (r[j] < 0)
@@ -416,8 +433,8 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(RowParams p)
         for (int j0 = 0; j0 < p.topk; j0 += SLOTS) {
             int r[SLOTS];
             float w[SLOTS], y[SLOTS][VEC];
-            slot_rows(p, at, j0, r);
-            slot_weights(p, at, j0, w);
+            slot_rows<WAVE>(p, at, j0, r);
+            slot_weights<WAVE>(p, at, j0, w);
             load_slots<T>(p.in, p.ld_in, r, b, p.bytes, y);
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j)
@@ -446,8 +463,8 @@ __global__ void __launch_bounds__(256) expert_combine_grad_kernel(RowParams p)
     for (int j0 = 0; j0 < p.topk; j0 += SLOTS) {
         float dot[SLOTS] = {}, w[SLOTS];
         int r[SLOTS];
-        slot_rows(p, at, j0, r);
-        slot_weights(p, at, j0, w);
+        slot_rows<WAVE>(p, at, j0, r);
+        slot_weights<WAVE>(p, at, j0, w);
         if (live) {
             for (int b = 16 * lane; b < p.bytes; b += 16 * p.lanes) {
                 float d[VEC];
@@ -489,7 +506,7 @@ __global__ void __launch_bounds__(256) expert_combine_grad_kernel(RowParams p)
                 for (int j = 0; j < SLOTS; ++j)
                     part[threadIdx.x >> 6][j] = dot[j];
             __syncthreads();
-            const int w0 = (threadIdx.x / p.lanes) * (p.lanes / 64);
+            const int w0 = (threadIdx.x >> p.log_lanes) * (p.lanes / 64);
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
                 dot[j] = part[w0][j];
@@ -524,8 +541,10 @@ struct RowKernels {
 int launch_rows(const RowKernels &k, RowParams p, hipStream_t s)
 {
     p.lanes = 1;
-    while (p.lanes < 256 && 16LL * p.lanes < p.bytes)
+    while (p.lanes < 256 && 16LL * p.lanes < p.bytes) {
         p.lanes *= 2;
+        ++p.log_lanes;
+    }
     const long long blocks = ceil_div_ll(p.tokens, 256 / p.lanes);
     if (blocks > (1 << 23)) // a launch holds fewer than 2^32 work-items
         return -22;
