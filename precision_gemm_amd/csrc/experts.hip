@@ -13,7 +13,7 @@ namespace {
 // The sort: a stable counting sort of the slots by expert. Slots without an
 // expert get the key `experts`, one past the last.
 //
-// The slots are cut into at most kMaxBlocks consecutive runs, one a workgroup.
+// The slots are cut into consecutive runs, one a workgroup (sort_plan).
 // The first kernel counts each run's keys. In the second, a workgroup adds up
 // the counts of the runs before its own and of all experts below each, which
 // is the row of its first slot with that expert; its waves, each on a
@@ -24,22 +24,30 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxBlocks = 256;
-constexpr int kLeastRun = 2048;  // slots of a run, but for the last
 constexpr int kMaxKeys = EXPERT_SORT_MAX_EXPERTS + 1;
 
 struct SortPlan {
     int blocks, run; // runs of `run` slots (a multiple of 64 * kSortWaves)
 };
 
-SortPlan sort_plan(long long slots)
+// Up to 2048 slots are one run and one kernel (2048 slots of 64 experts: 6.3
+// us, against 7.5 in two runs and kernels). Beyond, runs of 1024 (16384 slots:
+// 8.6 us, of 2048 9.5), longer ones where there would be over 256, or, up to
+// 8192, where each workgroup would read over 2^16 counts (1024 experts: 131072
+// slots 20 us with 64 runs, 25 with 128; 524288 slots 34 with 64, 43 with 256;
+// 2097152 slots 84 with 64, 56 with 256).
+SortPlan sort_plan(long long slots, int keys)
 {
     const long long unit = 64 * kSortWaves;
-    long long run = ceil_div_ll(ceil_div_ll(slots, kMaxBlocks), unit) * unit;
-    if (run < kLeastRun)
-        run = kLeastRun;
-    const long long blocks = slots > 0 ? ceil_div_ll(slots, run) : 1;
-    return SortPlan{(int)blocks, (int)run};
+    if (slots <= 2048)
+        return SortPlan{1, (int)(slots > 0 ? ceil_div_ll(slots, unit) * unit : unit)};
+    long long most = (1 << 16) / keys;
+    most = most < slots / 8192 ? slots / 8192 : most;
+    most = most < 256 ? most : 256;
+    long long run = ceil_div_ll(ceil_div_ll(slots, most), unit) * unit;
+    if (run < 1024)
+        run = 1024;
+    return SortPlan{(int)ceil_div_ll(slots, run), (int)run};
 }
 
 template <typename Id>
@@ -191,48 +199,12 @@ expert_place_kernel(const Id *ids, int slots, int experts, int run, const int *c
     }
 }
 
-// Few slots, in one workgroup and without counts: a slot's row is the number of
-// slots that come before it, which are those with a smaller (key, slot) pair,
-// and an expert's offset is the number of pairs below (expert, 0). Each thread
-// compares its pair with all of them, read from LDS four at a time.
-constexpr int kFewSlots = 256;
-
-template <typename Id>
-__global__ void __launch_bounds__(512)
-expert_few_kernel(const Id *ids, int slots, int experts, int *offsets, int *row_of_slot)
-{
-    __shared__ __attribute__((aligned(16))) int pairs[kFewSlots];
-    const int tid = threadIdx.x;
-    if (tid < kFewSlots)
-        pairs[tid] = tid < slots ? key_of(ids, tid, experts) << 8 | tid : INT32_MAX;
-    __syncthreads();
-    // (The slots first, then experts + 1 offsets.)
-    for (int q = tid; q < slots + experts + 1; q += 512) {
-        const int own = q < slots ? pairs[q] : (q - slots) << 8;
-        int below = 0;
-#pragma unroll 8
-        for (int i = 0; i < slots; i += 4) {
-            const i32x4 v = *reinterpret_cast<const i32x4 *>(pairs + i);
-            below += (v.x < own) + (v.y < own) + (v.z < own) + (v.w < own);
-        }
-        if (q >= slots)
-            offsets[q - slots] = below;
-        else
-            row_of_slot[q] = own >> 8 < experts ? below : -1;
-    }
-}
-
 template <typename Id>
 int launch_sort(int slots, int experts, const void *ids_, int *offsets, int *row_of_slot,
                 int *counts, hipStream_t s)
 {
     const Id *ids = static_cast<const Id *>(ids_);
-    if (slots <= kFewSlots) {
-        void *args[] = {&ids, &slots, &experts, &offsets, &row_of_slot};
-        return (int)hipLaunchKernel((const void *)expert_few_kernel<Id>, dim3(1), dim3(512), args,
-                                    0, s);
-    }
-    SortPlan plan = sort_plan(slots);
+    SortPlan plan = sort_plan(slots, experts + 1);
     if (plan.blocks == 1)
         counts = nullptr;
     if (counts) {
@@ -567,7 +539,7 @@ extern "C" size_t expert_sort_workspace_size(int tokens, int topk, int experts)
 {
     if (topk < 1 || !slots_ok(tokens, topk) || experts < 1 || experts > EXPERT_SORT_MAX_EXPERTS)
         return 0;
-    const SortPlan plan = sort_plan((long long)tokens * topk);
+    const SortPlan plan = sort_plan((long long)tokens * topk, experts + 1);
     return plan.blocks > 1 ? (size_t)plan.blocks * (experts + 1) * sizeof(int) : 0;
 }
 
