@@ -2985,38 +2985,93 @@ __device__ __forceinline__ void grouped_tile(const Params &p, const float *Ab, c
         opb.o0 = n0;
         opb.init(tid, kfirst);
 
+        // Two register buffers for the staged loads, by step parity: step s
+        // issues the loads of step s + 2 and writes the data of step s + 1,
+        // loaded one step earlier, halfway through its products. The last
+        // products of a step run after its barrier, over the first reads of
+        // the next. (Windows past K read inside the operand or zeros; neither
+        // is used.)
+        constexpr int LATE = TM * TN;
+        f32x4 ra[2][OpA::SLOTS], rb[2][OpB::SLOTS];
         const int nsteps = (Kt + BK - 1) / BK;
-        f32x4 ra[OpA::SLOTS], rb[OpB::SLOTS];
-        opa.template load_next<true>(tid, ra);
-        opb.template load_next<true>(tid, rb);
-        for (int s = 0; s < nsteps; ++s) {
-            float *cur = lds + (s & 1) * STAGE;
-            OpA::store(cur, tid, ra);
-            OpB::store(cur + OpA::STAGE, tid, rb);
-            // (After the last step the window lies past K; what a lane reads
-            // there, inside the operand or zeros, is not used.)
-            opa.template load_next<false>(tid, ra);
-            opb.template load_next<false>(tid, rb);
-            __syncthreads();
+        auto read_group = [&](const float *stage, int q, float (&fa)[TM][4], float (&fb)[TN][4]) {
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-                float fa[TM][4], fb[TN][4];
+            for (int i = 0; i < TM; ++i)
+                OpA::frag(stage, wm0 + 32 * i, q, lane, fa[i]);
 #pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    OpA::frag(cur, wm0 + 32 * i, q, lane, fa[i]);
+            for (int j = 0; j < TN; ++j)
+                OpB::frag(stage + OpA::STAGE, wn0 + 32 * j, q, lane, fb[j]);
+        };
+        auto mfma_group = [&](const float (&fa)[TM][4], const float (&fb)[TN][4], int first,
+                              int last) {
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    OpB::frag(cur + OpA::STAGE, wn0 + 32 * j, q, lane, fb[j]);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                    for (int i = 0; i < TM; ++i)
-#pragma unroll
-                        for (int j = 0; j < TN; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                                fa[i][kk], fb[j][kk], acc[i][j], 0, 0, 0);
+            for (int t = 0; t < 4 * TM * TN; ++t) {
+                if (t < first || t >= last)
+                    continue;
+                const int kk = t / (TM * TN), i = (t / TN) % TM, j = t % TN;
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i][kk], fb[j][kk], acc[i][j],
+                                                                 0, 0, 0);
             }
+        };
+        opa.template load_next<true>(tid, ra[0]);
+        opb.template load_next<true>(tid, rb[0]);
+        OpA::store(lds, tid, ra[0]);
+        OpB::store(lds + OpA::STAGE, tid, rb[0]);
+        opa.template load_next<false>(tid, ra[1]);
+        opb.template load_next<false>(tid, rb[1]);
+        __syncthreads();
+        float fa[NQ][TM][4], fb[NQ][TN][4];
+        read_group(lds, 0, fa[0], fb[0]);
+        auto k_step = [&](auto parity) {
+            constexpr int PAR = decltype(parity)::value;
+            const float *cur = lds + PAR * STAGE;
+            float *nxt = lds + (1 - PAR) * STAGE;
+#pragma unroll
+            for (int q = 1; q < NQ; ++q)
+                read_group(cur, q, fa[q], fb[q]);
+            mfma_group(fa[0], fb[0], 0, 4 * TM * TN);
+            constexpr int NW = OpA::SLOTS + OpB::SLOTS;
+            constexpr int NL = NW * OpA::EPS;
+            constexpr int NM = 4 * TM * TN * NQ - LATE;
+            opa.template load_next<false>(tid, ra[PAR]);
+            opb.template load_next<false>(tid, rb[PAR]);
+#pragma unroll
+            for (int q = 1; q < NQ - 1; ++q)
+                mfma_group(fa[q], fb[q], 0, 4 * TM * TN);
+            mfma_group(fa[NQ - 1], fb[NQ - 1], 0, 4 * TM * TN - LATE);
+            OpA::store(nxt, tid, ra[1 - PAR]);
+            OpB::store(nxt + OpA::STAGE, tid, rb[1 - PAR]);
+            __builtin_amdgcn_sched_group_barrier(0x100, 4 * (TM + TN) * (NQ - 1), 0);
+#pragma unroll
+            for (int w = 0; w < NL; ++w) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+            constexpr int MID = (NM - NL - NW) / 2 > 0 ? (NM - NL - NW) / 2 : 0;
+            if constexpr (MID > 0)
+                __builtin_amdgcn_sched_group_barrier(0x008, MID, 0);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            __syncthreads();
+            __builtin_amdgcn_sched_barrier(0);
+            read_group(nxt, 0, fa[0], fb[0]);
+            mfma_group(fa[NQ - 1], fb[NQ - 1], 4 * TM * TN - LATE, 4 * TM * TN);
+            __builtin_amdgcn_sched_group_barrier(0x100, 4 * (TM + TN), 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, LATE, 0);
+        };
+        using P0 = std::integral_constant<int, 0>;
+        using P1 = std::integral_constant<int, 1>;
+        int s = 0;
+        for (; s + 1 < nsteps; s += 2) {
+            k_step(P0{});
+            k_step(P1{});
         }
+        if (s < nsteps)
+            k_step(P0{});
     }
     float res[TM][TN][16];
 #pragma unroll
@@ -3057,6 +3112,8 @@ sgemm_grouped_outer_kernel(GroupedParams gp)
 {
     __shared__ __attribute__((aligned(16))) float lds[2 * (BM + BN) * kBK];
     Params p = gp.p;
+    // Group by group, a group's tiles over all XCDs: their work goes with its
+    // rows, and an XCD that had whole groups would keep the others waiting.
     const int tiles = p.tiles_m * p.tiles_n;
     const int g = blockIdx.x / tiles, t = blockIdx.x % tiles;
     int lo, hi;
@@ -3075,7 +3132,167 @@ sgemm_grouped_outer_kernel(GroupedParams gp)
         t / p.tiles_n * BM, t % p.tiles_n * BN, lds);
 }
 
+// E floats of a row from column k on, zeros from column K on; nothing outside
+// the row's K floats is read, and no alignment is needed.
+template <int E>
+struct Floats {
+    float x[E];
+};
+
+template <int E>
+__device__ __forceinline__ Floats<E> whole_floats(const float *x)
+{
+    if constexpr (E == 4)
+        return __builtin_bit_cast(Floats<4>, load16(x));
+    else if constexpr (E == 2)
+        return __builtin_bit_cast(Floats<2>, i32x2(*reinterpret_cast<const i32x2_any *>(x)));
+    else
+        return Floats<1>{{*x}};
+}
+
+template <int E>
+__device__ __forceinline__ Floats<E> row_floats(const float *row, int k, int K)
+{
+    if (k + E <= K)
+        return whole_floats<E>(row + k);
+    Floats<E> v;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        v.x[e] = k + e < K ? row[k + e] : 0.0f;
+    return v;
+}
+
+// Few rows a group: the groups' weights bound the call, so they go from memory
+// straight into the matrix instructions' registers. A workgroup owns 16 * EN
+// columns and up to 16 * MT rows of a group; its WAVES waves take every
+// WAVES-th block of 16 k, and their partial sums are added in LDS in the waves'
+// order. In v_mfma_f32_16x16x4_f32 lane l supplies row l % 16 and one k, l /
+// 16; the four products j of a block give it k = 4 (l / 16) + j, so that one
+// 16-byte load along k serves all four. B stored K x N is loaded along its
+// columns instead: product (j, e) takes column EN (l % 16) + e of row j.
+template <int MT, int EN, int WAVES, int U, bool B_KC>
+__global__ void __launch_bounds__(64 * WAVES) sgemm_grouped_stream_kernel(GroupedParams gp)
+{
+    constexpr int BM = 16 * MT, BN = 16 * EN;
+    constexpr int NL = B_KC ? EN : 4, EL = B_KC ? 4 : EN; // loads of B a block, their width
+    __shared__ float sums[WAVES][BM][BN];
+    const Params &p = gp.p;
+    int g, lo, m0, rows, tm = 0, tn = 0;
+    auto pick = [&](int tiles) {
+        return tile_order(tiles, p.tiles_n, gp.band, tm, tn) ? tm : -1;
+    };
+    if (!find_tile(gp.offsets, gp.groups, p.M, BM, pick, g, lo, rows, m0))
+        return;
+    const int n0 = tn * BN;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, kq = 4 * (lane >> 4);
+    const float *A = p.A + (long long)lo * p.lda, *B = p.B + g * gp.stride;
+    const float *ra[MT], *rb[NL];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        ra[i] = A + (long long)min(m0 + 16 * i + r, rows - 1) * p.lda;
+#pragma unroll
+    for (int x = 0; x < NL; ++x)
+        rb[x] = B_KC ? B + (long long)min(n0 + 16 * x + r, p.N - 1) * p.ldb
+                     : B + (long long)(kq + x) * p.ldb; // (row k on top of it)
+    const int col = n0 + EN * r; // B stored K x N: this lane's first column
+
+    f32x4 acc[MT][EN] = {};
+    // One block of 16 k. b[x]: B_KC, x = e: column n0 + 16 e + r, four k;
+    // otherwise x = j: row k + kq + j, EN columns.
+    auto products = [&](const Floats<4> (&a)[MT], const Floats<EL> (&b)[NL]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < EN; ++e)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                        a[i].x[j], B_KC ? b[B_KC ? e : 0].x[B_KC ? j : 0]
+                                        : b[B_KC ? 0 : j].x[B_KC ? 0 : e],
+                        acc[i][e], 0, 0, 0);
+    };
+    int k = 16 * wave;
+    if (B_KC || n0 + BN <= p.N) {
+        // U blocks at a time, all their loads before the first product (the
+        // compiler would wait for each load by itself).
+        for (; k + 16 * WAVES * (U - 1) + 16 <= p.K; k += 16 * WAVES * U) {
+            Floats<4> a[U][MT];
+            Floats<EL> b[U][NL];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int ku = k + 16 * WAVES * u;
+#pragma unroll
+                for (int x = 0; x < NL; ++x)
+                    b[u][x] = whole_floats<EL>(B_KC ? rb[x] + ku + kq
+                                                    : rb[x] + (long long)ku * p.ldb + col);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    a[u][i] = whole_floats<4>(ra[i] + ku + kq);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                products(a[u], b[u]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // What is left: the last blocks, the one K ends in, or the columns N ends in.
+    for (; k < p.K; k += 16 * WAVES) {
+        Floats<4> a[MT];
+        Floats<EL> b[NL];
+#pragma unroll
+        for (int x = 0; x < NL; ++x) {
+            if (B_KC)
+                b[x] = row_floats<EL>(rb[x], k + kq, p.K);
+            else // (a row behind K: no columns of it)
+                b[x] = row_floats<EL>(rb[x] + (long long)k * p.ldb, col,
+                                      k + kq + x < p.K ? p.N : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            a[i] = row_floats<4>(ra[i], k + kq, p.K);
+        products(a, b);
+    }
+    // acc[i][e][v]: row 16 i + 4 (l / 16) + v, column 16 e + r or EN r + e.
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < EN; ++e)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                sums[wave][16 * i + kq + v][B_KC ? 16 * e + r : EN * r + e] = acc[i][e][v];
+    __syncthreads();
+    const int left = min(BM, rows - m0);
+    for (int x = tid; x < left * BN; x += 64 * WAVES) {
+        const int m = x / BN, n = n0 + x % BN;
+        if (n >= p.N)
+            continue;
+        float sum = sums[0][m][x % BN];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w)
+            sum += sums[w][m][x % BN];
+        float *c = p.C + (long long)(lo + m0 + m) * p.ldc + n;
+        *c = p.beta == 0.0f ? p.alpha * sum : __builtin_fmaf(p.alpha, sum, p.beta * *c);
+    }
+}
+
 typedef void (*GroupedFn)(GroupedParams);
+
+struct GroupedTile {
+    GroupedFn fn;
+    int bm, bn, threads;
+};
+
+// 128 x 128 tiles run at 95 % of the matrix rate and 64 x 64 ones at 88 %, but
+// leave finer rounds: the cheaper by the rounds of the CUs that `t128` and
+// `t64` tiles take.
+bool larger_tile(double t128, double t64, int cus)
+{
+    auto rounds = [&](double t) { return (double)ceil_div((long long)(t + 0.999), cus); };
+    return 4.0 * rounds(t128) / 0.95 < rounds(t64) / 0.88;
+}
 
 int launch_grouped(GroupedFn fn, GroupedParams gp, long long blocks, int threads, hipStream_t s)
 {
@@ -3129,14 +3346,57 @@ extern "C" int sgemm_grouped(int transB, int M, int N, int K, int groups, const 
     gp.stride = strideB;
     const bool vec4 = aligned16(A) && aligned16(B) && lda % 4 == 0 && ldb % 4 == 0 &&
                       strideB % 4 == 0 && K % 4 == 0 && (transB || N % 4 == 0);
-    const int bm = 64, bn = 64;
-    const GroupedFn fn = vec4 ? (transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 4>
-                                        : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 4>)
-                              : (transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 1>
-                                        : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>);
-    gp.p.tiles_n = (int)ceil_div(N, bn);
-    gp.band = group_band(M, groups, bm);
-    return launch_grouped(fn, gp, most_tiles(M, groups, bm) * gp.p.tiles_n, 256,
+    // (Refused before the device is asked: not even 128 x 128 tiles fit a launch.)
+    if (most_tiles(M, groups, 128) * ceil_div(N, 128) > INT32_MAX / 256)
+        return -22;
+    int cus = 0;
+    const int st = num_cus_of_current_device(&cus);
+    if (st != 0)
+        return st;
+    // Row tiles as the groups would need with half a tile more than their
+    // average each.
+    const double used = groups < M ? groups : M;
+    auto tiles = [&](int bm, int bn) {
+        const double each = (double)M / groups / bm + 0.5;
+        return used * (each > 1.0 ? each : 1.0) * (double)ceil_div(N, bn);
+    };
+    GroupedTile t;
+    if (M <= 16LL * groups) {
+        // Up to 16 rows a group on average: the weights stream, under row tiles
+        // of 16 or 32 (256 rows over 16 groups, 1024 x 1024, weights from
+        // memory: 20 us, the 64 x 64 tile 28; 512 rows: that tile 28). 64
+        // columns a workgroup (100 rows over 16 groups: 16.0 us), or 16 and
+        // more waves where that leaves half the CUs without one (one row, one
+        // group, 4096 x 4096: 20.5 us against 33.5).
+        const int bm = M <= 8LL * groups ? 16 : 32;
+        const bool wide = 2.0 * tiles(bm, 64) >= cus;
+        if (bm == 16)
+            t = wide ? GroupedTile{transB ? sgemm_grouped_stream_kernel<1, 4, 8, 1, true>
+                                          : sgemm_grouped_stream_kernel<1, 4, 8, 1, false>,
+                                   16, 64, 512}
+                     : GroupedTile{transB ? sgemm_grouped_stream_kernel<1, 1, 16, 2, true>
+                                          : sgemm_grouped_stream_kernel<1, 1, 16, 2, false>,
+                                   16, 16, 1024};
+        else
+            t = wide ? GroupedTile{transB ? sgemm_grouped_stream_kernel<2, 4, 8, 1, true>
+                                          : sgemm_grouped_stream_kernel<2, 4, 8, 1, false>,
+                                   32, 64, 512}
+                     : GroupedTile{transB ? sgemm_grouped_stream_kernel<2, 1, 16, 2, true>
+                                          : sgemm_grouped_stream_kernel<2, 1, 16, 2, false>,
+                                   32, 16, 1024};
+    }
+    else if (!vec4)
+        t = {transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 1>
+                    : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>, 64, 64, 256};
+    else if (larger_tile(tiles(128, 128), tiles(64, 64), cus))
+        t = {transB ? sgemm_grouped_kernel<128, 128, 2, 2, 2, true, 4>
+                    : sgemm_grouped_kernel<128, 128, 2, 2, 2, false, 4>, 128, 128, 256};
+    else
+        t = {transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 4>
+                    : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 4>, 64, 64, 256};
+    gp.p.tiles_n = (int)ceil_div(N, t.bn);
+    gp.band = group_band(M, groups, t.bm);
+    return launch_grouped(t.fn, gp, most_tiles(M, groups, t.bm) * gp.p.tiles_n, t.threads,
                           reinterpret_cast<hipStream_t>(stream));
 }
 
@@ -3179,15 +3439,25 @@ extern "C" int sgemm_grouped_outer(int M, int N, int K, int groups, const int *o
     gp.stride = strideC;
     const bool vec4 = aligned16(A) && aligned16(B) && lda % 4 == 0 && ldb % 4 == 0 &&
                       M % 4 == 0 && N % 4 == 0;
-    const int bm = 64, bn = 64;
-    const GroupedFn fn = vec4 ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 4>
-                              : sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 1>;
-    gp.p.tiles_m = (int)ceil_div(M, bm);
-    gp.p.tiles_n = (int)ceil_div(N, bn);
-    const long long per_group = (long long)gp.p.tiles_m * gp.p.tiles_n;
-    if (per_group > INT32_MAX / 256)
+    // (Refused before the device is asked: not even 128 x 128 tiles fit a launch.)
+    if ((double)ceil_div(M, 128) * ceil_div(N, 128) * groups > (double)(INT32_MAX / 256))
         return -22;
-    return launch_grouped(fn, gp, per_group * groups, 256, reinterpret_cast<hipStream_t>(stream));
+    int cus = 0;
+    const int st = num_cus_of_current_device(&cus);
+    if (st != 0)
+        return st;
+    GroupedTile t{vec4 ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 4>
+                       : sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 1>, 64, 64, 256};
+    if (vec4 && larger_tile((double)ceil_div(M, 128) * ceil_div(N, 128) * groups,
+                            (double)ceil_div(M, 64) * ceil_div(N, 64) * groups, cus))
+        t = {sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 4>, 128, 128, 256};
+    const long long tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn);
+    if ((double)tm * tn * groups > (double)(INT32_MAX / 256))
+        return -22;
+    gp.p.tiles_m = (int)tm;
+    gp.p.tiles_n = (int)tn;
+    return launch_grouped(t.fn, gp, tm * tn * groups, t.threads,
+                          reinterpret_cast<hipStream_t>(stream));
 }
 
 extern "C" const char *sgemm_status_string(int status)
