@@ -480,48 +480,89 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const signed char *b
                                              0x00020000);
 }
 
+// vmcnt <= N, lgkmcnt and expcnt as they are.
 template <int N>
 __device__ __forceinline__ void wait_loads()
 {
-    // vmcnt <= N, lgkmcnt and expcnt as they are
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
-__device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *lds)
+// All waves meet: N of this wave's memory operations may still be under way,
+// its LDS reads are done.
+template <int N>
+__device__ __forceinline__ void meet()
 {
-    constexpr int BK = 128, KH = BK / 32, NW = WAVES_M * WAVES_N;
-    constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 32, TN = WN / 32;
-    constexpr int STAGE = (BM + BN) * BK;
-    constexpr int NA = BM * BK / 1024 / NW, NB = BN * BK / 1024 / NW; // blocks a wave loads
-    static_assert(NA >= 1 && NB >= 1 && STAGES >= 2 && (STAGES - 1) * (NA + NB) <= 63, "loads in flight");
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    wait_loads<N>();
+    __builtin_amdgcn_s_waitcnt(0xc07f); // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
 
-    I8Tile t;
-    if (!i8_tile_of<BM, BN>(p, t))
-        return;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // (Waves that share a SIMD, four apart, lie above one another in M.)
-    const int wm = (wave / WAVES_N) * WM, wn = (wave % WAVES_N) * WN;
+template <int BM, int BN, int WAVES_M, int WAVES_N>
+struct I8Core {
+    static constexpr int BK = 128, KH = BK / 32, NW = WAVES_M * WAVES_N;
+    static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 32, TN = WN / 32;
+    static constexpr int STAGE = (BM + BN) * BK;
+    static constexpr int NA = BM * BK / 1024 / NW, NB = BN * BK / 1024 / NW; // blocks a wave loads
+    static_assert(NA >= 1 && NB >= 1, "a wave loads of both operands");
+    static constexpr int PATCH = 16 * WN * 4; // bytes of LDS a wave's outputs turn over in
+    static constexpr int STORES = TM * 2 * (WN / 16); // a wave's stores of a whole tile
 
-    const __amdgpu_buffer_rsrc_t rsA = rows_rsrc(
-        t.A + (long long)t.m0 * p.lda, (long long)(t.M - t.m0 - 1) * p.lda + p.K);
-    const __amdgpu_buffer_rsrc_t rsB = rows_rsrc(
-        t.B + (long long)t.n0 * p.ldb, (long long)(p.N - t.n0 - 1) * p.ldb + p.K);
-    const int chunk = 16 * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+    int lane, wave, wm, wn, chunk, o;
+    int at[KH];
+    // The operands that loads are issued of.
+    const signed char *A, *B;
+    long long bytesA, bytesB;
+    int K;
     uint32_t offA[NA], offB[NB];
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-        offA[i] = (uint32_t)(min(8 * (wave + NW * i) + (lane >> 3), t.M - t.m0 - 1) * p.lda + chunk);
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-        offB[i] = (uint32_t)(min(8 * (wave + NW * i) + (lane >> 3), p.N - t.n0 - 1) * p.ldb + chunk);
+    i32x16 acc[TM][TN];
+    i32x4 fa[2][TM], fb[2][TN]; // of k-groups by parity
+    // What the outputs of the tile are scaled with: lane l holds the wave's
+    // rows l and 64 + l, and the four columns that it stores.
+    float sa[(WM + 63) / 64], sb[4], bias[4];
 
-    typedef __attribute__((address_space(3))) void lds_void;
-    auto issue = [&](int step, int stage) {
+    __device__ __forceinline__ void init()
+    {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        // (Waves that share a SIMD, four apart, lie above one another in M.)
+        wm = (wave / WAVES_N) * WM;
+        wn = (wave % WAVES_N) * WN;
+        chunk = 16 * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+        // This lane's 16 bytes of k-group q (32 bytes of the step) in row 32 i +
+        // l % 32 of the wave's part; 32 rows on is a fixed distance.
+        o = lane & 31;
+#pragma unroll
+        for (int q = 0; q < KH; ++q)
+            at[q] = o * BK + 16 * ((2 * q + (lane >> 5)) ^ ((o >> 1) & 7));
+    }
+
+    __device__ __forceinline__ void operands(const I8Params &p, const I8Tile &t)
+    {
+        A = t.A + (long long)t.m0 * p.lda;
+        B = t.B + (long long)t.n0 * p.ldb;
+        bytesA = (long long)(t.M - t.m0 - 1) * p.lda + p.K;
+        bytesB = (long long)(p.N - t.n0 - 1) * p.ldb + p.K;
+        K = p.K;
+        // (Rows behind the last repeat it; they are not stored.)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            offA[i] = (uint32_t)(min(8 * (wave + NW * i) + (lane >> 3), t.M - t.m0 - 1) * p.lda + chunk);
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            offB[i] = (uint32_t)(min(8 * (wave + NW * i) + (lane >> 3), p.N - t.n0 - 1) * p.ldb + chunk);
+    }
+
+    // The loads of a step into a stage; of zeros for a step past the last.
+    __device__ __forceinline__ void issue(int step, signed char *to) const
+    {
+        typedef __attribute__((address_space(3))) void lds_void;
+        const __amdgpu_buffer_rsrc_t rsA = rows_rsrc(A, bytesA), rsB = rows_rsrc(B, bytesB);
         const int k = step * BK;
-        const uint32_t off = k + chunk < p.K ? 0u : kOutside;
-        signed char *to = lds + stage * STAGE;
+        const uint32_t off = k + chunk < K ? 0u : kOutside;
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -529,25 +570,21 @@ __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *ld
 #pragma unroll
         for (int i = 0; i < NB; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsB, (lds_void *)(to + BM * BK + 1024 * (wave + NW * i)), 16, offB[i] | off, k, 0, 0);
-    };
+                rsB, (lds_void *)(to + BM * BK + 1024 * (wave + NW * i)), 16, offB[i] | off, k, 0,
+                0);
+    }
 
-    // This lane's 16 bytes of k-group q (32 bytes of the step) in row 32 i + l %
-    // 32 of the wave's part; 32 rows on is a fixed distance.
-    const int o = lane & 31;
-    int at[KH];
+    __device__ __forceinline__ void zero()
+    {
 #pragma unroll
-    for (int q = 0; q < KH; ++q)
-        at[q] = o * BK + 16 * ((2 * q + (lane >> 5)) ^ ((o >> 1) & 7));
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = i32x16{};
+    }
 
-    i32x16 acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            acc[i][j] = i32x16{};
-    i32x4 fa[2][TM], fb[2][TN]; // of k-groups by parity
-    auto read = [&](const signed char *stage, int q) {
+    __device__ __forceinline__ void read(const signed char *stage, int q)
+    {
         const signed char *a = stage + wm * BK + at[q], *b = stage + (BM + wn) * BK + at[q];
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -555,137 +592,175 @@ __device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *ld
 #pragma unroll
         for (int j = 0; j < TN; ++j)
             fb[q & 1][j] = *reinterpret_cast<const i32x4 *>(b + 32 * BK * j);
-    };
-    auto products = [&](int q) {
+    }
+
+    __device__ __forceinline__ void products(int q)
+    {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[q & 1][i], fb[q & 1][j],
                                                                   acc[i][j], 0, 0, 0);
-    };
-    auto meet = [&]() { // every wave's loads of the next step are in LDS, its reads of this one done
+    }
+
+    // All but the last k-group of the step in `stage` (whose first one is read).
+    __device__ __forceinline__ void step_front(const signed char *stage)
+    {
+#pragma unroll
+        for (int q = 0; q + 1 < KH; ++q) {
+            read(stage, q + 1);
+            products(q);
+            __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+        }
+    }
+
+    // The last k-group, with the first one of the next step's stage read and
+    // the loads of step `ahead` issued under its products.
+    __device__ __forceinline__ void step_back(const signed char *next, int ahead, signed char *to)
+    {
+        read(next, 0);
+        issue(ahead, to);
+        products(KH - 1);
+        constexpr int GAP = TM * TN / (NA + NB) > 0 ? TM * TN / (NA + NB) : 1;
+        __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+#pragma unroll
+        for (int i = 0; i < NA + NB; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, GAP, 0);
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
         __builtin_amdgcn_sched_barrier(0);
-        asm volatile("" ::: "memory");
-        wait_loads<(STAGES - 2) * (NA + NB)>();
-        __builtin_amdgcn_s_waitcnt(0xc07f); // lgkmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-    };
+    }
+
+    __device__ __forceinline__ int column() const { return wn + 4 * (lane % (WN / 4)); }
+
+    __device__ __forceinline__ void load_scales(const I8Params &p, const I8Tile &t)
+    {
+#pragma unroll
+        for (int x = 0; x < (WM + 63) / 64; ++x)
+            sa[x] = t.sA[min(t.m0 + wm + 64 * x + lane, t.M - 1)];
+        const int n = t.n0 + column();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            sb[e] = t.sB[min(n + e, p.N - 1)];
+            bias[e] = t.bias ? t.bias[min(n + e, p.N - 1)] : 0.0f;
+        }
+    }
+
+    // The wave's outputs, 16 rows at a time through a patch of LDS of its own,
+    // so that a row's leave as 16-byte (fp32) or 8-byte pieces. Rows 4 apart,
+    // which one write instruction holds, are 32 banks apart by the XOR. EDGE:
+    // the tile reaches past M or N.
+    template <typename T, bool EDGE>
+    __device__ __forceinline__ void turn_over(const I8Params &p, const I8Tile &t, float *patch) const
+    {
+        constexpr int PER = WN / 4, RPI = 64 / PER; // lanes a row, rows a store
+        const int r = lane / PER, c = 4 * (lane % PER);
+        const int n = t.n0 + wn + c;
+        const int left = t.M - (t.m0 + wm); // the wave's rows
+        T *out = static_cast<T *>(p.C) + (t.row0 + t.m0 + wm + r) * p.ldc + n;
+        const long long step = (long long)RPI * p.ldc;
+#pragma unroll
+        for (int h = 0; h < 2 * TM; ++h) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                const int row = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    patch[(row * WN + 32 * j + o) ^ (8 * (row & 4))] =
+                        (float)acc[h / 2][j][8 * (h & 1) + v];
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += RPI) {
+                const int row = r0 + r, m = 16 * h + row;
+                f32x4 x = *reinterpret_cast<const f32x4 *>(
+                    patch + ((row * WN + c) ^ (8 * (row & 4))));
+                const float s = __shfl(sa[(16 * h + r0) / 64], m & 63);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = scaled(x[e], s, sb[e], bias[e]);
+                if (!EDGE || (m < left && n + 4 <= p.N)) {
+                    store4(out, x);
+                } else if (m < left) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < p.N)
+                            out[e] = (T)x[e];
+                }
+                out += step;
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+
+    // Returns whether the tile was whole (and its stores one a piece).
+    __device__ __forceinline__ bool outputs(const I8Params &p, const I8Tile &t, float *patch) const
+    {
+        const bool whole = t.m0 + BM <= t.M && t.n0 + BN <= p.N;
+        with_type(p.type, [&](auto type) {
+            if (whole)
+                turn_over<decltype(type), false>(p, t, patch);
+            else
+                turn_over<decltype(type), true>(p, t, patch);
+        });
+        return whole;
+    }
+};
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+__device__ __forceinline__ void i8_large_tile(const I8Params &p, signed char *lds)
+{
+    typedef I8Core<BM, BN, WAVES_M, WAVES_N> Core;
+    constexpr int LOADS = Core::NA + Core::NB;
+    static_assert(STAGES >= 2 && (STAGES - 1) * LOADS <= 63, "loads in flight");
+    static_assert(Core::NW * Core::PATCH <= STAGES * Core::STAGE, "the patches fit in the stages");
+
+    I8Tile t;
+    if (!i8_tile_of<BM, BN>(p, t))
+        return;
+    Core c;
+    c.init();
+    c.operands(p, t);
 
     // Step s in stage s % STAGES: each k-group is read under the products of
     // the one before. Once the last one is read, all meet: the loads of step
     // s + 1 have to be there, those of step s + STAGES take the stage just
     // read, and the first k-group of s + 1 is read under the last products of
     // s. (After the last step this reads zeros.)
-    const int steps = (p.K + BK - 1) / BK;
+    const int steps = (p.K + Core::BK - 1) / Core::BK;
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s)
-        issue(s, s);
-    meet();
-    issue(STAGES - 1, STAGES - 1);
+        c.issue(s, lds + s * Core::STAGE);
+    meet<(STAGES - 2) * LOADS>();
+    c.issue(STAGES - 1, lds + (STAGES - 1) * Core::STAGE);
     int cur = 0;
-    if (t.m0 + wm < t.M) {
-        read(lds, 0);
+    if (t.m0 + c.wm < t.M) {
+        c.zero();
+        c.read(lds, 0);
         for (int s = 0; s < steps; ++s) {
-            const signed char *stage = lds + cur * STAGE;
-#pragma unroll
-            for (int q = 0; q + 1 < KH; ++q) {
-                read(stage, q + 1);
-                products(q);
-                __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
-            }
-            meet();
-            const int next = cur + 1 == STAGES ? 0 : cur + 1;
-            read(lds + next * STAGE, 0);
-            issue(s + STAGES, cur);
-            cur = next;
-            products(KH - 1);
-            constexpr int GAP = TM * TN / (NA + NB) > 0 ? TM * TN / (NA + NB) : 1;
-            __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
-#pragma unroll
-            for (int i = 0; i < NA + NB; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, GAP, 0);
-                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            }
-            __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
-            __builtin_amdgcn_sched_barrier(0);
+            signed char *stage = lds + cur * Core::STAGE;
+            c.step_front(stage);
+            meet<(STAGES - 2) * LOADS>();
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
+            c.step_back(lds + cur * Core::STAGE, s + STAGES, stage);
         }
+        c.load_scales(p, t);
     } else {
         // A wave whose rows all lie behind the group's last only loads, and
         // leaves the matrix unit to the other wave of its SIMD.
         for (int s = 0; s < steps; ++s) {
-            meet();
-            issue(s + STAGES, cur);
+            meet<(STAGES - 2) * LOADS>();
+            c.issue(s + STAGES, lds + cur * Core::STAGE);
             cur = cur + 1 == STAGES ? 0 : cur + 1;
         }
     }
     wait_loads<0>();
     __syncthreads();
-
-    // Each wave turns its part over in an LDS patch of its own, 32 rows at a
-    // time, so that a row's outputs leave as 16-byte (fp32) or 8-byte pieces.
-    constexpr int ROW = WN + 4; // floats; the pad keeps a row's lanes off the next row's banks
-    static_assert(NW * 32 * ROW * 4 <= STAGES * STAGE, "the patches must fit in the stages");
-    float *patch = reinterpret_cast<float *>(lds) + wave * 32 * ROW;
-    constexpr int PER = WN / 4; // lanes a row, four columns each
-    const int c = 4 * (lane % PER), n = t.n0 + wn + c;
-    float sb[4], bias[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        sb[e] = t.sB[min(n + e, p.N - 1)];
-        bias[e] = t.bias ? t.bias[min(n + e, p.N - 1)] : 0.0f;
-    }
-    const int r = lane / PER;
-    // EDGE: the tile reaches past M or N.
-    auto turn_over = [&](auto type, auto edge) {
-        typedef decltype(type) T;
-        constexpr bool EDGE = decltype(edge)::value;
-        T *out = static_cast<T *>(p.C) + (t.row0 + t.m0 + wm + r) * p.ldc + n;
-        const float *sa = t.sA + t.m0 + wm + r;
-        const int left = t.M - (t.m0 + wm + r); // rows from this lane's first one on
-        const long long step = (long long)(64 / PER) * p.ldc;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-#pragma unroll
-            for (int v = 0; v < 16; ++v)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    patch[(8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * ROW + 32 * j + o] =
-                        (float)acc[i][j][v];
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int r0 = 0; r0 < 32; r0 += 64 / PER) {
-                const int m = 32 * i + r0;
-                f32x4 x = *reinterpret_cast<const f32x4 *>(patch + (r0 + r) * ROW + c);
-                if (!EDGE || m < left) {
-                    const float s = sa[m];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[e] = scaled(x[e], s, sb[e], bias[e]);
-                    if (!EDGE || n + 4 <= p.N) {
-                        store4(out, x);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (n + e < p.N)
-                                out[e] = (T)x[e];
-                    }
-                }
-                out += step;
-            }
-            __builtin_amdgcn_wave_barrier();
-        }
-    };
-    const bool whole = t.m0 + BM <= t.M && t.n0 + BN <= p.N;
-    with_type(p.type, [&](auto type) {
-        if (whole)
-            turn_over(type, std::false_type{});
-        else
-            turn_over(type, std::true_type{});
-    });
+    if (t.m0 + c.wm < t.M)
+        c.outputs(p, t, reinterpret_cast<float *>(lds + c.wave * Core::PATCH));
 }
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
