@@ -462,3 +462,31 @@ def test_product_large(env, M, N, K, dtype):
     ([16] * 50 + [0] * 14, 2048, 512), ([2, 9, 0, 31, 1] * 20, 1030, 272), ([1] * 300, 520, 144)])
 def test_grouped_large(env, counts, N, K, dtype):
     large_case(env, sum(counts) + 9, N, K, dtype, counts=counts, first=4, bias=len(counts) % 2 == 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K,counts", [
+    (4001, 8192, 656, None), (8000, 8190, 1024, None), (4100, 16000, 784, None),
+    (0, 8192, 656, [3000, 1, 0, 2000, 255, 257, 500]), (0, 8190, 1040, [256, 512, 1024, 3000, 129]),
+    (0, 4096, 2048, [500] * 16 + [1] * 16)])
+def test_more_tiles_than_compute_units(env, M, N, K, counts, dtype):
+    """Several rounds of 256 x 256 tiles: whole ones, ragged ones, and tiles
+    whose lower waves have no rows."""
+    large_case(env, M or sum(counts) + 9, N, K, dtype, counts=counts, first=4 if counts else 0,
+               bias=N % 4 == 2)
+
+
+def test_large_products_repeat(env):
+    """The same call again and again gives the same bits, with other work on
+    the memory in between."""
+    torch, pg = env
+    M, N, K = 4001, 8192, 1040
+    A = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda")
+    B = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda")
+    sA, sB = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    C = [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pg.i8gemm(M, N, K, A, K, sA, B, K, sB, None, C[0], N)
+    for _ in range(20):
+        C[1].fill_(1.0)
+        pg.i8gemm(M, N, K, A, K, sA, B, K, sB, None, C[1], N)
+        assert torch.equal(C[0], C[1])
