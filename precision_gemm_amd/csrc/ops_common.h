@@ -101,6 +101,23 @@ __device__ __forceinline__ bool find_tile(const int *offsets, int groups, int ro
     return true;
 }
 
+// The group that is `nth` by its number of rows, the most first (equal ones in
+// their order); at most 64 groups, one a lane.
+__device__ __forceinline__ int group_by_size(const int *offsets, int groups, int rows, int nth)
+{
+    const int lane = __lane_id();
+    int lo = 0, hi = -1; // (lanes without a group come last)
+    if (lane < groups)
+        group_rows(offsets, lane, rows, lo, hi);
+    const int own = hi - lo;
+    int before = 0;
+    for (int i = 0; i < groups; ++i) {
+        const int n = __builtin_amdgcn_readlane(own, i);
+        before += n > own || (n == own && i < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < groups && before == nth));
+}
+
 // Workgroup -> (row tile, column tile) of `tiles_m` x `tiles_n`, or false for
 // one too many: consecutive workgroups go round the 8 XCDs, each of which gets
 // a contiguous run of the tiles, ordered in bands of `band` row tiles so that
