@@ -222,7 +222,9 @@ int launch_sort(int slots, int experts, const void *ids_, int *offsets, int *row
 // ---------------------------------------------------------------------------
 // Rows to and from the sorted order. `lanes` (a power of two up to 256)
 // neighbouring threads take one token's row, 16 bytes each at a time, so 256 /
-// lanes tokens share a workgroup. SLOTS slots (a power of two up to 8, as many
+// lanes tokens share a workgroup. A row's last 16 bytes are taken as they lie,
+// over the chunk before them: what both hold is written twice, the same. (A row
+// of fewer bytes goes element by element.) SLOTS slots (a power of two up to 8, as many
 // as topk needs) go together, so that their rows are in flight at once. Rows
 // need no alignment. With WAVE, a token has whole waves, and its slots' rows
 // and weights are scalars.
@@ -286,6 +288,12 @@ __device__ __forceinline__ void slot_weights(const RowParams &p, long long at, i
             w[j] = slot_value<WAVE>(p.weights, at + min(j0 + j, p.topk - 1));
 }
 
+// Where the chunk from byte b on is taken: at the row's end, the last 16 bytes.
+__device__ __forceinline__ int chunk_at(const RowParams &p, int b)
+{
+    return min(b, max(p.bytes - 16, 0));
+}
+
 template <int ES, int SLOTS, bool WAVE>
 __global__ void __launch_bounds__(256) expert_gather_kernel(RowParams p)
 {
@@ -295,7 +303,8 @@ __global__ void __launch_bounds__(256) expert_gather_kernel(RowParams p)
         return;
     const char *x = p.in + t * p.ld_in;
     const long long at = (long long)t * p.topk;
-    for (int b = 16 * lane; b < p.bytes; b += 16 * p.lanes) {
+    for (int b0 = 16 * lane; b0 < p.bytes; b0 += 16 * p.lanes) {
+        const int b = chunk_at(p, b0);
         const bool whole = b + 16 <= p.bytes;
         i32x4 v = {};
         if (whole)
@@ -400,7 +409,8 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(RowParams p)
     if (t >= p.tokens)
         return;
     const long long at = (long long)t * p.topk;
-    for (int b = 16 * lane; b < p.bytes; b += 16 * p.lanes) {
+    for (int b0 = 16 * lane; b0 < p.bytes; b0 += 16 * p.lanes) {
+        const int b = chunk_at(p, b0);
         float sum[VEC] = {};
         for (int j0 = 0; j0 < p.topk; j0 += SLOTS) {
             int r[SLOTS];
@@ -438,17 +448,21 @@ __global__ void __launch_bounds__(256) expert_combine_grad_kernel(RowParams p)
         slot_rows<WAVE>(p, at, j0, r);
         slot_weights<WAVE>(p, at, j0, w);
         if (live) {
-            for (int b = 16 * lane; b < p.bytes; b += 16 * p.lanes) {
+            for (int b0 = 16 * lane; b0 < p.bytes; b0 += 16 * p.lanes) {
+                const int b = chunk_at(p, b0);
+                const int again = (b0 - b) / (int)sizeof(T); // elements of the chunk before
                 float d[VEC];
                 if (p.dweights) {
                     float y[SLOTS][VEC];
                     load_slots<T>(p.in2, p.ld_in2, r, b, p.bytes, y);
                     load_chunk<T>(g, b, p.bytes, d);
+                    // (The elements of the chunk before are counted there.)
 #pragma unroll
                     for (int j = 0; j < SLOTS; ++j)
 #pragma unroll
                         for (int i = 0; i < VEC; ++i)
-                            dot[j] = __builtin_fmaf(d[i], y[j][i], dot[j]);
+                            dot[j] = i < again ? dot[j]
+                                               : __builtin_fmaf(d[i], y[j][i], dot[j]);
                 } else {
                     load_chunk<T>(g, b, p.bytes, d);
                 }

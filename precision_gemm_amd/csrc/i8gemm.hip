@@ -45,19 +45,20 @@ __device__ __forceinline__ void unpack(i32x4 v, float (&x)[16 / sizeof(T)])
         x[i] = (float)h[i];
 }
 
-// NT threads a row (NT = 64: four rows a workgroup, one a wave), which hold
-// the row in registers, CH chunks of 16 bytes each, between its maximum and
+// NT threads a row (below 256: 256 / NT rows a workgroup), which hold the row
+// in registers, CH chunks of 16 bytes each, between its maximum and
 // its rounding: one pass over memory. CH = 0: rows of any length, read twice.
 template <typename T, int NT, int CH>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
 i8_quantize_kernel(int M, int K, const T *X, int ldx, signed char *Q, int ldq, float *scale)
 {
     constexpr int VEC = 16 / sizeof(T);
-    constexpr int ROWS = NT == 64 ? 4 : 1, WAVES = NT / 64;
-    const int t = NT == 64 ? threadIdx.x & 63 : threadIdx.x;
-    const long long m = (long long)blockIdx.x * ROWS + (NT == 64 ? threadIdx.x >> 6 : 0);
+    constexpr int ROWS = NT < 256 ? 256 / NT : 1, WAVES = NT / 64;
+    static_assert(NT <= 64 || ROWS == 1, "a row is a part of a wave, a wave or a workgroup");
+    const int t = threadIdx.x % NT;
+    const long long m = (long long)blockIdx.x * ROWS + threadIdx.x / NT;
     if (m >= M)
-        return; // (whole waves, and with NT > 64 never)
+        return; // (all threads of a row, and with NT > 64 never)
     const T *x = X + m * ldx;
     signed char *q = Q + m * ldq;
 
@@ -93,7 +94,7 @@ i8_quantize_kernel(int M, int K, const T *X, int ldx, signed char *Q, int ldq, f
         }
     }
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
+    for (int d = 1; d < (NT < 64 ? NT : 64); d <<= 1)
         peak = max(peak, (uint32_t)__shfl_xor((int)peak, d));
     if constexpr (WAVES > 1) {
         __shared__ uint32_t peaks[WAVES];
@@ -156,7 +157,16 @@ int launch_quantize(int M, int K, const void *X, int ldx, signed char *Q, int ld
     const long long chunks = ceil_div_ll(K, VEC);
     Fn fn;
     int threads = 256, rows = 1;
-    if (chunks <= 64) {
+    if (chunks <= 8) {
+        fn = i8_quantize_kernel<T, 8, 1>;
+        rows = 32;
+    } else if (chunks <= 16) {
+        fn = i8_quantize_kernel<T, 16, 1>;
+        rows = 16;
+    } else if (chunks <= 32) {
+        fn = i8_quantize_kernel<T, 32, 1>;
+        rows = 8;
+    } else if (chunks <= 64) {
         fn = i8_quantize_kernel<T, 64, 1>;
         rows = 4;
     } else if (chunks <= 256) {
@@ -288,79 +298,121 @@ __device__ __forceinline__ void store4(T *c, f32x4 x)
 }
 
 // 16 bytes of a row from its byte k on, zeros from byte K on; nothing outside
-// the row's K bytes is read.
+// the row's K bytes is read. The chunk that K ends in comes from the row's last
+// 16 bytes, moved down.
 __device__ __forceinline__ i32x4 row_chunk(const signed char *row, int k, int K)
 {
     if (k + 16 <= K)
         return load16(row + k);
+    if (k >= K)
+        return i32x4{0, 0, 0, 0};
+    if (K >= 16) {
+        const int n = k + 16 - K; // 1 to 15 bytes down
+        i32x4 v = load16(row + K - 16);
+        if (n & 4)
+            v = i32x4{v[1], v[2], v[3], 0};
+        if (n & 8)
+            v = i32x4{v[2], v[3], 0, 0};
+        return i32x4{(int)__builtin_amdgcn_alignbyte(v[1], v[0], n & 3),
+                     (int)__builtin_amdgcn_alignbyte(v[2], v[1], n & 3),
+                     (int)__builtin_amdgcn_alignbyte(v[3], v[2], n & 3),
+                     (int)__builtin_amdgcn_alignbyte(0, v[3], n & 3)};
+    }
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 15; ++i)
         if (k + i < K)
             w[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
     return i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
 }
 
-// The tile for every call: 64 x 64 of C by four waves, each one 32 x 32
-// accumulator of v_mfma_i32_32x32x32_i8 (lane l supplies 16 bytes of row
+// The tile for every alignment: 64 T x 64 T of C by four waves, each one T x T
+// accumulators of v_mfma_i32_32x32x32_i8 (lane l supplies 16 bytes of row
 // l % 32 from k = 16 (l / 32) on; register v of lane l holds row 8 (v / 4) +
 // 4 (l / 32) + v % 4, column l % 32). 64-byte K-steps go through registers to
 // LDS, so any alignment and any K will do, and zeros behind K leave the sum as
 // it is. LDS rows are 64 bytes, four of them one sweep of the 64 banks, so the
 // 16-byte chunk index is XORed with row / 4 for conflict-free reads. Rows
 // behind M or N repeat the last one and are not stored.
+template <int T>
 __global__ void __launch_bounds__(256) i8_tile_kernel(I8Params p)
 {
-    constexpr int BM = 64, BN = 64, BK = 64;
-    __shared__ __attribute__((aligned(16))) signed char lds[2][2][64 * BK];
+    constexpr int BM = 64 * T, BN = 64 * T, BK = 64;
+    __shared__ __attribute__((aligned(16))) signed char lds[2][2][BM * BK];
     I8Tile t;
     if (!i8_tile_of<BM, BN>(p, t))
         return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int r = tid >> 2, c = tid & 3;
-    const signed char *ra = t.A + (long long)min(t.m0 + r, t.M - 1) * p.lda;
-    const signed char *rb = t.B + (long long)min(t.n0 + r, p.N - 1) * p.ldb;
-    const int at = r * BK + 16 * (c ^ ((r >> 2) & 3));
-    const int wm = 32 * (wave & 1), wn = 32 * (wave >> 1);
-
-    i32x16 acc = {};
-    const int steps = (p.K + BK - 1) / BK;
-    i32x4 va = {}, vb = {};
-    if (steps > 0) {
-        va = row_chunk(ra, 16 * c, p.K);
-        vb = row_chunk(rb, 16 * c, p.K);
+    const signed char *ra[T], *rb[T];
+#pragma unroll
+    for (int x = 0; x < T; ++x) {
+        ra[x] = t.A + (long long)min(t.m0 + 64 * x + r, t.M - 1) * p.lda;
+        rb[x] = t.B + (long long)min(t.n0 + 64 * x + r, p.N - 1) * p.ldb;
     }
+    const int at = r * BK + 16 * (c ^ ((r >> 2) & 3)); // (64 rows on: the same chunk)
+    const int wm = 32 * T * (wave & 1), wn = 32 * T * (wave >> 1);
+
+    i32x16 acc[T][T] = {};
+    const int steps = (p.K + BK - 1) / BK;
+    i32x4 va[T] = {}, vb[T] = {};
+    auto load = [&](int k) {
+#pragma unroll
+        for (int x = 0; x < T; ++x) {
+            va[x] = row_chunk(ra[x], k + 16 * c, p.K);
+            vb[x] = row_chunk(rb[x], k + 16 * c, p.K);
+        }
+    };
+    if (steps > 0)
+        load(0);
     for (int s = 0; s < steps; ++s) {
         signed char *la = lds[s & 1][0], *lb = lds[s & 1][1];
-        *reinterpret_cast<i32x4 *>(la + at) = va;
-        *reinterpret_cast<i32x4 *>(lb + at) = vb;
-        __syncthreads();
-        if (s + 1 < steps) {
-            va = row_chunk(ra, (s + 1) * BK + 16 * c, p.K);
-            vb = row_chunk(rb, (s + 1) * BK + 16 * c, p.K);
+#pragma unroll
+        for (int x = 0; x < T; ++x) {
+            *reinterpret_cast<i32x4 *>(la + at + 64 * BK * x) = va[x];
+            *reinterpret_cast<i32x4 *>(lb + at + 64 * BK * x) = vb[x];
         }
+        __syncthreads();
+        if (s + 1 < steps)
+            load((s + 1) * BK);
 #pragma unroll
         for (int q = 0; q < BK / 32; ++q) {
-            const int o = lane & 31, ch = 2 * q + (lane >> 5);
-            const i32x4 fa = *reinterpret_cast<const i32x4 *>(
-                la + (wm + o) * BK + 16 * (ch ^ (((wm + o) >> 2) & 3)));
-            const i32x4 fb = *reinterpret_cast<const i32x4 *>(
-                lb + (wn + o) * BK + 16 * (ch ^ (((wn + o) >> 2) & 3)));
-            acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa, fb, acc, 0, 0, 0);
+            const int o = lane & 31, ch = 16 * ((2 * q + (lane >> 5)) ^ ((o >> 2) & 3));
+            i32x4 fa[T], fb[T];
+#pragma unroll
+            for (int x = 0; x < T; ++x) {
+                fa[x] = *reinterpret_cast<const i32x4 *>(la + (wm + 32 * x + o) * BK + ch);
+                fb[x] = *reinterpret_cast<const i32x4 *>(lb + (wn + 32 * x + o) * BK + ch);
+            }
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int j = 0; j < T; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0,
+                                                                      0, 0);
         }
         // (The next step writes the other stage, which every wave left before
         // this step's barrier.)
     }
-    const int n = t.n0 + wn + (lane & 31);
-    if (n >= p.N)
-        return;
-    const float sb = t.sB[n], bias = t.bias ? t.bias[n] : 0.0f;
+    with_type(p.type, [&](auto type) {
+        typedef decltype(type) C;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-        const int m = t.m0 + wm + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-        if (m < t.M)
-            store_c(p, (t.row0 + m) * p.ldc + n, scaled((float)acc[v], t.sA[m], sb, bias));
-    }
+        for (int j = 0; j < T; ++j) {
+            const int n = t.n0 + wn + 32 * j + (lane & 31);
+            if (n >= p.N)
+                continue;
+            const float sb = t.sB[n], bias = t.bias ? t.bias[n] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int m = t.m0 + wm + 32 * i + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+                    if (m < t.M)
+                        static_cast<C *>(p.C)[(t.row0 + m) * p.ldc + n] =
+                            (C)scaled((float)acc[i][j][v], t.sA[m], sb, bias);
+                }
+        }
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -387,10 +439,10 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
     const signed char *ra[MT], *rb[NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        ra[i] = t.A + (long long)min(t.m0 + 16 * i + r, t.M - 1) * p.lda + kq;
+        ra[i] = t.A + (long long)min(t.m0 + 16 * i + r, t.M - 1) * p.lda;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-        rb[j] = t.B + (long long)min(t.n0 + 16 * j + r, p.N - 1) * p.ldb + kq;
+        rb[j] = t.B + (long long)min(t.n0 + 16 * j + r, p.N - 1) * p.ldb;
 
     i32x4 acc[MT][NT] = {};
     auto products = [&](const i32x4 (&fa)[MT], const i32x4 (&fb)[NT]) {
@@ -407,12 +459,12 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                fb[u][j] = load16(rb[j] + k + 64 * u);
+                fb[u][j] = load16(rb[j] + kq + k + 64 * u);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                fa[u][i] = load16(ra[i] + k + 64 * u);
+                fa[u][i] = load16(ra[i] + kq + k + 64 * u);
 #pragma unroll
         for (int u = 0; u < U; ++u)
             products(fa[u], fb[u]);
@@ -422,10 +474,10 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
         i32x4 fb[NT], fa[MT];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-            fb[j] = row_chunk(rb[j] + q, 0, p.K - q - kq);
+            fb[j] = row_chunk(rb[j], q + kq, p.K);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-            fa[i] = row_chunk(ra[i] + q, 0, p.K - q - kq);
+            fa[i] = row_chunk(ra[i], q + kq, p.K);
         products(fa, fb);
     }
 #pragma unroll
@@ -860,19 +912,23 @@ I8Variant choose_i8(const I8Params &p, int cus)
         if (m32 * ceil_div_ll(p.N, 64) <= cus && p.M <= 32)
             return {i8_stream_kernel<2, 4, 4, 2>, 32, 64, 256};
     }
+    const double used = p.groups < p.M ? p.groups : p.M;
+    // Row tiles: of groups, every one's own and half a tile more, since only
+    // the device knows their rows.
+    auto row_tiles = [&](int bm) {
+        if (!p.groups)
+            return (double)ceil_div_ll(p.M, bm);
+        const double each = (double)p.M / p.groups / bm + 0.5;
+        return used * (each > 1.0 ? each : 1.0);
+    };
     if (!direct)
-        return {i8_tile_kernel, 64, 64, 256};
+        return row_tiles(128) * (double)ceil_div_ll(p.N, 128) >= cus
+                   ? I8Variant{i8_tile_kernel<2>, 128, 128, 256}
+                   : I8Variant{i8_tile_kernel<1>, 64, 64, 256};
     const I8Large *best = nullptr;
     float least = 0.0f;
     for (const I8Large &l : kLarge) {
-        // Row tiles: of groups, every one's own and half a tile more, since
-        // only the device knows their rows.
-        double rows = (double)ceil_div_ll(p.M, l.v.bm);
-        if (p.groups) {
-            const double each = (double)p.M / p.groups / l.v.bm + 0.5;
-            rows = (p.groups < p.M ? p.groups : p.M) * (each > 1.0 ? each : 1.0);
-        }
-        const double tiles = rows * (double)ceil_div_ll(p.N, l.v.bn);
+        const double tiles = row_tiles(l.v.bm) * (double)ceil_div_ll(p.N, l.v.bn);
         if (l.one_round && tiles > cus)
             continue;
         const float rounds = (float)ceil_div_ll((long long)(tiles + 0.999), cus);
