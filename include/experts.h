@@ -16,14 +16,19 @@
  * neither read nor written. All pointers are DEVICE pointers owned by the
  * caller. Calls are asynchronous on `stream`, never synchronise the host,
  * allocate nothing, use no floating-point atomics and are deterministic. They
- * launch on the current device, which has to be the stream's. Entries of
- * row_of_slot outside [0, tokens*topk) count as -1.
+ * launch on the current device, which has to be the stream's. Outputs must not
+ * overlap inputs. Matrices need no alignment beyond their elements'. Entries of
+ * row_of_slot outside [0, tokens*topk) count as -1; the others have to differ
+ * from each other, as expert_sort makes them, where rows are written
+ * (expert_gather, expert_combine_grad).
  *
  * tokens*topk is at most 2^31 - 1. Status codes: 0 success, a positive
  * hipError_t, or minus (a base for the call + the position of the first
  * invalid argument): 400 for expert_sort, 500 for expert_gather, 600 for
- * expert_combine, 700 for expert_combine_grad. Nothing is launched on error.
- * sgemm_status_string() gives the message.
+ * expert_combine, 700 for expert_combine_grad; -22 for more rows than a launch
+ * holds (over 2^23 tokens with rows of more than 2048 bytes, twice as many for
+ * each halving of that). Nothing is launched on error. sgemm_status_string()
+ * gives the message.
  */
 #ifndef PRECISION_GEMM_AMD_EXPERTS_H
 #define PRECISION_GEMM_AMD_EXPERTS_H
@@ -80,8 +85,7 @@ int expert_combine(int tokens, int topk, int cols, const void *Y, int type, int 
  *   dY[r, :] = weights[t*topk + j] * dout[t, :]          (rounded once)
  *   dweights[t*topk + j] = sum_h dout[t, h] * Y[r, h]    (in fp32)
  * and dweights = 0 for a slot without. dweights may be NULL (Y is not read
- * then and may be NULL too); weights may be NULL, as above. dY must not
- * overlap Y.
+ * then and may be NULL too); weights may be NULL, as above.
  * Positions: tokens 1, topk 2, cols 3, dout 4, type 5, ldo 6, Y 7, ldy 8,
  * row_of_slot 9, weights 10, dY 11, lddy 12, dweights 13.
  */

@@ -15,17 +15,18 @@
  *
  * Ownership, execution (asynchronous on `stream`, no host synchronisation, no
  * allocation, deterministic) and thread safety are those of sgemm.h. The calls
- * launch on the current device, which has to be the stream's.
+ * launch on the current device, which has to be the stream's. Outputs must not
+ * overlap inputs.
  *
- * Alignment: none is required. Rows that start on 16-byte boundaries (A and B
- * 16-byte aligned, lda, ldb and strideB multiples of 16) with K a multiple of
- * 16 run the fast kernels.
+ * Alignment: none is required beyond the element types' own. Rows that start on
+ * 16-byte boundaries (A and B 16-byte aligned, lda, ldb and strideB multiples of
+ * 16) with K a multiple of 16 and lda and ldb below 2^22 run the fast kernels.
  *
  * Status codes: 0 success, a positive hipError_t, or minus (a base for the
  * call + the position of the first invalid argument): 100 for
  * i8_quantize_rows, 200 for i8gemm, 300 for i8gemm_grouped; e.g. -205 is a bad
- * lda of i8gemm. Nothing is launched on error. sgemm_status_string() gives the
- * message.
+ * lda of i8gemm; -22 for a product of more output tiles than a launch holds.
+ * Nothing is launched on error. sgemm_status_string() gives the message.
  */
 #ifndef PRECISION_GEMM_AMD_I8GEMM_H
 #define PRECISION_GEMM_AMD_I8GEMM_H

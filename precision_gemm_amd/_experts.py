@@ -56,8 +56,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _lib = None  # the loaded library, set by declare()
 
 
+_INT_MAX = 2**31 - 1  # sizes and leading dimensions are C ints
+
+
 def _span(rows, cols, ld):
     """Elements from the first to the last of `rows` rows, `ld` apart."""
+    if rows > _INT_MAX or cols > _INT_MAX or ld > _INT_MAX:
+        raise ValueError(f"{rows} rows of {cols}, {ld} apart: sizes are below 2**31")
     return (rows - 1) * ld + cols if rows > 0 and cols > 0 else 0
 
 

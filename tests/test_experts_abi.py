@@ -167,3 +167,16 @@ def test_binding_refuses_host_tensors(pg):
         pg.expert_sort(4, 1, 4, s, s, s, None)
     with pytest.raises(TypeError, match="offsets must be a GPU tensor"):
         pg.sgemm_grouped(0, 4, 4, 4, 1, s, 1.0, x, 4, x, 4, 16, 0.0, x, 4)
+
+
+def test_binding_refuses_sizes_beyond_an_int(pg):
+    """2^32 + 4 would reach the library as 4."""
+    torch = pytest.importorskip("torch")
+    from precision_gemm_amd import _experts
+    for rows, cols, ld in ((2**32 + 4, 4, 4), (4, 2**31, 2**31), (4, 4, 2**31)):
+        with pytest.raises(ValueError, match="below 2"):
+            _experts._span(rows, cols, ld)
+        with pytest.raises(ValueError, match="below 2"):
+            _experts._spans(2, 16, rows, cols, ld)
+    assert _experts._span(3, 4, 5) == 14 and _experts._span(0, 4, 5) == 0
+    assert _experts._spans(2, 100, 3, 4, 5) == 114 and torch is not None

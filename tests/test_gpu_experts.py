@@ -297,6 +297,18 @@ def test_nan_stays_in_its_token(env):
     assert (out[1] == 2).all() and (out[2] == 1).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,topk,cols", [(300, 4, 2047), (50, 3, 1030), (2000, 2, 9),
+                                              (20, 16, 515), (6, 64, 130), (33, 1, 2049)])
+def test_rows_that_end_anywhere(env, tokens, topk, cols, dtype):
+    """Rows whose last 16 bytes overlap the chunk before them: every element
+    counted once, from unaligned rows too."""
+    for pad, shift in ((0, 0), (1, 1), (2, 5)):
+        test_gather(env, tokens, topk, cols, 11, dtype, pad, shift)
+        test_combine(env, tokens, topk, cols, 11, dtype, pad, shift, True)
+        test_combine_grad(env, tokens, topk, cols, 11, dtype, pad, shift, True)
+
+
 def test_rows_outside_the_range_count_as_absent(env):
     torch, pg = env
     rows = torch.tensor([[0, 4], [2**31 - 1, 1]], dtype=torch.int32, device="cuda")

@@ -414,6 +414,27 @@ def test_other_stream_and_graph(env):
         assert all(torch.equal(a, b) for a, b in zip(eager, captured)), rep
 
 
+@pytest.mark.parametrize("M,N", [(1, 40), (16, 70), (20, 64), (60, 2000), (500, 300)])
+def test_products_without_k(env, M, N):
+    """K = 0: the bias, or 0; A and B are not read."""
+    product_case(env, M, N, 0, "bfloat16", bias=True)
+    product_case(env, M, N, 0, "float32", counts=[M - 1, 0, 1], bias=True)
+    torch, pg = env
+    s, c = torch.ones(M + N, device="cuda"), torch.full((M, N), 3.0, device="cuda")
+    e = torch.empty(0, dtype=torch.int8, device="cuda")
+    pg.i8gemm(M, N, 0, e, 1, s, e, 1, s, None, c, N)
+    assert (c == 0).all()
+
+
+@pytest.mark.parametrize("K", list(range(1, 50)) + [63, 65, 79, 81, 127, 129, 143, 145])
+def test_row_ends(env, K):
+    """Rows that end anywhere in a 16-byte chunk, with other bytes behind them
+    and at every alignment, through each kernel that takes them."""
+    for M, N in ((1, 33), (40, 40), (70, 150)):
+        product_case(env, M, N, K, "float32", lda=K + K % 7, ldb=K + 3, shift=K % 16)
+    product_case(env, 2000, 2100, K, "bfloat16", lda=K + 1, ldb=K + 2, shift=5)
+
+
 # --- large products: every tile of the dispatch, against 64-bit products on the GPU -------------
 
 
