@@ -20,7 +20,8 @@ namespace {
 // consecutive part of the run, then number their slots: a slot's row is its
 // expert's next row for the wave plus the lanes before it with the same
 // expert. Every count is an integer sum, so the order in which workgroups run
-// changes nothing.
+// changes nothing. The sort moves 8 bytes a slot, so latencies bound it: 256
+// slots take 4 us, 65536 of 64 experts 8.4 us, 2097152 24 us.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -227,7 +228,10 @@ int launch_sort(int slots, int experts, const void *ids_, int *offsets, int *row
 // of fewer bytes goes element by element.) SLOTS slots (a power of two up to 8, as many
 // as topk needs) go together, so that their rows are in flight at once. Rows
 // need no alignment. With WAVE, a token has whole waves, and its slots' rows
-// and weights are scalars.
+// and weights are scalars. Bound by memory: 16384 tokens x 4 of 2048 bf16 move
+// at 5.0 TB/s (gather, 67 us), 5.1 (sum, 65 us) and 4.7 (gradients, 127 us);
+// with a slot's row fetched after the one before it the sum took 94 us and the
+// gradients of 8192 x 8 slots 131 (114 so).
 // ---------------------------------------------------------------------------
 struct RowParams {
     const char *in;      // X or dout, or Y of the sum

@@ -46,8 +46,12 @@ __device__ __forceinline__ void unpack(i32x4 v, float (&x)[16 / sizeof(T)])
 }
 
 // NT threads a row (below 256: 256 / NT rows a workgroup), which hold the row
-// in registers, CH chunks of 16 bytes each, between its maximum and
-// its rounding: one pass over memory. CH = 0: rows of any length, read twice.
+// in registers, CH chunks of 16 bytes each, between its maximum and its
+// rounding: one pass over memory. CH = 0: rows of any length, read twice.
+// Bound by memory: 16384 x 4092 in fp32 takes 62 us (5.4 TB/s, a large copy's
+// rate), 16384 x 4096 in bf16 40 us (5.1); 4 x 4096 takes 3.7 us, a launch and
+// one trip to memory. Rows of up to 1 KiB share a wave or a part of one
+// (1000000 x 40 fp16: 42 us, 315 with a wave each).
 template <typename T, int NT, int CH>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
 i8_quantize_kernel(int M, int K, const T *X, int ldx, signed char *Q, int ldq, float *scale)
@@ -516,11 +520,12 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
 // same at every wait. Needs 16-byte-aligned rows, K a multiple of 16 and
 // leading dimensions below 2^22 (32-bit offsets within a tile).
 //
-// What bounds the 256 x 256 tile: power. On 8192^3 it runs at 2.33 POP/s where
-// the library product makes 2.11; without its loads the loop takes 17 % less,
-// without its LDS reads 18 %, on operands of zeros 30 %, and the clock stands
-// at 1.8 GHz. Eight waves of 128 x 64 each beat four of 128 x 128 (4001 x 8192
-// x 4096: 132 us against 144), whose outputs leave one wave a SIMD idle.
+// What bounds the 256 x 256 tile: power. On 8192^3 it runs at 2.50 POP/s (441
+// us), where the library product makes 2.11; the matrix units are busy 55 % of
+// the cycles of a clock that stands at 1.8 GHz. Without its loads the loop takes
+// 17 % less, without its LDS reads 18 %, and on operands of zeros 30 %. Eight
+// waves of 128 x 64 each beat four of 128 x 128 (4001 x 8192 x 4096: 132 us
+// against 144), whose outputs leave one wave a SIMD idle.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kOutside = 0x80000000u;
 constexpr int kMaxTileLd = 1 << 22;
@@ -866,8 +871,8 @@ const I8Large kLarge[] = {
     {{i8_large_kernel<64, 64, 2, 2, 3>, 64, 64, 256}, 0.33f, 4.0f, false},
     {{i8_large_kernel<64, 128, 2, 2, 3>, 64, 128, 256}, 0.45f, 4.5f, false},
     {{i8_large_kernel<128, 128, 2, 4, 4>, 128, 128, 512}, 0.70f, 5.0f, false},
-    {{i8_large_kernel<128, 256, 2, 4, 3>, 128, 256, 512}, 1.10f, 7.0f, false},
-    {{i8_large_kernel<256, 256, 2, 4, 2>, 256, 256, 512}, 1.85f, 10.0f, false},
+    {{i8_large_kernel<128, 256, 2, 4, 3>, 128, 256, 512}, 1.10f, 6.5f, false},
+    {{i8_large_kernel<256, 256, 2, 4, 2>, 256, 256, 512}, 1.85f, 8.0f, false},
 };
 
 // The kernel of a call. Times below are graph replays over weights that no
