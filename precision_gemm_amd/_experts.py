@@ -224,10 +224,10 @@ def sgemm_grouped(transB, M, N, K, groups, offsets, alpha, A, lda, B, ldb, strid
     d = _first("offsets", offsets)
     rows, cols = (N, K) if transB else (K, N)
     return _call(_lib.sgemm_grouped, d, stream, check, int(transB), M, N, K, groups,
-                 _at("offsets", offsets, _I32, d, groups + 1), alpha,
+                 _at("offsets", offsets, _I32, d, groups + 1), float(alpha),
                  _at("A", A, _F32, d, _span(M, K, lda)), lda,
                  _at("B", B, _F32, d, _spans(groups, strideB, rows, cols, ldb)), ldb, strideB,
-                 beta, _at("C", C, _F32, d, _span(M, N, ldc)), ldc)
+                 float(beta), _at("C", C, _F32, d, _span(M, N, ldc)), ldc)
 
 
 def sgemm_grouped_outer(M, N, K, groups, offsets, alpha, A, lda, B, ldb, beta, C, ldc, strideC,
@@ -236,7 +236,7 @@ def sgemm_grouped_outer(M, N, K, groups, offsets, alpha, A, lda, B, ldb, beta, C
     rows offsets[g] <= k < offsets[g + 1] of A (K x M) and B (K x N)."""
     d = _first("offsets", offsets)
     return _call(_lib.sgemm_grouped_outer, d, stream, check, M, N, K, groups,
-                 _at("offsets", offsets, _I32, d, groups + 1), alpha,
+                 _at("offsets", offsets, _I32, d, groups + 1), float(alpha),
                  _at("A", A, _F32, d, _span(K, M, lda)), lda,
-                 _at("B", B, _F32, d, _span(K, N, ldb)), ldb, beta,
+                 _at("B", B, _F32, d, _span(K, N, ldb)), ldb, float(beta),
                  _at("C", C, _F32, d, _spans(groups, strideC, M, N, ldc)), ldc, strideC)

@@ -419,6 +419,31 @@ __global__ void __launch_bounds__(256) i8_tile_kernel(I8Params p)
     });
 }
 
+// 16 bytes from any address by two aligned loads and a shift, for streams of
+// unaligned rows, whose bytes come slowly by unaligned loads. Reads the aligned
+// 16 bytes around the first and the last byte.
+__device__ __forceinline__ i32x4 load16_shifted(const signed char *p)
+{
+    const uint32_t s = (uint32_t)(uintptr_t)p & 15u;
+    const signed char *q = p - s;
+    const i32x4 a = *reinterpret_cast<const i32x4 *>(q);
+    const i32x4 b = *reinterpret_cast<const i32x4 *>(q + (s ? 16 : 0));
+    int w[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    if (s & 4)
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            w[i] = w[i + 1];
+    if (s & 8)
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            w[i] = w[i + 2];
+    i32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = (int)__builtin_amdgcn_alignbyte(w[i + 1], w[i], s & 3);
+    return r;
+}
+
 // ---------------------------------------------------------------------------
 // Few rows: the weights' bytes bound the call, so they go from memory straight
 // into the matrix instructions' registers, once, and no LDS stage stands
@@ -427,9 +452,11 @@ __global__ void __launch_bounds__(256) i8_tile_kernel(I8Params p)
 // flight at once, and their exact integer sums are added in LDS.
 // v_mfma_i32_16x16x64_i8: lane l supplies 16 bytes of row l % 16 from k =
 // 16 (l / 16) on; register v of lane l holds row 4 (l / 16) + v, column l % 16.
-// Rows behind the last repeat it and are not stored.
+// Rows behind the last repeat it and are not stored. ALIGNED: rows start on
+// 16-byte boundaries; otherwise load16_shifted, inside the row (256 rows over
+// 64 groups, N = 2048: K = 2048 46 us, K = 2047 78, by unaligned loads 141).
 // ---------------------------------------------------------------------------
-template <int MT, int NT, int WAVES, int U>
+template <int MT, int NT, int WAVES, int U, bool ALIGNED>
 __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
 {
     constexpr int BM = 16 * MT, BN = 16 * NT;
@@ -456,33 +483,38 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
             for (int j = 0; j < NT; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
     };
-    int k = wave * 64 * U;
-    for (; k + 64 * U <= p.K; k += WAVES * 64 * U) {
-        i32x4 fb[U][NT], fa[U][MT];
+    for (int k = wave * 64 * U; k < p.K; k += WAVES * 64 * U) {
+        if (ALIGNED ? k + 64 * U <= p.K : k >= 16 && k + 64 * U + 16 <= p.K) {
+            i32x4 fb[U][NT], fa[U][MT];
+            auto load = [&](const signed char *x) {
+                return ALIGNED ? load16(x) : load16_shifted(x);
+            };
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    fb[u][j] = load(rb[j] + kq + k + 64 * u);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    fa[u][i] = load(ra[i] + kq + k + 64 * u);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                products(fa[u], fb[u]);
+            continue;
+        }
+        // The block at a row's end (or, unaligned, its start).
+        for (int q = k; q < p.K && q < k + 64 * U; q += 64) {
+            i32x4 fb[NT], fa[MT];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                fb[u][j] = load16(rb[j] + kq + k + 64 * u);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
+                fb[j] = row_chunk(rb[j], q + kq, p.K);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                fa[u][i] = load16(ra[i] + kq + k + 64 * u);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            products(fa[u], fb[u]);
-    }
-    // The block that K ends in (one wave's).
-    for (int q = k; q < p.K && q < k + 64 * U; q += 64) {
-        i32x4 fb[NT], fa[MT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            fb[j] = row_chunk(rb[j], q + kq, p.K);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-            fa[i] = row_chunk(ra[i], q + kq, p.K);
-        products(fa, fb);
+                fa[i] = row_chunk(ra[i], q + kq, p.K);
+            products(fa, fb);
+        }
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -856,6 +888,14 @@ struct I8Variant {
     int bm, bn, threads;
 };
 
+template <int MT, int NT, int WAVES, int U>
+I8Variant stream_variant(bool aligned)
+{
+    return {aligned ? i8_stream_kernel<MT, NT, WAVES, U, true>
+                    : i8_stream_kernel<MT, NT, WAVES, U, false>,
+            16 * MT, 16 * NT, 64 * WAVES};
+}
+
 // The tiles that load straight into LDS, with what they cost on 256 CUs
 // (measured, us): `step` for 128 bytes of K of one tile a CU, `fixed` for the
 // launch, the first loads and the outputs. `one_round`: only where every CU
@@ -879,9 +919,10 @@ const I8Large kLarge[] = {
 // cache holds.
 I8Variant choose_i8(const I8Params &p, int cus)
 {
-    const bool direct = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.lda % 16 == 0 &&
-                        p.ldb % 16 == 0 && p.strideB % 16 == 0 && p.K % 16 == 0 &&
-                        p.lda < kMaxTileLd && p.ldb < kMaxTileLd && p.K > 0;
+    const bool aligned = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.lda % 16 == 0 &&
+                         p.ldb % 16 == 0 && p.strideB % 16 == 0;
+    const bool direct =
+        aligned && p.K % 16 == 0 && p.lda < kMaxTileLd && p.ldb < kMaxTileLd && p.K > 0;
     const long long n16 = ceil_div_ll(p.N, 16);
     if (p.groups) {
         // Up to 8 rows a group on average: the weights stream (256 rows over
@@ -889,7 +930,7 @@ I8Variant choose_i8(const I8Params &p, int cus)
         // 512 over 128, 4096 x 1024: 96 against 102; with 16 rows a group 76
         // against 58).
         if (p.M <= 8LL * p.groups || (!direct && p.M <= 16LL * p.groups))
-            return {i8_stream_kernel<1, 2, 4, 2>, 16, 32, 256};
+            return stream_variant<1, 2, 4, 2>(aligned);
     } else if (p.M <= 16) {
         // One row tile: 16 channels a workgroup, K over 8 waves, or 16 for a
         // token or a few over a deep K (1 x 4096 x 16384: 14.7 us against
@@ -898,12 +939,11 @@ I8Variant choose_i8(const I8Params &p, int cus)
         // 17.9 us against 19.1; one row 17.0 against 17.1, 28672 channels 26.8
         // against 23.7).
         if (p.M <= 4)
-            return p.K >= 4096 && n16 <= 2LL * cus
-                       ? I8Variant{i8_stream_kernel<1, 1, 16, 2>, 16, 16, 1024}
-                       : I8Variant{i8_stream_kernel<1, 1, 8, 2>, 16, 16, 512};
+            return p.K >= 4096 && n16 <= 2LL * cus ? stream_variant<1, 1, 16, 2>(aligned)
+                                                   : stream_variant<1, 1, 8, 2>(aligned);
         if (n16 >= 4LL * cus)
-            return {i8_stream_kernel<1, 2, 4, 2>, 16, 32, 256};
-        return {i8_stream_kernel<1, 1, 8, 2>, 16, 16, 512};
+            return stream_variant<1, 2, 4, 2>(aligned);
+        return stream_variant<1, 1, 8, 2>(aligned);
     } else {
         // Row tiles of 32 as long as every CU gets one workgroup at most: 16,
         // 32 or 64 channels (64 x 1024 x 4096: 7.9 us, the 32 x 64 tile 10.0;
@@ -911,11 +951,11 @@ I8Variant choose_i8(const I8Params &p, int cus)
         // the 64 x 64 tile; 128 x 4096 x 4096, two a CU: 17.8 and 11.8).
         const long long m32 = ceil_div_ll(p.M, 32);
         if (m32 * n16 <= cus)
-            return {i8_stream_kernel<2, 1, 8, 2>, 32, 16, 512};
+            return stream_variant<2, 1, 8, 2>(aligned);
         if (m32 * ceil_div_ll(p.N, 32) <= cus)
-            return {i8_stream_kernel<2, 2, 8, 2>, 32, 32, 512};
+            return stream_variant<2, 2, 8, 2>(aligned);
         if (m32 * ceil_div_ll(p.N, 64) <= cus && p.M <= 32)
-            return {i8_stream_kernel<2, 4, 4, 2>, 32, 64, 256};
+            return stream_variant<2, 4, 4, 2>(aligned);
     }
     const double used = p.groups < p.M ? p.groups : p.M;
     // Row tiles: of groups, every one's own and half a tile more, since only

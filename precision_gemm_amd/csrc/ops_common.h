@@ -55,8 +55,9 @@ __device__ __forceinline__ bool find_tile(const int *offsets, int groups, int ro
                                           int &m_out)
 {
     const int lane = __lane_id();
-    const int per = (groups + 63) >> 6;
-    const int g0 = lane * per, g1 = min(g0 + per, groups);
+    const unsigned per = ((unsigned)groups + 63u) >> 6;
+    const int g0 = (int)min(lane * per, (unsigned)groups);
+    const int g1 = (int)min(g0 + per, (unsigned)groups);
     int tiles = 0;
     for (int g = g0; g < g1; ++g) {
         int lo, hi;

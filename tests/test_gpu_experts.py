@@ -485,6 +485,42 @@ def test_sgemm_grouped_outer_without_product(env, alpha, beta):
     outer_case(env, [0, 0], 40, 20, 0, 2, alpha=1.0, beta=beta)
 
 
+def test_offsets_out_of_range(env):
+    """Offsets outside the rows are brought into them, and an end before its
+    start makes an empty group: whatever the array holds, other memory is left
+    alone."""
+    torch, pg = env
+    A, B = torch.ones(8, 16, device="cuda"), torch.ones(3, 16, 4, device="cuda")
+    B[1], B[2] = 2, 4
+    for off, want in (([-5, 2, 6, 100], [1, 1, 2, 2, 2, 2, 4, 4]),
+                      ([0, 4, 1, 1], [1, 1, 1, 1, 0, 0, 0, 0]), ([9, 9, 9, 9], [0] * 8),
+                      ([2**31 - 1, -2**31, 2**31 - 1, 0], None)):
+        store = torch.zeros(10, 4, device="cuda")
+        o = torch.tensor(off, dtype=torch.int32, device="cuda")
+        pg.sgemm_grouped(0, 8, 4, 16, 3, o, 1.0, A, 16, B, 4, 64, 0.0, store[1:], 4)
+        if want is not None:
+            assert store[1:9, 0].tolist() == [16.0 * w for w in want], off
+        assert (store[0] == 0).all() and (store[9] == 0).all()
+        C = torch.full((5, 16, 4), 7.0, device="cuda")
+        pg.sgemm_grouped_outer(16, 4, 8, 3, o, 1.0, A, 16, torch.ones(8, 4, device="cuda"), 4, 0.0,
+                               C[1:], 4, 64)
+        if want is not None:
+            rows = [want.count(w) for w in (1, 2, 4)]
+            assert C[1:4, 0, 0].tolist() == rows, off
+        assert (C[0] == 7).all() and (C[4] == 7).all()
+
+
+@pytest.mark.parametrize("groups", [65, 129, 1000])
+def test_many_groups(env, groups):
+    """More groups than a wave has lanes: several a lane."""
+    rng = np.random.default_rng(groups)
+    counts = [int(c) for c in rng.integers(0, 4, groups)]
+    grouped_case(env, 0, counts, 36, 24, 1, 2)
+    grouped_case(env, 1, counts, 20, 17)
+    outer_case(env, counts, 24, 20, 1, 2)
+    grouped_case(env, 0, [c * 40 for c in counts[:70]], 64, 32)
+
+
 def test_sgemm_grouped_large_offsets(env):
     """Rows and weights beyond 2^32 bytes."""
     torch, pg = env
