@@ -2945,6 +2945,117 @@ struct GroupedParams {
     int band;            // row tiles of a band of the tile order
 };
 
+// An operand of any alignment and extent (of at least 4 along its stored rows),
+// with 16-byte loads all the same: floats are 4-byte aligned, which is all such
+// a load needs, so only the edges differ. A partial first K-step goes through
+// 4-byte loads, masked one by one. Where a chunk along the outer dimension ends
+// behind the operand's extent it is loaded from as far back as it sticks out,
+// and moved into place on its way to LDS (what then fills its end belongs to
+// outputs that are not stored).
+template <bool KC, int BO, int BK, int NT>
+struct AnyOperand {
+    typedef Operand<KC, BO, BK, NT, 1> Base;
+    static constexpr int STAGE = Base::STAGE, SLOTS = Base::SLOTS, C4 = Base::C4, EPS = 1;
+    static_assert(KC || NT % C4 == 0, "a thread's chunks lie above one another");
+
+    Base base; // the first K-step
+    const float *X;
+    long long ld, total;
+    int O, K, o0;
+    int over;              // floats this thread's chunks stick out
+    int kn;                // first k of the next full step
+    uint32_t off[SLOTS];
+    const float *wp;       // window of the next full K-step
+    WindowRange win;
+
+    __device__ __forceinline__ void init(int tid, int kfirst)
+    {
+        base.X = X;
+        base.ld = ld;
+        base.total = total;
+        base.O = O;
+        base.K = K;
+        base.o0 = o0;
+        base.init(tid, kfirst);
+        // Windows start 3 floats early where there are any, so that no offset
+        // is negative.
+        const int back = !KC && o0 > 0 ? 3 : 0;
+        over = 0;
+        if (!KC) {
+            const int left = O - (o0 + 4 * (tid % C4));
+            over = left > 0 && left < 4 ? 4 - left : 0;
+        }
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            const int f = tid + s * NT, r = f / C4, c4 = f % C4;
+            const bool ok = KC ? o0 + r < O : o0 + 4 * c4 < O;
+            off[s] = ok ? (uint32_t)(((long long)r * ld + 4 * c4 + back - over) * 4) : kOOB;
+        }
+        kn = kfirst + BK;
+        const long long k0 = kn;
+        const long long at = KC ? (long long)o0 * ld + k0 : k0 * ld + o0 - back;
+        wp = reinterpret_cast<const float *>(reinterpret_cast<uintptr_t>(X) + 4 * at);
+        win.init(4 * (total - at), (int32_t)(KC ? 4LL * BK : 4LL * BK * ld));
+    }
+
+    // FIRST: the first K-step; otherwise the next full one.
+    template <bool FIRST>
+    __device__ __forceinline__ void load_next(int tid, f32x4 (&regs)[SLOTS])
+    {
+        if constexpr (FIRST) {
+            base.template load_next<true>(tid, regs);
+            if (!KC) // as the chunks of the later steps come
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s)
+                    regs[s] = over == 1   ? f32x4{0.0f, regs[s][0], regs[s][1], regs[s][2]}
+                              : over == 2 ? f32x4{0.0f, 0.0f, regs[s][0], regs[s][1]}
+                              : over == 3 ? f32x4{0.0f, 0.0f, 0.0f, regs[s][0]}
+                                          : regs[s];
+        } else {
+            // (A step past the last reads nothing: a chunk could reach over the
+            // operand's end.)
+            const uint32_t left = win.take(), range = kn < K ? left : 0u;
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<float *>(wp), (short)0, (int)range, kRsrcWord3);
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s)
+                regs[s] = load4(rs, off[s]);
+            wp += KC ? (long long)BK : (long long)BK * ld;
+            kn += BK;
+        }
+    }
+
+    __device__ __forceinline__ void store(float *lds, int tid, const f32x4 (&regs)[SLOTS]) const
+    {
+        if constexpr (KC) {
+            Base::store(lds, tid, regs);
+        } else {
+            f32x4 v[SLOTS];
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s) {
+                v[s] = regs[s];
+                if (over & 1)
+                    v[s] = f32x4{v[s][1], v[s][2], v[s][3], v[s][3]};
+                if (over & 2)
+                    v[s] = f32x4{v[s][2], v[s][3], v[s][3], v[s][3]};
+            }
+            Base::store(lds, tid, v);
+        }
+    }
+
+    __device__ __forceinline__ static void frag(const float *lds, int w, int q, int lane,
+                                                float (&v)[4])
+    {
+        Base::frag(lds, w, q, lane, v);
+    }
+};
+
+// VEC: 4 or 1 floats a load as in Operand, 0: AnyOperand.
+template <bool KC, int BO, int BK, int NT, int VEC>
+using GroupedOperand =
+    std::conditional_t<VEC == 0, AnyOperand<KC, BO, BK, NT>,
+                       Operand<KC, BO, BK, NT, VEC == 0 ? 4 : VEC>>;
+
 template <int BM, int BN, int WAVES_M, int WAVES_N, bool A_KC, bool B_KC, int VEC>
 __device__ __forceinline__ void grouped_tile(const Params &p, const float *Ab, const float *Bb,
                                              float *Cb, int Kt, int m0, int n0, float *lds)
@@ -2952,8 +3063,8 @@ __device__ __forceinline__ void grouped_tile(const Params &p, const float *Ab, c
     constexpr int BK = kBK, NT = 64 * WAVES_M * WAVES_N;
     constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 32, TN = WN / 32;
     constexpr int NQ = BK / 8;
-    using OpA = Operand<A_KC, BM, BK, NT, VEC>;
-    using OpB = Operand<B_KC, BN, BK, NT, VEC>;
+    using OpA = GroupedOperand<A_KC, BM, BK, NT, VEC>;
+    using OpB = GroupedOperand<B_KC, BN, BK, NT, VEC>;
     constexpr int STAGE = OpA::STAGE + OpB::STAGE;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -3015,8 +3126,8 @@ __device__ __forceinline__ void grouped_tile(const Params &p, const float *Ab, c
         };
         opa.template load_next<true>(tid, ra[0]);
         opb.template load_next<true>(tid, rb[0]);
-        OpA::store(lds, tid, ra[0]);
-        OpB::store(lds + OpA::STAGE, tid, rb[0]);
+        opa.store(lds, tid, ra[0]);
+        opb.store(lds + OpA::STAGE, tid, rb[0]);
         opa.template load_next<false>(tid, ra[1]);
         opb.template load_next<false>(tid, rb[1]);
         __syncthreads();
@@ -3039,8 +3150,8 @@ __device__ __forceinline__ void grouped_tile(const Params &p, const float *Ab, c
             for (int q = 1; q < NQ - 1; ++q)
                 mfma_group(fa[q], fb[q], 0, 4 * TM * TN);
             mfma_group(fa[NQ - 1], fb[NQ - 1], 0, 4 * TM * TN - LATE);
-            OpA::store(nxt, tid, ra[1 - PAR]);
-            OpB::store(nxt + OpA::STAGE, tid, rb[1 - PAR]);
+            opa.store(nxt, tid, ra[1 - PAR]);
+            opb.store(nxt + OpA::STAGE, tid, rb[1 - PAR]);
             __builtin_amdgcn_sched_group_barrier(0x100, 4 * (TM + TN) * (NQ - 1), 0);
 #pragma unroll
             for (int w = 0; w < NL; ++w) {
@@ -3390,9 +3501,10 @@ extern "C" int sgemm_grouped(int transB, int M, int N, int K, int groups, const 
                                           : sgemm_grouped_stream_kernel<2, 1, 16, 2, false>,
                                    32, 16, 1024};
     }
-    else if (!vec4)
-        t = {transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 1>
-                    : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>, 64, 64, 256};
+    else if (!vec4) // (1060 rows over 6 groups, N = 3367, K = 2415: 190 us, in tiles of 128 226)
+        t = {transB   ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 0>
+             : N >= 4 ? sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 0>
+                      : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>, 64, 64, 256};
     else if (larger_tile(tiles(128, 128), tiles(64, 64), cus))
         t = {transB ? sgemm_grouped_kernel<128, 128, 2, 2, 2, true, 4>
                     : sgemm_grouped_kernel<128, 128, 2, 2, 2, false, 4>, 128, 128, 256};
@@ -3451,11 +3563,13 @@ extern "C" int sgemm_grouped_outer(int M, int N, int K, int groups, const int *o
     const int st = num_cus_of_current_device(&cus);
     if (st != 0)
         return st;
-    GroupedTile t{vec4 ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 4>
-                       : sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 1>, 64, 64, 256};
-    if (vec4 && larger_tile((double)ceil_div(M, 128) * ceil_div(N, 128) * groups,
-                            (double)ceil_div(M, 64) * ceil_div(N, 64) * groups, cus))
-        t = {sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 4>, 128, 128, 256};
+    GroupedTile t{vec4               ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 4>
+                  : M >= 4 && N >= 4 ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 0>
+                                     : sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 1>, 64, 64, 256};
+    if (M >= 4 && N >= 4 && larger_tile((double)ceil_div(M, 128) * ceil_div(N, 128) * groups,
+                                        (double)ceil_div(M, 64) * ceil_div(N, 64) * groups, cus))
+        t = {vec4 ? sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 4>
+                  : sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 0>, 128, 128, 256};
     const long long tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn);
     if ((double)tm * tn * groups > (double)(INT32_MAX / 256))
         return -22;

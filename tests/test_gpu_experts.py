@@ -510,6 +510,47 @@ def test_offsets_out_of_range(env):
         assert (C[0] == 7).all() and (C[4] == 7).all()
 
 
+@pytest.mark.parametrize("N,K", [(4, 4), (5, 7), (6, 33), (63, 65), (65, 18), (66, 47), (67, 50),
+                                 (129, 130), (200, 1001), (191, 259)])
+def test_products_of_any_extent(env, N, K):
+    """Extents off 4 and 64 in every position, at every 4-byte alignment, and
+    nothing read outside the operands (NaN lies around them)."""
+    counts = [70, 0, 130, 1, 64]
+    for pad, shift in ((0, 0), (1, 1), (2, 3), (5, 2)):
+        grouped_case(env, 0, counts, N, K, 1, 2, pad=pad, shift=shift)
+        grouped_case(env, 1, counts, N, K, 1, 2, pad=pad, shift=shift, beta=0.5)
+        outer_case(env, counts, N, K, 1, 2, pad=pad, shift=shift, alpha=-2.0)
+
+
+@pytest.mark.parametrize("tB", [0, 1])
+def test_nan_around_the_operands(env, tB):
+    """What lies beside rows, before the first and behind the last, is NaN."""
+    torch, pg = env
+    M, N, K, G = 150, 67, 45, 2
+    off = torch.tensor([0, 80, 150], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(3)
+
+    def make(groups, rows, cols, lead):
+        ld = cols + 3
+        store = torch.full((lead + groups * rows * ld,), torch.nan)
+        v = torch.randint(-4, 5, (groups, rows, cols), generator=g).float()
+        store[lead:].view(groups, rows, ld)[:, :, :cols] = v
+        return store.cuda()[lead:], ld, v.double()
+
+    for lead in (0, 1, 6):
+        A, lda, hA = make(1, M, K, lead)
+        B, ldb, hB = make(G, N if tB else K, K if tB else N, lead)
+        D, ldd, hD = make(1, M, N, lead)
+        C = torch.full((M, N), torch.nan, device="cuda")
+        pg.sgemm_grouped(tB, M, N, K, G, off, 1.0, A, lda, B, ldb, (N if tB else K) * ldb, 0.0, C, N)
+        W = torch.full((G, K, N), torch.nan, device="cuda")
+        pg.sgemm_grouped_outer(K, N, M, G, off, 1.0, A, lda, D, ldd, 0.0, W, N, K * N)
+        for e, (lo, hi) in enumerate(((0, 80), (80, 150))):
+            b = hB[e].T if tB else hB[e]
+            assert torch.equal(C[lo:hi].cpu().double(), hA[0, lo:hi] @ b)
+            assert torch.equal(W[e].cpu().double(), hA[0, lo:hi].T @ hD[0, lo:hi])
+
+
 @pytest.mark.parametrize("groups", [65, 129, 1000])
 def test_many_groups(env, groups):
     """More groups than a wave has lanes: several a lane."""
