@@ -3470,47 +3470,55 @@ extern "C" int sgemm_grouped(int transB, int M, int N, int K, int groups, const 
     if (st != 0)
         return st;
     // Row tiles as the groups would need with half a tile more than their
-    // average each.
+    // average each (one group: what it needs).
     const double used = groups < M ? groups : M;
     auto tiles = [&](int bm, int bn) {
-        const double each = (double)M / groups / bm + 0.5;
+        const double each = groups == 1 ? (double)ceil_div(M, bm) : (double)M / groups / bm + 0.5;
         return used * (each > 1.0 ? each : 1.0) * (double)ceil_div(N, bn);
     };
-    GroupedTile t;
-    if (M <= 16LL * groups) {
-        // Up to 16 rows a group on average: the weights stream, under row tiles
-        // of 16 or 32 (256 rows over 16 groups, 1024 x 1024, weights from
-        // memory: 20 us, the 64 x 64 tile 28; 512 rows: that tile 28). 64
-        // columns a workgroup (100 rows over 16 groups: 16.0 us), or 16 and
-        // more waves where that leaves half the CUs without one (one row, one
-        // group, 4096 x 4096: 20.5 us against 33.5).
-        const int bm = M <= 8LL * groups ? 16 : 32;
-        const bool wide = 2.0 * tiles(bm, 64) >= cus;
-        if (bm == 16)
-            t = wide ? GroupedTile{transB ? sgemm_grouped_stream_kernel<1, 4, 8, 1, true>
-                                          : sgemm_grouped_stream_kernel<1, 4, 8, 1, false>,
-                                   16, 64, 512}
-                     : GroupedTile{transB ? sgemm_grouped_stream_kernel<1, 1, 16, 2, true>
-                                          : sgemm_grouped_stream_kernel<1, 1, 16, 2, false>,
-                                   16, 16, 1024};
-        else
-            t = wide ? GroupedTile{transB ? sgemm_grouped_stream_kernel<2, 4, 8, 1, true>
-                                          : sgemm_grouped_stream_kernel<2, 4, 8, 1, false>,
-                                   32, 64, 512}
-                     : GroupedTile{transB ? sgemm_grouped_stream_kernel<2, 1, 16, 2, true>
-                                          : sgemm_grouped_stream_kernel<2, 1, 16, 2, false>,
-                                   32, 16, 1024};
+    // The kernels, with what a round of the CUs costs (us for K = 1024 beyond a
+    // launch, from 24 to 512 rows a group of 1, 2 and 8 groups; the streams' as
+    // in rounds after the first, where they share CUs). Few rows or columns stream under row tiles of 16 or 32, in 16 columns a
+    // workgroup and 16 waves along K or in 64 and 8. One row, one group, 4096 x
+    // 4096: 20.5 us in 16 columns, 33.5 in 64. 256 rows over 16 groups, 1024 x
+    // 1024, weights from memory: 20 us in 32 x 64, 28 in 64 x 64 tiles; 64 rows,
+    // one group, 1024 x 1024: 7 us in 16 x 16, 9 in 32 x 16, 18 in 64 x 64. The
+    // streams load rows along N that are off 16 bytes by 4, which 32 x 64 does
+    // not bear (32 rows over 8 groups each, 4095 x 4095: 198 us, 64 x 64 161);
+    // tiles of 128 take aligned operands only (1060 rows over 6 groups, N =
+    // 3367, K = 2415: 226 us, 64 x 64 190).
+    struct Choice {
+        GroupedTile t;
+        double round;
+        bool fits;
+    };
+    const Choice choices[] = {
+        {{transB ? sgemm_grouped_stream_kernel<1, 1, 16, 2, true>
+                 : sgemm_grouped_stream_kernel<1, 1, 16, 2, false>, 16, 16, 1024}, 3.5, true},
+        {{transB ? sgemm_grouped_stream_kernel<2, 1, 16, 2, true>
+                 : sgemm_grouped_stream_kernel<2, 1, 16, 2, false>, 32, 16, 1024}, 5.0, true},
+        {{transB ? sgemm_grouped_stream_kernel<1, 4, 8, 1, true>
+                 : sgemm_grouped_stream_kernel<1, 4, 8, 1, false>, 16, 64, 512}, 7.5, true},
+        {{transB ? sgemm_grouped_stream_kernel<2, 4, 8, 1, true>
+                 : sgemm_grouped_stream_kernel<2, 4, 8, 1, false>, 32, 64, 512}, 13.5,
+         vec4 || transB != 0},
+        {{transB   ? vec4 ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 4>
+                          : sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 0>
+          : vec4   ? sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 4>
+          : N >= 4 ? sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 0>
+                   : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>, 64, 64, 256}, 14.6, true},
+        {{transB ? sgemm_grouped_kernel<128, 128, 2, 2, 2, true, 4>
+                 : sgemm_grouped_kernel<128, 128, 2, 2, 2, false, 4>, 128, 128, 256}, 54.0, vec4},
+    };
+    GroupedTile t{};
+    double least = 0.0;
+    for (const Choice &c : choices) {
+        const double cost = c.round * std::ceil(tiles(c.t.bm, c.t.bn) / cus);
+        if (c.fits && (t.fn == nullptr || cost < least)) {
+            t = c.t;
+            least = cost;
+        }
     }
-    else if (!vec4) // (1060 rows over 6 groups, N = 3367, K = 2415: 190 us, in tiles of 128 226)
-        t = {transB   ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 0>
-             : N >= 4 ? sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 0>
-                      : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>, 64, 64, 256};
-    else if (larger_tile(tiles(128, 128), tiles(64, 64), cus))
-        t = {transB ? sgemm_grouped_kernel<128, 128, 2, 2, 2, true, 4>
-                    : sgemm_grouped_kernel<128, 128, 2, 2, 2, false, 4>, 128, 128, 256};
-    else
-        t = {transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 4>
-                    : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 4>, 64, 64, 256};
     gp.p.tiles_n = (int)ceil_div(N, t.bn);
     gp.band = group_band(M, groups, t.bm);
     return launch_grouped(t.fn, gp, most_tiles(M, groups, t.bm) * gp.p.tiles_n, t.threads,
