@@ -3215,6 +3215,15 @@ sgemm_grouped_kernel(GroupedParams gp)
         n0, lds);
 }
 
+// The t-th of a group's tiles so that the tiles of an XCD (every 8th block) lie
+// side by side (4096 x 16 outputs of one group, 8192 rows: 25 us; dealt out
+// singly, so that two XCDs read each line of A, 42).
+__device__ __forceinline__ int xcd_together(int t, int tiles)
+{
+    const int x = t % 8;
+    return x * (tiles / 8) + min(x, tiles % 8) + t / 8;
+}
+
 template <int BM, int BN, int WAVES_M, int WAVES_N, int MIN_WAVES_PER_EU, int VEC>
 __global__ void
 __attribute__((amdgpu_flat_work_group_size(64 * WAVES_M * WAVES_N, 64 * WAVES_M * WAVES_N),
@@ -3228,7 +3237,7 @@ sgemm_grouped_outer_kernel(GroupedParams gp)
     // us against 316). Up to 64 groups, those with the most rows first, so that
     // short tiles fill the end.
     const int tiles = p.tiles_m * p.tiles_n;
-    const int t = blockIdx.x % tiles;
+    const int t = xcd_together(blockIdx.x % tiles, tiles);
     int g = blockIdx.x / tiles;
     if (gp.groups <= 64)
         g = group_by_size(gp.offsets, gp.groups, p.K, g);
@@ -3285,7 +3294,9 @@ __device__ __forceinline__ Floats<E> row_floats(const float *row, int k, int K)
 // order. In v_mfma_f32_16x16x4_f32 lane l supplies row l % 16 and one k, l /
 // 16; the four products j of a block give it k = 4 (l / 16) + j, so that one
 // 16-byte load along k serves all four. B stored K x N is loaded along its
-// columns instead: product (j, e) takes column EN (l % 16) + e of row j.
+// columns instead: product (j, e) takes column EN (l % 16) + e of row j. Where
+// that would reach over N a lane takes the last EN columns, and those that it
+// shares with the lane before it are not stored.
 template <int MT, int EN, int WAVES, int U, bool B_KC>
 __global__ void __launch_bounds__(64 * WAVES) sgemm_grouped_stream_kernel(GroupedParams gp)
 {
@@ -3312,7 +3323,7 @@ __global__ void __launch_bounds__(64 * WAVES) sgemm_grouped_stream_kernel(Groupe
     for (int x = 0; x < NL; ++x)
         rb[x] = B_KC ? B + (long long)min(n0 + 16 * x + r, p.N - 1) * p.ldb
                      : B + (long long)(kq + x) * p.ldb; // (row k on top of it)
-    const int col = n0 + EN * r; // B stored K x N: this lane's first column
+    const int col = min(n0 + EN * r, p.N - EL); // B stored K x N: this lane's first column
 
     f32x4 acc[MT][EN] = {};
     // One block of 16 k. b[x]: B_KC, x = e: column n0 + 16 e + r, four k;
@@ -3330,31 +3341,29 @@ __global__ void __launch_bounds__(64 * WAVES) sgemm_grouped_stream_kernel(Groupe
                         acc[i][e], 0, 0, 0);
     };
     int k = 16 * wave;
-    if (B_KC || n0 + BN <= p.N) {
-        // U blocks at a time, all their loads before the first product (the
-        // compiler would wait for each load by itself).
-        for (; k + 16 * WAVES * (U - 1) + 16 <= p.K; k += 16 * WAVES * U) {
-            Floats<4> a[U][MT];
-            Floats<EL> b[U][NL];
+    // U blocks at a time, all their loads before the first product (the compiler
+    // would wait for each load by itself).
+    for (; k + 16 * WAVES * (U - 1) + 16 <= p.K; k += 16 * WAVES * U) {
+        Floats<4> a[U][MT];
+        Floats<EL> b[U][NL];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int ku = k + 16 * WAVES * u;
+        for (int u = 0; u < U; ++u) {
+            const int ku = k + 16 * WAVES * u;
 #pragma unroll
-                for (int x = 0; x < NL; ++x)
-                    b[u][x] = whole_floats<EL>(B_KC ? rb[x] + ku + kq
-                                                    : rb[x] + (long long)ku * p.ldb + col);
+            for (int x = 0; x < NL; ++x)
+                b[u][x] = whole_floats<EL>(B_KC ? rb[x] + ku + kq
+                                                : rb[x] + (long long)ku * p.ldb + col);
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    a[u][i] = whole_floats<4>(ra[i] + ku + kq);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                products(a[u], b[u]);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < MT; ++i)
+                a[u][i] = whole_floats<4>(ra[i] + ku + kq);
         }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            products(a[u], b[u]);
+        __builtin_amdgcn_sched_barrier(0);
     }
-    // What is left: the last blocks, the one K ends in, or the columns N ends in.
+    // What is left: the last blocks, and the one K ends in.
     for (; k < p.K; k += 16 * WAVES) {
         Floats<4> a[MT];
         Floats<EL> b[NL];
@@ -3371,14 +3380,15 @@ __global__ void __launch_bounds__(64 * WAVES) sgemm_grouped_stream_kernel(Groupe
             a[i] = row_floats<4>(ra[i], k + kq, p.K);
         products(a, b);
     }
-    // acc[i][e][v]: row 16 i + 4 (l / 16) + v, column 16 e + r or EN r + e.
+    // acc[i][e][v]: row 16 i + 4 (l / 16) + v, column n0 + 16 e + r or col + e.
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int e = 0; e < EN; ++e)
+        if (B_KC || col + e >= n0 + EN * r)
 #pragma unroll
-        for (int e = 0; e < EN; ++e)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-                sums[wave][16 * i + kq + v][B_KC ? 16 * e + r : EN * r + e] = acc[i][e][v];
+                for (int v = 0; v < 4; ++v)
+                    sums[wave][16 * i + kq + v][B_KC ? 16 * e + r : col + e - n0] = acc[i][e][v];
     __syncthreads();
     const int left = min(BM, rows - m0);
     for (int x = tid; x < left * BN; x += 64 * WAVES) {
@@ -3394,6 +3404,123 @@ __global__ void __launch_bounds__(64 * WAVES) sgemm_grouped_stream_kernel(Groupe
     }
 }
 
+// The outer form with few tiles: those of 64 x 64 would leave most CUs without
+// one. A workgroup owns 16 * EM x 16 * EN outputs of a group; its WAVES waves
+// take every WAVES-th block of 4 * U rows, and their partial sums are added in
+// LDS in the waves' order. One wave a SIMD: with more, matrix instructions
+// hold up the loads (64 x 64 outputs, 8192 rows, in 32 x 32 tiles: 38 us with 4
+// waves, 70 with 8, 88 with 16; loads or products alone take 27). In
+// v_mfma_f32_16x16x4_f32 lane l supplies column l % 16 of row l / 16; with one
+// load of EM and EN floats it supplies EM x EN products, whose outputs lie EM
+// and EN apart. Where a load would reach over the operand's columns a lane
+// takes the last ones, and outputs that it shares with the lane before it are
+// not stored.
+template <int EM, int EN, int WAVES, int U>
+__global__ void __launch_bounds__(64 * WAVES) sgemm_grouped_outer_stream_kernel(GroupedParams gp)
+{
+    constexpr int BM = 16 * EM, BN = 16 * EN;
+    __shared__ float sums[WAVES][BM][BN];
+    const Params &p = gp.p;
+    const int tiles = p.tiles_m * p.tiles_n, t = xcd_together(blockIdx.x % tiles, tiles);
+    int g = blockIdx.x / tiles;
+    if (gp.groups <= 64) // as in sgemm_grouped_outer_kernel
+        g = group_by_size(gp.offsets, gp.groups, p.K, g);
+    int lo, hi;
+    group_rows(gp.offsets, g, p.K, lo, hi);
+    const int K = p.alpha == 0.0f ? 0 : hi - lo;
+    if (K == 0 && p.beta == 1.0f)
+        return;
+    const int m0 = t / p.tiles_n * BM, n0 = t % p.tiles_n * BN;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, kr = lane >> 4;
+    const int col = min(n0 + EN * r, p.N - EN);
+    const long long stepA = 4LL * p.lda, stepB = 4LL * p.ldb; // four rows
+    int k = 4 * U * wave;
+    const float *a = p.A + (long long)(lo + k + kr) * p.lda + min(m0 + EM * r, p.M - EM);
+    const float *b = p.B + (long long)(lo + k + kr) * p.ldb + col;
+
+    f32x4 acc[EM][EN] = {};
+    auto products = [&](const Floats<EM> &a, const Floats<EN> &b) {
+#pragma unroll
+        for (int i = 0; i < EM; ++i)
+#pragma unroll
+            for (int e = 0; e < EN; ++e)
+                acc[i][e] =
+                    __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[i], b.x[e], acc[i][e], 0, 0, 0);
+    };
+    // The next block's loads before this one's products; a block that is not
+    // there is the last one again. (The barriers keep the compiler from waiting
+    // for each load by itself.)
+    Floats<EM> fa[2][U];
+    Floats<EN> fb[2][U];
+    auto load = [&](Floats<EM> (&x)[U], Floats<EN> (&y)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x[u] = whole_floats<EM>(a + u * stepA);
+            y[u] = whole_floats<EN>(b + u * stepB);
+        }
+    };
+    auto block = [&](int now) {
+        const bool next = k + 4 * U * WAVES + 4 * U <= K;
+        if (next) {
+            a += U * WAVES * stepA;
+            b += U * WAVES * stepB;
+        }
+        load(fa[1 - now], fb[1 - now]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            products(fa[now][u], fb[now][u]);
+        __builtin_amdgcn_sched_barrier(0);
+        k += 4 * U * WAVES;
+        return next;
+    };
+    if (k + 4 * U <= K) {
+        load(fa[0], fb[0]);
+        while (block(0) && block(1))
+            ;
+        a += U * WAVES * stepA;
+        b += U * WAVES * stepB;
+    }
+    // The block that the rows end in, which only one wave has left.
+    for (; k < K; k += 4, a += stepA, b += stepB) {
+        Floats<EM> x{};
+        Floats<EN> y{};
+        if (k + kr < K) {
+            x = whole_floats<EM>(a);
+            y = whole_floats<EN>(b);
+        }
+        products(x, y);
+    }
+    // acc[i][e][v]: of lane row 4 (l / 16) + v of A and lane column r of B.
+#pragma unroll
+    for (int i = 0; i < EM; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int first = m0 + EM * (4 * kr + v), m = min(first, p.M - EM) + i;
+#pragma unroll
+            for (int e = 0; e < EN; ++e)
+                if (m >= first && col + e >= n0 + EN * r)
+                    sums[wave][m - m0][col + e - n0] = acc[i][e][v];
+        }
+    __syncthreads();
+    const int rows = min(BM, p.M - m0);
+    for (int x = tid; x < rows * BN; x += 64 * WAVES) {
+        const int m = x / BN, n = n0 + x % BN;
+        if (n >= p.N)
+            continue;
+        float sum = sums[0][m][x % BN];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w)
+            sum += sums[w][m][x % BN];
+        float *c = p.C + g * gp.stride + (long long)(m0 + m) * p.ldc + n;
+        const float value = K == 0 ? 0.0f : p.alpha * sum;
+        *c = p.beta == 0.0f ? value : K == 0 ? p.beta * *c
+                                             : __builtin_fmaf(p.alpha, sum, p.beta * *c);
+    }
+}
+
 typedef void (*GroupedFn)(GroupedParams);
 
 struct GroupedTile {
@@ -3401,13 +3528,26 @@ struct GroupedTile {
     int bm, bn, threads;
 };
 
-// 128 x 128 tiles run at 95 % of the matrix rate and 64 x 64 ones at 88 %, but
-// leave finer rounds: the cheaper by the rounds of the CUs that `t128` and
-// `t64` tiles take.
-bool larger_tile(double t128, double t64, int cus)
+// A kernel with what a round of the CUs costs it.
+struct Choice {
+    GroupedTile t;
+    double round;
+    bool fits;
+};
+
+template <int N, typename Tiles>
+GroupedTile cheapest(const Choice (&choices)[N], const Tiles &tiles, int cus)
 {
-    auto rounds = [&](double t) { return (double)ceil_div((long long)(t + 0.999), cus); };
-    return 4.0 * rounds(t128) / 0.95 < rounds(t64) / 0.88;
+    GroupedTile t{};
+    double least = 0.0;
+    for (const Choice &c : choices) {
+        const double cost = c.round * std::ceil(tiles(c.t.bm, c.t.bn) / cus);
+        if (c.fits && (t.fn == nullptr || cost < least)) {
+            t = c.t;
+            least = cost;
+        }
+    }
+    return t;
 }
 
 int launch_grouped(GroupedFn fn, GroupedParams gp, long long blocks, int threads, hipStream_t s)
@@ -3477,48 +3617,39 @@ extern "C" int sgemm_grouped(int transB, int M, int N, int K, int groups, const 
         return used * (each > 1.0 ? each : 1.0) * (double)ceil_div(N, bn);
     };
     // The kernels, with what a round of the CUs costs (us for K = 1024 beyond a
-    // launch, from 24 to 512 rows a group of 1, 2 and 8 groups; the streams' as
-    // in rounds after the first, where they share CUs). Few rows or columns stream under row tiles of 16 or 32, in 16 columns a
-    // workgroup and 16 waves along K or in 64 and 8. One row, one group, 4096 x
-    // 4096: 20.5 us in 16 columns, 33.5 in 64. 256 rows over 16 groups, 1024 x
-    // 1024, weights from memory: 20 us in 32 x 64, 28 in 64 x 64 tiles; 64 rows,
-    // one group, 1024 x 1024: 7 us in 16 x 16, 9 in 32 x 16, 18 in 64 x 64. The
-    // streams load rows along N that are off 16 bytes by 4, which 32 x 64 does
-    // not bear (32 rows over 8 groups each, 4095 x 4095: 198 us, 64 x 64 161);
-    // tiles of 128 take aligned operands only (1060 rows over 6 groups, N =
+    // launch, from 1 to 256 rows a group of 1 and 8 groups; the streams' as in
+    // rounds after the first, where they share CUs). Few rows or columns stream
+    // under row tiles of 16 or 32, in 16 or 64 columns a workgroup. One row, one
+    // group, 4096 x 4096: 20.5 us in 16 columns, 33.5 in 64. 256 rows over 16
+    // groups, 1024 x 1024, weights from memory: 20 us in 32 x 64, 28 in 64 x 64
+    // tiles; 64 rows, one group, 1024 x 1024: 7 us in 16 x 16, 9 in 32 x 16, 18
+    // in 64 x 64. Waves of a workgroup: matrix instructions of four waves a SIMD
+    // hold up each other's loads (8 rows, one group, 4096 x 4096: 18.3 us with 8,
+    // 22.1 with 16; 32 rows: 22.6 us with 4, 27.1 with 16), but the wider
+    // tiles need the loads in flight (64 rows: 30 us with 8, 38 with 4). Tiles
+    // of 128 take 16-byte aligned operands only (1060 rows over 6 groups, N =
     // 3367, K = 2415: 226 us, 64 x 64 190).
-    struct Choice {
-        GroupedTile t;
-        double round;
-        bool fits;
-    };
     const Choice choices[] = {
-        {{transB ? sgemm_grouped_stream_kernel<1, 1, 16, 2, true>
-                 : sgemm_grouped_stream_kernel<1, 1, 16, 2, false>, 16, 16, 1024}, 3.5, true},
-        {{transB ? sgemm_grouped_stream_kernel<2, 1, 16, 2, true>
-                 : sgemm_grouped_stream_kernel<2, 1, 16, 2, false>, 32, 16, 1024}, 5.0, true},
+        {{transB ? sgemm_grouped_stream_kernel<1, 1, 8, 2, true>
+                 : sgemm_grouped_stream_kernel<1, 1, 8, 2, false>, 16, 16, 512}, 3.5, true},
+        {{transB ? sgemm_grouped_stream_kernel<2, 1, 4, 4, true>
+                 : sgemm_grouped_stream_kernel<2, 1, 4, 4, false>, 32, 16, 256}, 5.0, true},
         {{transB ? sgemm_grouped_stream_kernel<1, 4, 8, 1, true>
-                 : sgemm_grouped_stream_kernel<1, 4, 8, 1, false>, 16, 64, 512}, 7.5, true},
+                 : sgemm_grouped_stream_kernel<1, 4, 8, 1, false>, 16, 64, 512},
+         transB ? 8.7 : 7.5, transB || N >= 4},
         {{transB ? sgemm_grouped_stream_kernel<2, 4, 8, 1, true>
                  : sgemm_grouped_stream_kernel<2, 4, 8, 1, false>, 32, 64, 512}, 13.5,
-         vec4 || transB != 0},
+         transB || N >= 4},
         {{transB   ? vec4 ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 4>
                           : sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 0>
           : vec4   ? sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 4>
           : N >= 4 ? sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 0>
-                   : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>, 64, 64, 256}, 14.6, true},
+                   : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>, 64, 64, 256},
+         vec4 ? 14.6 : 17.0, true},
         {{transB ? sgemm_grouped_kernel<128, 128, 2, 2, 2, true, 4>
                  : sgemm_grouped_kernel<128, 128, 2, 2, 2, false, 4>, 128, 128, 256}, 54.0, vec4},
     };
-    GroupedTile t{};
-    double least = 0.0;
-    for (const Choice &c : choices) {
-        const double cost = c.round * std::ceil(tiles(c.t.bm, c.t.bn) / cus);
-        if (c.fits && (t.fn == nullptr || cost < least)) {
-            t = c.t;
-            least = cost;
-        }
-    }
+    const GroupedTile t = cheapest(choices, tiles, cus);
     gp.p.tiles_n = (int)ceil_div(N, t.bn);
     gp.band = group_band(M, groups, t.bm);
     return launch_grouped(t.fn, gp, most_tiles(M, groups, t.bm) * gp.p.tiles_n, t.threads,
@@ -3571,13 +3702,24 @@ extern "C" int sgemm_grouped_outer(int M, int N, int K, int groups, const int *o
     const int st = num_cus_of_current_device(&cus);
     if (st != 0)
         return st;
-    GroupedTile t{vec4               ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 4>
-                  : M >= 4 && N >= 4 ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 0>
-                                     : sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 1>, 64, 64, 256};
-    if (M >= 4 && N >= 4 && larger_tile((double)ceil_div(M, 128) * ceil_div(N, 128) * groups,
-                                        (double)ceil_div(M, 64) * ceil_div(N, 64) * groups, cus))
-        t = {vec4 ? sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 4>
-                  : sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 0>, 128, 128, 256};
+    auto tiles = [&](int bm, int bn) {
+        return (double)ceil_div(M, bm) * ceil_div(N, bn) * groups;
+    };
+    // As in sgemm_grouped. 1024 x 64 outputs of one group, 8192 rows: 25 us in
+    // 16 x 16 tiles, 40 in 32 x 32, 127 in 64 x 64; 256 x 256 of 2 groups, 8192
+    // rows: 29, 23 and 65; 512 x 512 of 8 groups, 512 rows: 15, 11.5 and 7.
+    const Choice choices[] = {
+        {{sgemm_grouped_outer_stream_kernel<1, 1, 4, 8>, 16, 16, 256}, 4.0, true},
+        {{sgemm_grouped_outer_stream_kernel<2, 2, 4, 4>, 32, 32, 256}, 7.4, M >= 2 && N >= 2},
+        {{vec4               ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 4>
+          : M >= 4 && N >= 4 ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 0>
+                             : sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 1>, 64, 64, 256},
+         vec4 ? 14.6 : 17.0, true},
+        {{vec4 ? sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 4>
+               : sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 0>, 128, 128, 256},
+         vec4 ? 54.0 : 60.0, M >= 4 && N >= 4},
+    };
+    const GroupedTile t = cheapest(choices, tiles, cus);
     const long long tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn);
     if ((double)tm * tn * groups > (double)(INT32_MAX / 256))
         return -22;

@@ -754,3 +754,22 @@ def test_binding_refuses(env):
         pg.sgemm_grouped(0, 4, 8, 8, 2, off, 1.0, x, 8, y, 8, 64, 0.0, x, 8)
     with pytest.raises(ValueError, match="C holds"):
         pg.sgemm_grouped_outer(8, 8, 4, 2, off, 1.0, x, 8, x, 8, 0.0, y, 8, 64)
+
+
+@pytest.mark.parametrize("M,N,counts", [(1, 1, [5, 0, 70]), (1, 33, [300]), (2, 2, [40, 3]),
+                                        (3, 70, [16, 17, 15]), (33, 1, [129]), (47, 31, [0, 64, 0]),
+                                        (16, 500, [1000]), (64, 64, [2049]), (65, 130, [33, 31])])
+def test_outer_products_of_few_tiles(env, M, N, counts):
+    """Tiles smaller than 64 x 64, and rows that end in every part of a block."""
+    for pad, shift in ((0, 0), (3, 1)):
+        outer_case(env, counts, M, N, 1, 2, pad=pad, shift=shift)
+        outer_case(env, counts, M, N, 1, 2, pad=pad, shift=shift, alpha=0.5, beta=-1.0)
+
+
+@pytest.mark.parametrize("tB", [0, 1])
+@pytest.mark.parametrize("M,N,K", [(17, 1, 64), (33, 3, 7), (40, 100, 1000), (100, 65, 17),
+                                   (300, 20, 333), (64, 130, 2049)])
+def test_products_of_few_tiles(env, M, N, K, tB):
+    grouped_case(env, tB, [M], N, K, 1, 2)
+    grouped_case(env, tB, [M], N, K, 1, 2, pad=1, shift=1, alpha=0.5, beta=-1.0)
+    grouped_case(env, tB, [M, 0, 5], N, K, 1, 2, pad=3, shift=2)
