@@ -454,7 +454,7 @@ __device__ __forceinline__ i32x4 load16_shifted(const signed char *p)
 // 16 (l / 16) on; register v of lane l holds row 4 (l / 16) + v, column l % 16.
 // Rows behind the last repeat it and are not stored. ALIGNED: rows start on
 // 16-byte boundaries; otherwise load16_shifted, inside the row (256 rows over
-// 64 groups, N = 2048: K = 2048 46 us, K = 2047 78, by unaligned loads 141).
+// 64 groups, N = 2048: K = 2048 46 us, K = 2047 84, by unaligned loads 141).
 // ---------------------------------------------------------------------------
 template <int MT, int NT, int WAVES, int U, bool ALIGNED>
 __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
