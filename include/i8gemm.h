@@ -77,6 +77,7 @@ int i8gemm(int M, int N, int K, const signed char *A, int lda, const float *scal
  * Positions: M 1 (rows of A and C), N 2, K 3, groups 4, offsets 5, A 6, lda 7,
  * scaleA 8, B 9, ldb 10, strideB 11 (>= 0; 0 shares one B), scaleB 12, C 14,
  * c_type 15, ldc 16. groups == 0: nothing is launched.
+ * At most 65536 groups; every workgroup reads all offsets.
  */
 int i8gemm_grouped(int M, int N, int K, int groups, const int *offsets, const signed char *A,
                    int lda, const float *scaleA, const signed char *B, int ldb, long long strideB,

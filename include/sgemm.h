@@ -420,7 +420,8 @@ int sgemm_strided_batched_noalloc(int transA, int transB, int M, int N, int K,
  *
  * Status codes: minus (a base for the call + the position of the first invalid
  * argument in its own list), base 800 for sgemm_grouped and 900 for
- * sgemm_grouped_outer, or -22. Leading dimensions are below 2^21. Execution
+ * sgemm_grouped_outer, or -22. Leading dimensions are below 2^21; sgemm_grouped
+ * takes up to 65536 groups (every workgroup reads all offsets). Execution
  * and accuracy are as above (K is a group's own row count in the outer form).
  */
 int sgemm_grouped(int transB, int M, int N, int K, int groups, const int *offsets,

@@ -1069,7 +1069,7 @@ extern "C" int i8gemm_grouped(int M, int N, int K, int groups, const int *offset
     if (M < 0) return -301;
     if (N < 0) return -302;
     if (K < 0 || K > I8GEMM_MAX_K) return -303;
-    if (groups < 0) return -304;
+    if (groups < 0 || groups > kMaxGroups) return -304;
     const int row = K > 1 ? K : 1;
     if (lda < row) return -307;
     if (ldb < row) return -310;

@@ -143,6 +143,10 @@ inline long long most_tiles(int rows, int groups, int bm)
     return rows / bm + (groups < rows ? groups : rows);
 }
 
+// Every workgroup reads all offsets to find its tile, so the groups' part of the
+// work grows with their square.
+constexpr int kMaxGroups = 65536;
+
 // Row tiles of a band of the tile order: as many as a group has on average.
 inline int group_band(long long rows, long long groups, int bm)
 {

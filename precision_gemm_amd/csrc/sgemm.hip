@@ -3104,7 +3104,7 @@ __device__ __forceinline__ void grouped_tile(const Params &p, const float *Ab, c
         // is used.)
         constexpr int LATE = TM * TN;
         f32x4 ra[2][OpA::SLOTS], rb[2][OpB::SLOTS];
-        const int nsteps = (Kt + BK - 1) / BK;
+        const int nsteps = Kt / BK + (Kt % BK != 0);
         auto read_group = [&](const float *stage, int q, float (&fa)[TM][4], float (&fb)[TN][4]) {
 #pragma unroll
             for (int i = 0; i < TM; ++i)
@@ -3427,7 +3427,8 @@ __global__ void __launch_bounds__(64 * WAVES) sgemm_grouped_outer_stream_kernel(
         g = group_by_size(gp.offsets, gp.groups, p.K, g);
     int lo, hi;
     group_rows(gp.offsets, g, p.K, lo, hi);
-    const int K = p.alpha == 0.0f ? 0 : hi - lo;
+    // (Unsigned, as k goes beyond K.)
+    const unsigned K = p.alpha == 0.0f ? 0 : hi - lo;
     if (K == 0 && p.beta == 1.0f)
         return;
     const int m0 = t / p.tiles_n * BM, n0 = t % p.tiles_n * BN;
@@ -3436,9 +3437,10 @@ __global__ void __launch_bounds__(64 * WAVES) sgemm_grouped_outer_stream_kernel(
     const int r = lane & 15, kr = lane >> 4;
     const int col = min(n0 + EN * r, p.N - EN);
     const long long stepA = 4LL * p.lda, stepB = 4LL * p.ldb; // four rows
-    int k = 4 * U * wave;
-    const float *a = p.A + (long long)(lo + k + kr) * p.lda + min(m0 + EM * r, p.M - EM);
-    const float *b = p.B + (long long)(lo + k + kr) * p.ldb + col;
+    unsigned k = 4 * U * wave;
+    const long long row = (long long)lo + k + kr;
+    const float *a = p.A + row * p.lda + min(m0 + EM * r, p.M - EM);
+    const float *b = p.B + row * p.ldb + col;
 
     f32x4 acc[EM][EN] = {};
     auto products = [&](const Floats<EM> &a, const Floats<EN> &b) {
@@ -3535,14 +3537,17 @@ struct Choice {
     bool fits;
 };
 
-template <int N, typename Tiles>
-GroupedTile cheapest(const Choice (&choices)[N], const Tiles &tiles, int cus)
+// The cheapest by the rounds of `tiles(bm, bn)` tiles; none if the `blocks(bm,
+// bn)` of no choice fit a launch.
+template <int N, typename Tiles, typename Blocks>
+GroupedTile cheapest(const Choice (&choices)[N], const Tiles &tiles, const Blocks &blocks, int cus)
 {
     GroupedTile t{};
     double least = 0.0;
     for (const Choice &c : choices) {
         const double cost = c.round * std::ceil(tiles(c.t.bm, c.t.bn) / cus);
-        if (c.fits && (t.fn == nullptr || cost < least)) {
+        if (c.fits && (double)blocks(c.t.bm, c.t.bn) * c.t.threads <= INT32_MAX &&
+            (t.fn == nullptr || cost < least)) {
             t = c.t;
             least = cost;
         }
@@ -3550,13 +3555,11 @@ GroupedTile cheapest(const Choice (&choices)[N], const Tiles &tiles, int cus)
     return t;
 }
 
-int launch_grouped(GroupedFn fn, GroupedParams gp, long long blocks, int threads, hipStream_t s)
+int launch_grouped(const GroupedTile &t, GroupedParams gp, double blocks, hipStream_t s)
 {
-    if (blocks * threads > INT32_MAX)
-        return -22;
     void *args[] = {&gp};
-    return (int)hipLaunchKernel((const void *)fn, dim3((unsigned)blocks), dim3(threads), args, 0,
-                                s);
+    return (int)hipLaunchKernel((const void *)t.fn, dim3((unsigned)blocks), dim3(t.threads), args,
+                                0, s);
 }
 
 } // namespace
@@ -3570,7 +3573,7 @@ extern "C" int sgemm_grouped(int transB, int M, int N, int K, int groups, const 
     if (M < 0) return -802;
     if (N < 0) return -803;
     if (K < 0) return -804;
-    if (groups < 0) return -805;
+    if (groups < 0 || groups > kMaxGroups) return -805;
     const int rowB = transB ? K : N;
     if (lda < (K > 1 ? K : 1) || lda > kMaxLd) return -809;
     if (ldb < (rowB > 1 ? rowB : 1) || ldb > kMaxLd) return -811;
@@ -3649,11 +3652,15 @@ extern "C" int sgemm_grouped(int transB, int M, int N, int K, int groups, const 
         {{transB ? sgemm_grouped_kernel<128, 128, 2, 2, 2, true, 4>
                  : sgemm_grouped_kernel<128, 128, 2, 2, 2, false, 4>, 128, 128, 256}, 54.0, vec4},
     };
-    const GroupedTile t = cheapest(choices, tiles, cus);
+    auto blocks = [&](int bm, int bn) {
+        return (double)most_tiles(M, groups, bm) * ceil_div(N, bn);
+    };
+    const GroupedTile t = cheapest(choices, tiles, blocks, cus);
+    if (t.fn == nullptr)
+        return -22;
     gp.p.tiles_n = (int)ceil_div(N, t.bn);
     gp.band = group_band(M, groups, t.bm);
-    return launch_grouped(t.fn, gp, most_tiles(M, groups, t.bm) * gp.p.tiles_n, t.threads,
-                          reinterpret_cast<hipStream_t>(stream));
+    return launch_grouped(t, gp, blocks(t.bm, t.bn), reinterpret_cast<hipStream_t>(stream));
 }
 
 extern "C" int sgemm_grouped_outer(int M, int N, int K, int groups, const int *offsets,
@@ -3719,14 +3726,12 @@ extern "C" int sgemm_grouped_outer(int M, int N, int K, int groups, const int *o
                : sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 0>, 128, 128, 256},
          vec4 ? 54.0 : 60.0, M >= 4 && N >= 4},
     };
-    const GroupedTile t = cheapest(choices, tiles, cus);
-    const long long tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn);
-    if ((double)tm * tn * groups > (double)(INT32_MAX / 256))
+    const GroupedTile t = cheapest(choices, tiles, tiles, cus);
+    if (t.fn == nullptr)
         return -22;
-    gp.p.tiles_m = (int)tm;
-    gp.p.tiles_n = (int)tn;
-    return launch_grouped(t.fn, gp, tm * tn * groups, t.threads,
-                          reinterpret_cast<hipStream_t>(stream));
+    gp.p.tiles_m = (int)ceil_div(M, t.bm);
+    gp.p.tiles_n = (int)ceil_div(N, t.bn);
+    return launch_grouped(t, gp, tiles(t.bm, t.bn), reinterpret_cast<hipStream_t>(stream));
 }
 
 extern "C" const char *sgemm_status_string(int status)

@@ -156,6 +156,13 @@ def test_oversize_grids_are_rejected(pg):
                 ldc=4096) == -22
 
 
+def test_too_many_groups_are_rejected(pg):
+    for name, code in (("i8gemm_grouped", -304), ("sgemm_grouped", -805)):
+        assert call(pg, name, groups=65537) == code
+        assert call(pg, name, groups=2**31 - 1) == code
+        assert "65536" in pg.sgemm_status_string(code)
+
+
 def test_binding_refuses_host_tensors(pg):
     torch = pytest.importorskip("torch")
     x, q, s = torch.zeros(4, 4), torch.zeros(4, 4, dtype=torch.int8), torch.zeros(4)

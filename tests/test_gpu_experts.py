@@ -773,3 +773,21 @@ def test_products_of_few_tiles(env, M, N, K, tB):
     grouped_case(env, tB, [M], N, K, 1, 2)
     grouped_case(env, tB, [M], N, K, 1, 2, pad=1, shift=1, alpha=0.5, beta=-1.0)
     grouped_case(env, tB, [M, 0, 5], N, K, 1, 2, pad=3, shift=2)
+
+
+def test_the_most_groups(env):
+    """65536 groups, most of them empty, around row and column ends."""
+    torch, pg = env
+    G, M, N, K = 65536, 70, 33, 5
+    rng = np.random.default_rng(1)
+    owner = np.sort(rng.choice(G, M))
+    owner[0], owner[-1] = 0, G - 1
+    off = torch.from_numpy(np.searchsorted(owner, np.arange(G + 1)).astype(np.int32)).cuda()
+    A = rng.integers(-8, 9, (M, K)).astype(np.float32)
+    B = rng.integers(-8, 9, (G, K, N)).astype(np.float32)
+    log(f"[grouped] G={G} M={M} N={N} K={K}")
+    C = torch.full((M, N), torch.nan, device="cuda")
+    pg.sgemm_grouped(0, M, N, K, G, off, 1.0, torch.from_numpy(A).cuda(), K,
+                     torch.from_numpy(B).cuda(), N, K * N, 0.0, C, N)
+    want = np.stack([A[m] @ B[owner[m]] for m in range(M)])  # exact: small whole numbers
+    assert np.array_equal(C.cpu().numpy(), want)
