@@ -483,28 +483,8 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
             for (int j = 0; j < NT; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
     };
-    for (int k = wave * 64 * U; k < p.K; k += WAVES * 64 * U) {
-        if (ALIGNED ? k + 64 * U <= p.K : k >= 16 && k + 64 * U + 16 <= p.K) {
-            i32x4 fb[U][NT], fa[U][MT];
-            auto load = [&](const signed char *x) {
-                return ALIGNED ? load16(x) : load16_shifted(x);
-            };
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    fb[u][j] = load(rb[j] + kq + k + 64 * u);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    fa[u][i] = load(ra[i] + kq + k + 64 * u);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                products(fa[u], fb[u]);
-            continue;
-        }
-        // The block at a row's end (or, unaligned, its start).
+    // A block at a row's end or, unaligned, its start.
+    auto edge = [&](int k) {
         for (int q = k; q < p.K && q < k + 64 * U; q += 64) {
             i32x4 fb[NT], fa[MT];
 #pragma unroll
@@ -515,7 +495,30 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
                 fa[i] = row_chunk(ra[i], q + kq, p.K);
             products(fa, fb);
         }
+    };
+    auto load = [&](const signed char *x) { return ALIGNED ? load16(x) : load16_shifted(x); };
+    int k = wave * 64 * U;
+    if (!ALIGNED && wave == 0) {
+        edge(0);
+        k = WAVES * 64 * U;
     }
+    for (; k + 64 * U + (ALIGNED ? 0 : 16) <= p.K; k += WAVES * 64 * U) {
+        i32x4 fb[U][NT], fa[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                fb[u][j] = load(rb[j] + kq + k + 64 * u);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                fa[u][i] = load(ra[i] + kq + k + 64 * u);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            products(fa[u], fb[u]);
+    }
+    edge(k);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
