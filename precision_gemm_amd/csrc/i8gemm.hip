@@ -19,16 +19,17 @@ constexpr float kLeastScale = 1.17549435e-38f; // 2^-126
 // The integer nearest to x / s (ties to even), |x / s| < 127.5. r, from a
 // product with the reciprocal, can be one off next to a tie; d = x - r s is
 // exact (for r = 0 it is x, for r = +-1 the subtraction of numbers within a
-// factor of two, beyond that a multiple of s's last place below 2^24 of them),
-// so comparing it with s / 2 (exact: s >= 2^-126) puts r right.
+// factor of two, or, for x just below s / 2, one that rounds to no less than
+// s / 2; beyond that a multiple of s's last place below 2^24 of them), and so is
+// 2 d, so comparing that with s puts r right. (s / 2 would not be exact: from
+// 2^-126 to 2^-125 half of an odd last place is no number.)
 __device__ __forceinline__ int quantize_one(float x, float s, float inv)
 {
     float r = __builtin_rintf(x * inv);
     const float d = __builtin_fmaf(-r, s, x);
-    const float half = 0.5f * s;
-    const float a = __builtin_fabsf(d);
+    const float twice = 2.0f * __builtin_fabsf(d);
     const bool odd = ((int)r) & 1;
-    if (a > half || (a == half && odd))
+    if (twice > s || (twice == s && odd))
         r += d > 0.0f ? 1.0f : -1.0f;
     return (int)r;
 }

@@ -511,3 +511,21 @@ def test_large_products_repeat(env):
         C[1].fill_(1.0)
         pg.i8gemm(M, N, K, A, K, sA, B, K, sB, None, C[1], N)
         assert torch.equal(C[0], C[1])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_quantize_borders_of_the_smallest_scales(env, dtype):
+    """The same for scales from 2^-126 to 2^-124, of which half is not always a
+    number: a tie is told from the values beside it all the same."""
+    torch, _ = env
+    g = torch.Generator().manual_seed(3)
+    X = torch.empty(256, 768)
+    for m in range(256):
+        peak = (127 * (1 + 3 * torch.rand(1, generator=g).double()) * 2.0 ** -126).float()
+        s = (peak.double() / 127).float()
+        k = torch.arange(256).double() - 127.5
+        mid = (k.clamp(-126.5, 126.5) * s.double()).float()
+        X[m] = torch.cat([mid, torch.nextafter(mid, torch.tensor(torch.inf)),
+                          torch.nextafter(mid, torch.tensor(-torch.inf))])
+        X[m, 0] = peak
+    quantize_case(env, X.to(getattr(torch, dtype)))
