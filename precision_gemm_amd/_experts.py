@@ -8,8 +8,10 @@ dimensions and strides count elements. Each tensor is taken from its first
 element on and has to reach as far as the call will go (the rows behind one
 another at the leading dimension, whatever the tensor's own shape); one that is
 too short, of another type or on another device is refused with a TypeError or
-ValueError before anything is launched. The work runs on `stream`, or else on
-the current stream of the operands' device.
+ValueError before anything is launched, and so is a view with gaps between its
+elements for an operand without a leading dimension (ids, row_of_slot, offsets,
+weights, scales, bias). The work runs on `stream`, or else on the current stream
+of the operands' device.
 """
 from __future__ import annotations
 
@@ -81,8 +83,9 @@ def _first(name, t):
     return t.get_device()
 
 
-def _at(name, t, dtypes, device, need):
-    """Address of an operand that the call takes `need` elements of."""
+def _at(name, t, dtypes, device, need, packed=False):
+    """Address of an operand that the call takes `need` elements of; packed: one
+    behind the other, as there is no leading dimension to say otherwise."""
     try:
         if t.get_device() == device and t.dtype in dtypes and need <= t.numel() and \
                 t.is_contiguous():
@@ -100,6 +103,9 @@ def _at(name, t, dtypes, device, need):
     if need > have:
         raise ValueError(f"{name} holds {have} elements from its first one on, "
                          f"the call needs {need}")
+    if packed and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, got shape {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
     return t.data_ptr()
 
 
@@ -123,7 +129,7 @@ def i8_quantize_rows(M, K, X, ldx, Q, ldq, scale, stream=None, check=True) -> in
     return _call(_lib.i8_quantize_rows, d, stream, check, M, K,
                  _at("X", X, _FLOATS, d, _span(M, K, ldx)), _TYPES[X.dtype], ldx,
                  _at("Q", Q, _INT8, d, _span(M, K, ldq)), ldq,
-                 _at("scale", scale, _F32, d, M))
+                 _at("scale", scale, _F32, d, M, True))
 
 
 def i8gemm(M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, C, ldc, stream=None, check=True) -> int:
@@ -132,10 +138,10 @@ def i8gemm(M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, C, ldc, stream=None, c
     d = _first("A", A)
     return _call(_lib.i8gemm, d, stream, check, M, N, K,
                  _at("A", A, _INT8, d, _span(M, K, lda)), lda,
-                 _at("scaleA", scaleA, _F32, d, M),
+                 _at("scaleA", scaleA, _F32, d, M, True),
                  _at("B", B, _INT8, d, _span(N, K, ldb)), ldb,
-                 _at("scaleB", scaleB, _F32, d, N),
-                 None if bias is None else _at("bias", bias, _F32, d, N),
+                 _at("scaleB", scaleB, _F32, d, N, True),
+                 None if bias is None else _at("bias", bias, _F32, d, N, True),
                  _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
 
 
@@ -145,12 +151,12 @@ def i8gemm_grouped(M, N, K, groups, offsets, A, lda, scaleA, B, ldb, strideB, sc
     holds groups + 1 int32, scaleB and bias groups x N."""
     d = _first("offsets", offsets)
     return _call(_lib.i8gemm_grouped, d, stream, check, M, N, K, groups,
-                 _at("offsets", offsets, _I32, d, groups + 1),
+                 _at("offsets", offsets, _I32, d, groups + 1, True),
                  _at("A", A, _INT8, d, _span(M, K, lda)), lda,
-                 _at("scaleA", scaleA, _F32, d, M),
+                 _at("scaleA", scaleA, _F32, d, M, True),
                  _at("B", B, _INT8, d, _spans(groups, strideB, N, K, ldb)), ldb, strideB,
-                 _at("scaleB", scaleB, _F32, d, groups * N),
-                 None if bias is None else _at("bias", bias, _F32, d, groups * N),
+                 _at("scaleB", scaleB, _F32, d, groups * N, True),
+                 None if bias is None else _at("bias", bias, _F32, d, groups * N, True),
                  _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
 
 
@@ -166,16 +172,14 @@ def expert_sort(tokens, topk, experts, ids, offsets, row_of_slot, workspace, str
     expert_sort_workspace_size() is 0."""
     d = _first("ids", ids)
     slots = tokens * topk
-    p_ids = _at("ids", ids, _IDS, d, slots)
+    p_ids = _at("ids", ids, _IDS, d, slots, True)
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws_bytes = workspace.numel() * workspace.element_size()
-        ws = _at("workspace", workspace, (workspace.dtype,), d, 0)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+        ws = _at("workspace", workspace, (workspace.dtype,), d, 0, True)
     return _call(_lib.expert_sort, d, stream, check, tokens, topk, experts, p_ids,
-                 ids.element_size(), _at("offsets", offsets, _I32, d, experts + 1),
-                 _at("row_of_slot", row_of_slot, _I32, d, slots), ws, ws_bytes)
+                 ids.element_size(), _at("offsets", offsets, _I32, d, experts + 1, True),
+                 _at("row_of_slot", row_of_slot, _I32, d, slots, True), ws, ws_bytes)
 
 
 def expert_gather(tokens, topk, cols, X, ldx, row_of_slot, Y, ldy, stream=None, check=True) -> int:
@@ -185,7 +189,7 @@ def expert_gather(tokens, topk, cols, X, ldx, row_of_slot, Y, ldy, stream=None, 
     slots = tokens * topk
     return _call(_lib.expert_gather, d, stream, check, tokens, topk, cols,
                  _at("X", X, _ANY, d, _span(tokens, cols, ldx)), _TYPES[X.dtype], ldx,
-                 _at("row_of_slot", row_of_slot, _I32, d, slots),
+                 _at("row_of_slot", row_of_slot, _I32, d, slots, True),
                  _at("Y", Y, (X.dtype,), d, _span(slots, cols, ldy)), ldy)
 
 
@@ -197,8 +201,8 @@ def expert_combine(tokens, topk, cols, Y, ldy, row_of_slot, weights, out, ldo, s
     slots = tokens * topk
     return _call(_lib.expert_combine, d, stream, check, tokens, topk, cols,
                  _at("Y", Y, _FLOATS, d, _span(slots, cols, ldy)), _TYPES[Y.dtype], ldy,
-                 _at("row_of_slot", row_of_slot, _I32, d, slots),
-                 None if weights is None else _at("weights", weights, _F32, d, slots),
+                 _at("row_of_slot", row_of_slot, _I32, d, slots, True),
+                 None if weights is None else _at("weights", weights, _F32, d, slots, True),
                  _at("out", out, (Y.dtype,), d, _span(tokens, cols, ldo)), ldo)
 
 
@@ -211,10 +215,10 @@ def expert_combine_grad(tokens, topk, cols, dout, ldo, Y, ldy, row_of_slot, weig
     return _call(_lib.expert_combine_grad, d, stream, check, tokens, topk, cols,
                  _at("dout", dout, _FLOATS, d, _span(tokens, cols, ldo)), _TYPES[dout.dtype], ldo,
                  None if Y is None else _at("Y", Y, (dout.dtype,), d, _span(slots, cols, ldy)),
-                 ldy, _at("row_of_slot", row_of_slot, _I32, d, slots),
-                 None if weights is None else _at("weights", weights, _F32, d, slots),
+                 ldy, _at("row_of_slot", row_of_slot, _I32, d, slots, True),
+                 None if weights is None else _at("weights", weights, _F32, d, slots, True),
                  _at("dY", dY, (dout.dtype,), d, _span(slots, cols, lddy)), lddy,
-                 None if dweights is None else _at("dweights", dweights, _F32, d, slots))
+                 None if dweights is None else _at("dweights", dweights, _F32, d, slots, True))
 
 
 def sgemm_grouped(transB, M, N, K, groups, offsets, alpha, A, lda, B, ldb, strideB, beta, C, ldc,
@@ -224,7 +228,7 @@ def sgemm_grouped(transB, M, N, K, groups, offsets, alpha, A, lda, B, ldb, strid
     d = _first("offsets", offsets)
     rows, cols = (N, K) if transB else (K, N)
     return _call(_lib.sgemm_grouped, d, stream, check, int(transB), M, N, K, groups,
-                 _at("offsets", offsets, _I32, d, groups + 1), float(alpha),
+                 _at("offsets", offsets, _I32, d, groups + 1, True), float(alpha),
                  _at("A", A, _F32, d, _span(M, K, lda)), lda,
                  _at("B", B, _F32, d, _spans(groups, strideB, rows, cols, ldb)), ldb, strideB,
                  float(beta), _at("C", C, _F32, d, _span(M, N, ldc)), ldc)
@@ -236,7 +240,7 @@ def sgemm_grouped_outer(M, N, K, groups, offsets, alpha, A, lda, B, ldb, beta, C
     rows offsets[g] <= k < offsets[g + 1] of A (K x M) and B (K x N)."""
     d = _first("offsets", offsets)
     return _call(_lib.sgemm_grouped_outer, d, stream, check, M, N, K, groups,
-                 _at("offsets", offsets, _I32, d, groups + 1), float(alpha),
+                 _at("offsets", offsets, _I32, d, groups + 1, True), float(alpha),
                  _at("A", A, _F32, d, _span(K, M, lda)), lda,
                  _at("B", B, _F32, d, _span(K, N, ldb)), ldb, float(beta),
                  _at("C", C, _F32, d, _spans(groups, strideC, M, N, ldc)), ldc, strideC)

@@ -187,3 +187,58 @@ def test_binding_refuses_sizes_beyond_an_int(pg):
             _experts._spans(2, 16, rows, cols, ld)
     assert _experts._span(3, 4, 5) == 14 and _experts._span(0, 4, 5) == 0
     assert _experts._spans(2, 100, 3, 4, 5) == 114 and torch is not None
+
+
+@pytest.fixture()
+def on_host(pg, monkeypatch):
+    """Host tensors that count as device 0's, for what the binding refuses, and
+    calls that end before the library's."""
+    torch = pytest.importorskip("torch")
+    from precision_gemm_amd import _experts
+
+    class OnDevice(torch.Tensor):
+        is_cuda = property(lambda self: True)
+        get_device = lambda self: 0  # noqa: E731
+
+    monkeypatch.setattr(_experts, "_call", lambda fn, device, stream, check, *args: args)
+    return torch, lambda *shape, dtype=torch.float32: \
+        torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice)
+
+
+def test_binding_refuses_vectors_with_gaps(pg, on_host):
+    """A part of a wider router's output, say: ids[:, :2] of [T, 4]. Taken as it
+    lies, its elements would be those of other slots."""
+    torch, make = on_host
+    T, k, E, H, N = 6, 2, 4, 8, 4
+    i32 = torch.int32
+    x, y, q = make(T * k, H), make(T * k, H), make(T * k, H, dtype=torch.int8)
+    vectors = dict(ids=make(T, 2 * k, dtype=i32), offsets=make(2 * E + 2, dtype=i32),
+                   row_of_slot=make(T, 2 * k, dtype=i32), weights=make(T, 2 * k),
+                   dweights=make(T, 2 * k), scale=make(2 * T), scaleA=make(2 * T),
+                   scaleB=make(E, 2 * N), bias=make(E, 2 * N))
+    gaps = {n: v[::2] if v.dim() == 1 else v[:, :v.shape[1] // 2] for n, v in vectors.items()}
+    whole = {n: v.contiguous() for n, v in gaps.items()}
+    calls = [
+        (lambda v: pg.i8_quantize_rows(T, H, x, H, q, H, v["scale"]), ["scale"]),
+        (lambda v: pg.i8gemm(T, N, H, q, H, v["scaleA"], q, H, v["scaleB"][:1], v["bias"][:1], x, H),
+         ["scaleA"]),
+        (lambda v: pg.i8gemm_grouped(T, N, H, E, v["offsets"], q, H, v["scaleA"], q, H, 0,
+                                     v["scaleB"], v["bias"], x, H),
+         ["offsets", "scaleA", "scaleB", "bias"]),
+        (lambda v: pg.expert_sort(T, k, E, v["ids"], v["offsets"], v["row_of_slot"], None),
+         ["ids", "offsets", "row_of_slot"]),
+        (lambda v: pg.expert_gather(T, k, H, x, H, v["row_of_slot"], y, H), ["row_of_slot"]),
+        (lambda v: pg.expert_combine(T, k, H, y, H, v["row_of_slot"], v["weights"], x, H),
+         ["row_of_slot", "weights"]),
+        (lambda v: pg.expert_combine_grad(T, k, H, x, H, y, H, v["row_of_slot"], v["weights"], y, H,
+                                          v["dweights"]), ["row_of_slot", "weights", "dweights"]),
+        (lambda v: pg.sgemm_grouped(0, T, H, H, E, v["offsets"], 1.0, x, H, y, H, 0, 0.0, x, H),
+         ["offsets"]),
+        (lambda v: pg.sgemm_grouped_outer(H, 1, T, E, v["offsets"], 1.0, x, H, x, H, 0.0, y, 1, 8),
+         ["offsets"]),
+    ]
+    for call_with, names in calls:
+        call_with(whole)  # taken
+        for name in names:
+            with pytest.raises(ValueError, match="^%s must be contiguous" % name):
+                call_with({**whole, name: gaps[name]})
