@@ -242,3 +242,35 @@ def test_binding_refuses_vectors_with_gaps(pg, on_host):
         for name in names:
             with pytest.raises(ValueError, match="^%s must be contiguous" % name):
                 call_with({**whole, name: gaps[name]})
+
+
+def test_binding_refuses_sizes_below_an_int(pg, on_host):
+    """-2^32 + 4 would reach the library as 4, past the check of the tensors'
+    extents, which a negative size needs nothing of. (Negative ints are the
+    library's to refuse.)"""
+    torch, make = on_host
+    n, big = 4 - 2**32, 4 - 2**64
+    x, q, s = make(2), make(2, dtype=torch.int8), make(1)
+    i = make(1, dtype=torch.int32)
+    for bad in (
+            lambda: pg.i8_quantize_rows(n, 4, x, 4, q, 4, s),
+            lambda: pg.i8_quantize_rows(4, n, x, 4, q, 4, make(4)),
+            lambda: pg.i8gemm(n, 1, 2, q, 2, s, q, 2, s, None, x, 1),
+            lambda: pg.i8gemm(1, n, 2, q, 2, s, q, 2, s, None, x, 1),
+            lambda: pg.i8gemm(2, 1, 1, q, n, make(2), q, 1, s, None, x, 1),
+            lambda: pg.i8gemm_grouped(1, 1, 2, n, i, q, 2, s, q, 2, 2, s, None, x, 1),
+            lambda: pg.i8gemm_grouped(1, 1, 2, 2, make(3, dtype=torch.int32), q, 2, s, q, 2, big,
+                                      make(2), None, x, 1),
+            lambda: pg.expert_sort(n, 1, 4, i, make(5, dtype=torch.int32), i, None),
+            lambda: pg.expert_sort(1, n, 4, i, make(5, dtype=torch.int32), i, None),
+            lambda: pg.expert_sort(1, 1, n, i, i, i, None),
+            lambda: pg.expert_gather(1, n, 2, x, 2, i, x, 2),
+            lambda: pg.expert_combine(1, n, 2, x, 2, i, None, x, 2),
+            lambda: pg.expert_combine_grad(1, n, 2, x, 2, x, 2, i, None, x, 2, s),
+            lambda: pg.sgemm_grouped(0, 1, 1, 1, n, i, 1.0, x, 1, x, 1, 1, 0.0, x, 1),
+            lambda: pg.sgemm_grouped_outer(1, 1, 1, n, i, 1.0, x, 1, x, 1, 0.0, x, 1, 1),
+            lambda: pg.sgemm_grouped_outer(1, 1, 1, 2, make(3, dtype=torch.int32), 1.0, x, 1, x, 1,
+                                           0.0, x, 1, big)):
+        with pytest.raises(ValueError, match="below 2|negative|positive"):
+            bad()
+    assert pg.i8gemm(-1, 1, 2, q, 2, s, q, 2, s, None, x, 1)[0] == -1
