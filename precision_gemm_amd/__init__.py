@@ -98,9 +98,9 @@ def _load():
     # torch's, and its device calls then fail. So torch, when installed, is
     # imported first.
     try:
-        import torch
+        import torch  # noqa: F401
     except ImportError:
-        torch = None
+        pass
     lib = ctypes.CDLL(path)
     i, f, p, ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
     lib.sgemm.restype = i
@@ -145,9 +145,8 @@ def _load():
     lib.sgemm_set_dispatch_overrides.argtypes = [ctypes.POINTER(ctypes.c_int), i]
     lib.sgemm_dispatch_override_count.restype = i
     lib.sgemm_dispatch_override_count.argtypes = []
-    if torch is not None:
-        from . import _experts
-        _experts.declare(lib)
+    from . import _experts
+    _experts.declare(lib)
     _lib = lib
     return lib
 
@@ -430,7 +429,8 @@ def matmul(A, B, C, alpha=1.0, beta=0.0, transA=False, transB=False, stream=None
 
 
 # The calls whose operands are always tensors come from their own module, loaded
-# on first use: it needs torch, which importing this package does not.
+# on first use: it imports torch, where there is one, which importing this package
+# does not.
 _EXPERTS = ("i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "expert_sort",
             "expert_sort_workspace_size", "expert_gather", "expert_combine",
             "expert_combine_grad", "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped",

@@ -17,15 +17,25 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
 import precision_gemm_amd as _pg
+
+try:
+    import torch
+except ImportError:  # the names are there without it; the calls are not
+    torch = None
 
 EXPERT_SORT_MAX_EXPERTS = 1024
 I8GEMM_MAX_K = 131071
 
-_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
-_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+if torch is not None:
+    _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+    _INT8, _F32, _I32 = (torch.int8,), (torch.float32,), (torch.int32,)
+    _IDS = (torch.int32, torch.int64)
+    _ANY = _FLOATS + _INT8
+    _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_lib = None  # the loaded library, set by declare()
 
 
 def declare(lib):
@@ -48,14 +58,6 @@ def declare(lib):
         getattr(lib, name).restype = i
     lib.expert_sort_workspace_size.restype = sz
     _lib = lib
-
-
-_INT8, _F32, _I32 = (torch.int8,), (torch.float32,), (torch.int32,)
-_ANY = _FLOATS + _INT8
-_IDS = (torch.int32, torch.int64)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda device: torch.cuda.current_stream(device).cuda_stream)
-_lib = None  # the loaded library, set by declare()
 
 
 _INT_MAX = 2**31 - 1  # sizes and leading dimensions are C ints
@@ -87,6 +89,8 @@ def _slots(tokens, topk):
 
 def _first(name, t):
     """The device of a call's operands, from one of them, with the library loaded."""
+    if torch is None:
+        raise ImportError("the expert and 8-bit calls take torch tensors, and torch is missing")
     if _lib is None:
         _pg._load()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:

@@ -4,6 +4,7 @@ a kernel, so it runs without a GPU."""
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 
@@ -274,3 +275,25 @@ def test_binding_refuses_sizes_below_an_int(pg, on_host):
         with pytest.raises(ValueError, match="below 2|negative|positive"):
             bad()
     assert pg.i8gemm(-1, 1, 2, q, 2, s, q, 2, s, None, x, 1)[0] == -1
+
+
+def test_without_torch(pg):
+    """Every public name is there without torch, as those of the fp32 calls
+    were before; the calls that take tensors say what they miss."""
+    code = """
+import sys
+sys.modules["torch"] = None  # imports of it fail
+from precision_gemm_amd import *
+import precision_gemm_amd as pg
+assert all(hasattr(pg, n) for n in pg.__all__)
+assert I8GEMM_MAX_K == 131071 and expert_sort_workspace_size(65536, 8, 128) > 0
+assert sgemm_select_variant(0, 0, 64, 64, 64, 1, 1, 256) >= 0
+try:
+    i8gemm(1, 1, 1, None, 1, None, None, 1, None, None, None, 1)
+except ImportError as e:
+    assert "torch" in str(e)
+else:
+    raise SystemExit("taken")
+"""
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
