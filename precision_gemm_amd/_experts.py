@@ -192,8 +192,8 @@ def expert_sort(tokens, topk, experts, ids, offsets, row_of_slot, workspace, str
     p_ids = _at("ids", ids, _IDS, d, slots, True)
     ws, ws_bytes = None, 0
     if workspace is not None:
+        ws = _at("workspace", workspace, (getattr(workspace, "dtype", None),), d, 0, True)
         ws_bytes = workspace.numel() * workspace.element_size()
-        ws = _at("workspace", workspace, (workspace.dtype,), d, 0, True)
     return _call(_lib.expert_sort, d, stream, check, tokens, topk, experts, p_ids,
                  ids.element_size(), _at("offsets", offsets, _I32, d, experts + 1, True),
                  _at("row_of_slot", row_of_slot, _I32, d, slots, True), ws, ws_bytes)

@@ -297,3 +297,14 @@ else:
 """
     out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert out.returncode == 0, out.stderr
+
+
+def test_binding_refuses_other_workspaces(pg, on_host):
+    torch, make = on_host
+    i = make(8, dtype=torch.int32)
+    for ws in (1 << 20, b"0" * 4096, torch.zeros(4096)):
+        with pytest.raises(TypeError, match="workspace must be a GPU tensor"):
+            pg.expert_sort(4, 2, 4, i, i, i, ws)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        pg.expert_sort(4, 2, 4, i, i, i, make(64, 2)[:, 0])
+    assert pg.expert_sort(4, 2, 4, i, i, i, make(64))[-1] == 256
