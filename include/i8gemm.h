@@ -25,7 +25,8 @@
  * Status codes: 0 success, a positive hipError_t, or minus (a base for the
  * call + the position of the first invalid argument): 100 for
  * i8_quantize_rows, 200 for i8gemm, 300 for i8gemm_grouped; e.g. -205 is a bad
- * lda of i8gemm; -22 for a product of more output tiles than a launch holds.
+ * lda of i8gemm; -22 for a product of more output tiles than a launch (2^32 - 1
+ * work-items) holds, whichever kernel runs.
  * Nothing is launched on error. sgemm_status_string() gives the message.
  */
 #ifndef PRECISION_GEMM_AMD_I8GEMM_H
@@ -83,6 +84,42 @@ int i8gemm_grouped(int M, int N, int K, int groups, const int *offsets, const si
                    int lda, const float *scaleA, const signed char *B, int ldb, long long strideB,
                    const float *scaleB, const float *bias, void *C, int c_type, int ldc,
                    sgemm_stream_t stream);
+
+/*
+ * Kernels the two calls choose among (see i8gemm_select_kernel): the tile of C
+ * one workgroup owns. Results do not depend on the kernel.
+ */
+enum i8gemm_kernel {
+    /* B streams from memory into registers, K split over the waves */
+    I8GEMM_KERNEL_S16x16 = 0,     /* 8 waves */
+    I8GEMM_KERNEL_S16x16_W16 = 1, /* 16 waves */
+    I8GEMM_KERNEL_S16x32 = 2,     /* 4 waves */
+    I8GEMM_KERNEL_S32x16 = 3,     /* 8 waves */
+    I8GEMM_KERNEL_S32x32 = 4,     /* 8 waves */
+    I8GEMM_KERNEL_S32x64 = 5,     /* 4 waves */
+    /* K-steps through registers to LDS: rows of any alignment */
+    I8GEMM_KERNEL_T64x64 = 6,
+    I8GEMM_KERNEL_T128x128 = 7,
+    /* K-steps straight into LDS: the fast kernels (see Alignment above) */
+    I8GEMM_KERNEL_L32x64 = 8,
+    I8GEMM_KERNEL_L64x64_R4 = 9,  /* four stages of LDS instead of three */
+    I8GEMM_KERNEL_L64x64 = 10,
+    I8GEMM_KERNEL_L64x128 = 11,
+    I8GEMM_KERNEL_L128x128 = 12,
+    I8GEMM_KERNEL_L128x256 = 13,
+    I8GEMM_KERNEL_L256x256 = 14,
+    I8GEMM_KERNEL_COUNT = 15
+};
+
+/*
+ * Host-side dispatch decision, exposed for tests and tuning (no device call):
+ * the kernel that i8gemm (groups == 0) or i8gemm_grouped launches for this
+ * shape, given whether rows start on 16-byte boundaries (`aligned`; leading
+ * dimensions are taken to be below 2^22) and the device's compute-unit count.
+ * Returns an i8gemm_kernel, -22 for more output tiles than a launch of any
+ * kernel that takes the call holds, or a negative status for invalid sizes.
+ */
+int i8gemm_select_kernel(int M, int N, int K, int groups, int aligned, int num_cus);
 
 #ifdef __cplusplus
 }

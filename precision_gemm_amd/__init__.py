@@ -31,8 +31,8 @@ __all__ = [
     "sgemm_set_dispatch_overrides", "sgemm_dispatch_override_count", "load_dispatch_overrides",
     "MAX_DISPATCH_OVERRIDES",
     "library_path",
-    "i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "expert_sort",
-    "expert_sort_workspace_size", "expert_gather", "expert_combine", "expert_combine_grad",
+    "i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "I8GEMM_KERNELS",
+    "i8gemm_select_kernel", "expert_sort", "expert_sort_workspace_size", "expert_gather", "expert_combine", "expert_combine_grad",
     "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped", "sgemm_grouped_outer",
     "VARIANT_AUTO", "VARIANT_L256x128", "VARIANT_M128x128", "VARIANT_S64x64",
     "VARIANT_S64x64_V1", "VARIANT_T64x64", "VARIANT_L256x256", "VARIANT_S64x64_K2",
@@ -431,8 +431,8 @@ def matmul(A, B, C, alpha=1.0, beta=0.0, transA=False, transB=False, stream=None
 # The calls whose operands are always tensors come from their own module, loaded
 # on first use: it imports torch, where there is one, which importing this package
 # does not.
-_EXPERTS = ("i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "expert_sort",
-            "expert_sort_workspace_size", "expert_gather", "expert_combine",
+_EXPERTS = ("i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "I8GEMM_KERNELS",
+            "i8gemm_select_kernel", "expert_sort", "expert_sort_workspace_size", "expert_gather", "expert_combine",
             "expert_combine_grad", "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped",
             "sgemm_grouped_outer")
 

@@ -26,6 +26,11 @@ except ImportError:  # the names are there without it; the calls are not
 
 EXPERT_SORT_MAX_EXPERTS = 1024
 I8GEMM_MAX_K = 131071
+# Kernels of the 8-bit product by number (i8gemm_kernel of the C header): S
+# stream B, T take rows of any alignment, L load straight into LDS.
+I8GEMM_KERNELS = ("S16x16", "S16x16_W16", "S16x32", "S32x16", "S32x32", "S32x64", "T64x64",
+                  "T128x128", "L32x64", "L64x64_R4", "L64x64", "L64x128", "L128x128", "L128x256",
+                  "L256x256")
 
 if torch is not None:
     _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
@@ -46,6 +51,7 @@ def declare(lib):
     lib.i8_quantize_rows.argtypes = [i, i, p, i, i, p, i, p, p]
     lib.i8gemm.argtypes = [i, i, i, p, i, p, p, i, p, p, p, i, i, p]
     lib.i8gemm_grouped.argtypes = [i, i, i, i, p, p, i, p, p, i, ll, p, p, p, i, i, p]
+    lib.i8gemm_select_kernel.argtypes = [i, i, i, i, i, i]
     lib.expert_sort.argtypes = [i, i, i, p, i, p, p, p, sz, p]
     lib.expert_sort_workspace_size.argtypes = [i, i, i]
     lib.expert_gather.argtypes = [i, i, i, p, i, i, p, p, i, p]
@@ -54,7 +60,8 @@ def declare(lib):
     lib.sgemm_grouped.argtypes = [i, i, i, i, i, p, f, p, i, p, i, ll, f, p, i, p]
     lib.sgemm_grouped_outer.argtypes = [i, i, i, i, p, f, p, i, p, i, f, p, i, ll, p]
     for name in ("i8_quantize_rows", "i8gemm", "i8gemm_grouped", "expert_sort", "expert_gather",
-                 "expert_combine", "expert_combine_grad", "sgemm_grouped", "sgemm_grouped_outer"):
+                 "expert_combine", "expert_combine_grad", "sgemm_grouped", "sgemm_grouped_outer",
+                 "i8gemm_select_kernel"):
         getattr(lib, name).restype = i
     lib.expert_sort_workspace_size.restype = sz
     _lib = lib
@@ -173,6 +180,14 @@ def i8gemm_grouped(M, N, K, groups, offsets, A, lda, scaleA, B, ldb, strideB, sc
                  _at("scaleB", scaleB, _F32, d, groups * N, True),
                  None if bias is None else _at("bias", bias, _F32, d, groups * N, True),
                  _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
+
+
+def i8gemm_select_kernel(M, N, K, groups, aligned, num_cus) -> int:
+    """C ABI ``i8gemm_select_kernel`` (host-side dispatch decision): an index of
+    I8GEMM_KERNELS, or a negative status."""
+    if _lib is None:
+        _pg._load()
+    return _lib.i8gemm_select_kernel(M, N, K, groups, int(bool(aligned)), num_cus)
 
 
 def expert_sort_workspace_size(tokens, topk, experts) -> int:

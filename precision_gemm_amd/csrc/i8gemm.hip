@@ -900,118 +900,158 @@ I8Variant stream_variant(bool aligned)
             16 * MT, 16 * NT, 64 * WAVES};
 }
 
+I8Variant variant_of(int kernel, bool aligned)
+{
+    switch (kernel) {
+    case I8GEMM_KERNEL_S16x16: return stream_variant<1, 1, 8, 2>(aligned);
+    case I8GEMM_KERNEL_S16x16_W16: return stream_variant<1, 1, 16, 2>(aligned);
+    case I8GEMM_KERNEL_S16x32: return stream_variant<1, 2, 4, 2>(aligned);
+    case I8GEMM_KERNEL_S32x16: return stream_variant<2, 1, 8, 2>(aligned);
+    case I8GEMM_KERNEL_S32x32: return stream_variant<2, 2, 8, 2>(aligned);
+    case I8GEMM_KERNEL_S32x64: return stream_variant<2, 4, 4, 2>(aligned);
+    case I8GEMM_KERNEL_T64x64: return {i8_tile_kernel<1>, 64, 64, 256};
+    case I8GEMM_KERNEL_T128x128: return {i8_tile_kernel<2>, 128, 128, 256};
+    case I8GEMM_KERNEL_L32x64: return {i8_large_kernel<32, 64, 1, 2, 4>, 32, 64, 128};
+    case I8GEMM_KERNEL_L64x64_R4: return {i8_large_kernel<64, 64, 2, 2, 4>, 64, 64, 256};
+    case I8GEMM_KERNEL_L64x64: return {i8_large_kernel<64, 64, 2, 2, 3>, 64, 64, 256};
+    case I8GEMM_KERNEL_L64x128: return {i8_large_kernel<64, 128, 2, 2, 3>, 64, 128, 256};
+    case I8GEMM_KERNEL_L128x128: return {i8_large_kernel<128, 128, 2, 4, 4>, 128, 128, 512};
+    case I8GEMM_KERNEL_L128x256: return {i8_large_kernel<128, 256, 2, 4, 3>, 128, 256, 512};
+    default: return {i8_large_kernel<256, 256, 2, 4, 2>, 256, 256, 512};
+    }
+}
+
 // The tiles that load straight into LDS, with what they cost on 256 CUs
 // (measured, us): `step` for 128 bytes of K of one tile a CU, `fixed` for the
 // launch, the first loads and the outputs. `one_round`: only where every CU
 // gets at most one tile, as its four stages leave room for few workgroups.
 struct I8Large {
-    I8Variant v;
+    int kernel, bm, bn;
     float step, fixed;
     bool one_round;
 };
 const I8Large kLarge[] = {
-    {{i8_large_kernel<32, 64, 1, 2, 4>, 32, 64, 128}, 0.22f, 4.0f, false},
-    {{i8_large_kernel<64, 64, 2, 2, 4>, 64, 64, 256}, 0.28f, 4.0f, true},
-    {{i8_large_kernel<64, 64, 2, 2, 3>, 64, 64, 256}, 0.33f, 4.0f, false},
-    {{i8_large_kernel<64, 128, 2, 2, 3>, 64, 128, 256}, 0.45f, 4.5f, false},
-    {{i8_large_kernel<128, 128, 2, 4, 4>, 128, 128, 512}, 0.70f, 5.0f, false},
-    {{i8_large_kernel<128, 256, 2, 4, 3>, 128, 256, 512}, 1.10f, 6.5f, false},
-    {{i8_large_kernel<256, 256, 2, 4, 2>, 256, 256, 512}, 1.85f, 8.0f, false},
+    {I8GEMM_KERNEL_L32x64, 32, 64, 0.22f, 4.0f, false},
+    {I8GEMM_KERNEL_L64x64_R4, 64, 64, 0.28f, 4.0f, true},
+    {I8GEMM_KERNEL_L64x64, 64, 64, 0.33f, 4.0f, false},
+    {I8GEMM_KERNEL_L64x128, 64, 128, 0.45f, 4.5f, false},
+    {I8GEMM_KERNEL_L128x128, 128, 128, 0.70f, 5.0f, false},
+    {I8GEMM_KERNEL_L128x256, 128, 256, 1.10f, 6.5f, false},
+    {I8GEMM_KERNEL_L256x256, 256, 256, 1.85f, 8.0f, false},
 };
 
-// The kernel of a call. Times below are graph replays over weights that no
-// cache holds.
-I8Variant choose_i8(const I8Params &p, int cus)
+long long i8_row_tiles(int M, int groups, int bm)
 {
-    const bool aligned = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.lda % 16 == 0 &&
-                         p.ldb % 16 == 0 && p.strideB % 16 == 0;
-    const bool direct =
-        aligned && p.K % 16 == 0 && p.lda < kMaxTileLd && p.ldb < kMaxTileLd && p.K > 0;
-    const long long n16 = ceil_div_ll(p.N, 16);
-    if (p.groups) {
+    return groups ? most_tiles(M, groups, bm) : ceil_div_ll(M, bm);
+}
+
+// Whether a launch holds `tiles` workgroups: fewer than 2^32 work-items.
+bool fits_launch(double tiles, int threads) { return tiles * threads <= 4294967295.0; }
+
+// The kernel of a call (an i8gemm_kernel), or -22 if the tiles of none fit a
+// launch. Those whose tiles do not are passed over. Times below are graph
+// replays over weights that no cache holds.
+int choose_i8(int M, int N, int K, int groups, bool aligned, bool direct, int cus)
+{
+    auto takes = [&](int kernel) {
+        const I8Variant v = variant_of(kernel, aligned);
+        return fits_launch((double)i8_row_tiles(M, groups, v.bm) * (double)ceil_div_ll(N, v.bn),
+                           v.threads);
+    };
+    const long long n16 = ceil_div_ll(N, 16);
+    int stream = -1;
+    if (groups) {
         // Up to 8 rows a group on average: the weights stream (256 rows over
         // 64 groups, 2048 x 2048: 48.5 us against 51.5 with the 32 x 64 tile;
         // 512 over 128, 4096 x 1024: 96 against 102; with 16 rows a group 76
         // against 58).
-        if (p.M <= 8LL * p.groups || (!direct && p.M <= 16LL * p.groups))
-            return stream_variant<1, 2, 4, 2>(aligned);
-    } else if (p.M <= 16) {
+        if (M <= 8LL * groups || (!direct && M <= 16LL * groups))
+            stream = I8GEMM_KERNEL_S16x32;
+    } else if (M <= 16) {
         // One row tile: 16 channels a workgroup, K over 8 waves, or 16 for a
         // token or a few over a deep K (1 x 4096 x 16384: 14.7 us against
         // 16.5; with 16 rows 18.9 against 17.6). With many workgroups, 32
         // channels for as many rows as make A's bytes count (16 x 16384 x 4096:
         // 17.9 us against 19.1; one row 17.0 against 17.1, 28672 channels 26.8
         // against 23.7).
-        if (p.M <= 4)
-            return p.K >= 4096 && n16 <= 2LL * cus ? stream_variant<1, 1, 16, 2>(aligned)
-                                                   : stream_variant<1, 1, 8, 2>(aligned);
-        if (n16 >= 4LL * cus)
-            return stream_variant<1, 2, 4, 2>(aligned);
-        return stream_variant<1, 1, 8, 2>(aligned);
+        if (M <= 4)
+            stream = K >= 4096 && n16 <= 2LL * cus ? I8GEMM_KERNEL_S16x16_W16
+                                                   : I8GEMM_KERNEL_S16x16;
+        else
+            stream = n16 >= 4LL * cus ? I8GEMM_KERNEL_S16x32 : I8GEMM_KERNEL_S16x16;
     } else {
         // Row tiles of 32 as long as every CU gets one workgroup at most: 16,
         // 32 or 64 channels (64 x 1024 x 4096: 7.9 us, the 32 x 64 tile 10.0;
         // 64 x 4096 x 4096: 10.9 and 11.7; 32 x 16384 x 4096: 20.7 and 28 with
         // the 64 x 64 tile; 128 x 4096 x 4096, two a CU: 17.8 and 11.8).
-        const long long m32 = ceil_div_ll(p.M, 32);
+        const long long m32 = ceil_div_ll(M, 32);
         if (m32 * n16 <= cus)
-            return stream_variant<2, 1, 8, 2>(aligned);
-        if (m32 * ceil_div_ll(p.N, 32) <= cus)
-            return stream_variant<2, 2, 8, 2>(aligned);
-        if (m32 * ceil_div_ll(p.N, 64) <= cus && p.M <= 32)
-            return stream_variant<2, 4, 4, 2>(aligned);
+            stream = I8GEMM_KERNEL_S32x16;
+        else if (m32 * ceil_div_ll(N, 32) <= cus)
+            stream = I8GEMM_KERNEL_S32x32;
+        else if (m32 * ceil_div_ll(N, 64) <= cus && M <= 32)
+            stream = I8GEMM_KERNEL_S32x64;
     }
-    const double used = p.groups < p.M ? p.groups : p.M;
+    if (stream >= 0 && takes(stream))
+        return stream;
+    const double used = groups < M ? groups : M;
     // Row tiles: of groups, every one's own and half a tile more, since only
     // the device knows their rows.
     auto row_tiles = [&](int bm) {
-        if (!p.groups)
-            return (double)ceil_div_ll(p.M, bm);
-        const double each = (double)p.M / p.groups / bm + 0.5;
+        if (!groups)
+            return (double)ceil_div_ll(M, bm);
+        const double each = (double)M / groups / bm + 0.5;
         return used * (each > 1.0 ? each : 1.0);
     };
-    if (!direct)
-        return row_tiles(128) * (double)ceil_div_ll(p.N, 128) >= cus
-                   ? I8Variant{i8_tile_kernel<2>, 128, 128, 256}
-                   : I8Variant{i8_tile_kernel<1>, 64, 64, 256};
-    const I8Large *best = nullptr;
+    if (!direct) {
+        if (row_tiles(128) * (double)ceil_div_ll(N, 128) < cus && takes(I8GEMM_KERNEL_T64x64))
+            return I8GEMM_KERNEL_T64x64;
+        return takes(I8GEMM_KERNEL_T128x128) ? I8GEMM_KERNEL_T128x128 : -22;
+    }
+    int best = -22;
     float least = 0.0f;
     for (const I8Large &l : kLarge) {
-        const double tiles = row_tiles(l.v.bm) * (double)ceil_div_ll(p.N, l.v.bn);
-        if (l.one_round && tiles > cus)
+        const double tiles = row_tiles(l.bm) * (double)ceil_div_ll(N, l.bn);
+        if ((l.one_round && tiles > cus) || !takes(l.kernel))
             continue;
         const float rounds = (float)ceil_div_ll((long long)(tiles + 0.999), cus);
-        const float cost = l.fixed + rounds * (float)ceil_div_ll(p.K, 128) * l.step;
-        if (best == nullptr || cost < least) {
-            best = &l;
+        const float cost = l.fixed + rounds * (float)ceil_div_ll(K, 128) * l.step;
+        if (best < 0 || cost < least) {
+            best = l.kernel;
             least = cost;
         }
     }
-    return best->v;
+    return best;
+}
+
+// (Refused before the device is asked: not even 256 x 256 tiles fit a launch.)
+bool too_many_tiles(int M, int N, int groups)
+{
+    return !fits_launch((double)i8_row_tiles(M, groups, 256) * (double)ceil_div_ll(N, 256), 512);
 }
 
 int launch_i8(I8Params p, hipStream_t s)
 {
-    // (Every tile is at most 256 x 256: more of those than a launch can hold
-    // are refused before the device is asked.)
-    if ((p.groups ? most_tiles(p.M, p.groups, 256) : ceil_div_ll(p.M, 256)) *
-            ceil_div_ll(p.N, 256) > (1 << 22))
+    if (too_many_tiles(p.M, p.N, p.groups))
         return -22;
     int cus = 0;
     const int st = current_cus(&cus);
     if (st != 0)
         return st;
-    const I8Variant v = choose_i8(p, cus);
-    const long long tiles_m =
-        p.groups ? most_tiles(p.M, p.groups, v.bm) : ceil_div_ll(p.M, v.bm);
-    const long long tiles_n = ceil_div_ll(p.N, v.bn);
-    if (tiles_m * tiles_n * v.threads > 0xffffffffLL || tiles_m * tiles_n > INT32_MAX)
-        return -22;
-    p.tiles_m = (int)tiles_m;
-    p.tiles_n = (int)tiles_n;
+    const bool aligned = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.lda % 16 == 0 &&
+                         p.ldb % 16 == 0 && p.strideB % 16 == 0;
+    const bool direct =
+        aligned && p.K % 16 == 0 && p.lda < kMaxTileLd && p.ldb < kMaxTileLd && p.K > 0;
+    const int kernel = choose_i8(p.M, p.N, p.K, p.groups, aligned, direct, cus);
+    if (kernel < 0)
+        return kernel;
+    const I8Variant v = variant_of(kernel, aligned);
+    p.tiles_m = (int)i8_row_tiles(p.M, p.groups, v.bm);
+    p.tiles_n = (int)ceil_div_ll(p.N, v.bn);
     p.band = p.groups ? group_band(p.M, p.groups, v.bm) : 8;
     void *args[] = {&p};
-    return (int)hipLaunchKernel((const void *)v.fn, dim3((unsigned)(tiles_m * tiles_n)),
+    return (int)hipLaunchKernel((const void *)v.fn,
+                                dim3((unsigned)((long long)p.tiles_m * p.tiles_n)),
                                 dim3(v.threads), args, 0, s);
 }
 
@@ -1091,4 +1131,15 @@ extern "C" int i8gemm_grouped(int M, int N, int K, int groups, const int *offset
     I8Params p{A,   B,   scaleA, scaleB, bias,   C,      offsets, strideB, M,
                N,   K,   lda,    ldb,    ldc,    c_type, groups, 0, 0, 0};
     return launch_i8(p, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int i8gemm_select_kernel(int M, int N, int K, int groups, int aligned, int num_cus)
+{
+    if (M < 0) return -201;
+    if (N < 0) return -202;
+    if (K < 0 || K > I8GEMM_MAX_K) return -203;
+    if (groups < 0 || groups > kMaxGroups) return -304;
+    if (too_many_tiles(M, N, groups)) return -22;
+    return choose_i8(M, N, K, groups, aligned != 0, aligned != 0 && K > 0 && K % 16 == 0,
+                     num_cus > 1 ? num_cus : 1);
 }

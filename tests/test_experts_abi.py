@@ -308,3 +308,51 @@ def test_binding_refuses_other_workspaces(pg, on_host):
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         pg.expert_sort(4, 2, 4, i, i, i, make(64, 2)[:, 0])
     assert pg.expert_sort(4, 2, 4, i, i, i, make(64))[-1] == 256
+
+
+I8_THREADS = dict(S16x16=512, S16x16_W16=1024, S16x32=256, S32x16=512, S32x32=512, S32x64=256,
+                  L32x64=128, L128x128=512, L128x256=512, L256x256=512)  # others 256
+
+
+def i8_work_items(name, M, N, groups):
+    """Work-items of a call's launch: every group may have a partly filled row tile."""
+    bm, bn = map(int, re.match(r"[STL](\d+)x(\d+)", name).groups())
+    rows = M // bm + min(groups, M) if groups else -(-M // bm)
+    return rows * -(-N // bn) * I8_THREADS.get(name, 256)
+
+
+def test_i8_kernel_numbers(pg):
+    text = open(os.path.join(ROOT, "include", "i8gemm.h")).read()
+    numbers = dict(re.findall(r"I8GEMM_KERNEL_(\w+) = (\d+)", text))
+    assert int(numbers.pop("COUNT")) == len(pg.I8GEMM_KERNELS)
+    assert {n: int(v) for n, v in numbers.items()} == {n: i for i, n in enumerate(pg.I8GEMM_KERNELS)}
+
+
+def test_i8_kernels_whose_tiles_fit_a_launch(pg):
+    """A kernel whose tiles a launch does not hold is passed over for one whose
+    tiles it does."""
+    import random
+    rng = random.Random(7)
+    size = lambda most: int(2 ** rng.uniform(0, most))  # noqa: E731
+    calls = [(524288, 8192, 4096, 65536, 1), (8192, 350000, 16, 1024, 1), (2**30, 1, 16, 0, 1),
+             (1, 2**29, 64, 0, 1), (4, 2**30, 64, 0, 1), (16, 2**30, 64, 0, 0)]
+    calls += [(size(31), size(31), rng.choice([1, 16, 100, 4096]), rng.choice([0, 0, size(16)]),
+               rng.randrange(2)) for _ in range(20000)]
+    refused = 0
+    for M, N, K, groups, aligned in calls:
+        kernel = pg.i8gemm_select_kernel(M, N, K, groups, aligned, 256)
+        if kernel >= 0:
+            name = pg.I8GEMM_KERNELS[kernel]
+            assert i8_work_items(name, M, N, groups) < 2**32, (M, N, K, groups, aligned, name)
+            assert name[0] != "L" or (aligned and K % 16 == 0)
+            continue
+        refused += 1
+        assert kernel == -22
+        largest = "L256x256" if aligned and K % 16 == 0 else "T128x128"
+        assert i8_work_items(largest, M, N, groups) >= 2**32, (M, N, K, groups, aligned)
+    assert 0 < refused < 20000
+    assert pg.i8gemm_select_kernel(524288, 8192, 4096, 65536, 1, 256) >= 0
+    for bad, status in (((-1, 1, 1, 0), -201), ((1, -1, 1, 0), -202), ((1, 1, 131072, 0), -203),
+                        ((1, 1, 1, 65537), -304)):
+        assert pg.i8gemm_select_kernel(*bad, 1, 256) == status
+    assert pg.i8gemm_select_kernel(0, 0, 0, 0, 0, 0) >= 0

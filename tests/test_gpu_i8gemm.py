@@ -529,3 +529,53 @@ def test_quantize_borders_of_the_smallest_scales(env, dtype):
                           torch.nextafter(mid, torch.tensor(-torch.inf))])
         X[m, 0] = peak
     quantize_case(env, X.to(getattr(torch, dtype)))
+
+
+def test_rows_that_only_the_largest_tiles_hold(env):
+    """2^30 rows: 2^31 work-items in 256 x 256 tiles, more than a launch holds
+    in any other."""
+    torch, pg = env
+    M, K = 1 << 30, 16
+    log(f"[i8gemm] {M}x1x{K}")
+    A = torch.empty(M, K, dtype=torch.int8, device="cuda")
+    A.view(-1).view(torch.int64).random_(generator=torch.Generator(device="cuda").manual_seed(1))
+    B = torch.tensor([[1, -2, 3, -4, 5, -6, 7, -8, 9, 10, -11, 12, 13, 14, -15, 127]],
+                     dtype=torch.int8, device="cuda")
+    one = torch.ones(M, device="cuda")
+    C = torch.full((M + 1,), 7.0, device="cuda")
+    pg.i8gemm(M, 1, K, A, K, one, B, K, one, None, C, 1)
+    torch.cuda.synchronize()
+    for lo in range(0, M, 1 << 26):
+        a = A[lo:lo + (1 << 26)]
+        want = torch.zeros(a.shape[0], device="cuda")
+        for k in range(K):  # whole numbers below 2^24
+            want += a[:, k].float() * float(B[0, k])
+        assert torch.equal(C[lo:lo + (1 << 26)], want), lo
+    assert C[M].item() == 7
+
+
+def test_groups_that_only_larger_tiles_hold(env):
+    """Few rows a group would stream, in more tiles than a launch holds."""
+    torch, pg = env
+    G, M, N, K = 1024, 8192, 350000, 16
+    log(f"[i8gemm grouped] {M}x{N}x{K} groups={G}")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    A = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    B = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    cut = torch.randint(0, M + 1, (G - 1,), generator=g, device="cuda").sort().values
+    off = torch.cat([cut.new_zeros(1), cut, cut.new_full((1,), M)]).int()
+    sA = 2.0 ** torch.randint(-3, 4, (M,), generator=g, device="cuda").float()
+    sB = 2.0 ** torch.randint(-3, 4, (G, N), generator=g, device="cuda").float()
+    C = torch.full((M, N), 7.0, dtype=torch.float32, device="cuda")
+    pg.i8gemm_grouped(M, N, K, G, off, A, K, sA, B, K, 0, sB, None, C, N)
+    torch.cuda.synchronize()
+    group = torch.repeat_interleave(torch.arange(G, device="cuda"), off.diff().long())
+    b = B.float().t().contiguous()
+    for lo in range(0, M, 512):  # sums below 2^24, scales powers of two: exact
+        rows = slice(lo, lo + 512)
+        want = torch.zeros(512, N, device="cuda")
+        for k in range(K):
+            want += A[rows, k, None].float() * b[k]
+        want *= sA[rows, None]
+        want *= sB[group[rows]]
+        assert torch.equal(C[rows], want), lo
