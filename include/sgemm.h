@@ -437,6 +437,45 @@ int sgemm_grouped_outer(int M, int N, int K, int groups, const int *offsets,
                         sgemm_stream_t stream);
 
 /*
+ * Kernels of the grouped products: the tile of C one workgroup owns. S: the
+ * operands stream into the matrix instructions' registers, K split over the
+ * waves; T: tiles through LDS, on 16-byte aligned operands, _ANY on others, _V1
+ * with 1-float loads (fewer than 4 columns, where streaming tiles would not
+ * fit a launch).
+ */
+enum sgemm_grouped_kernel {
+    SGEMM_GROUPED_S16x16 = 0,
+    SGEMM_GROUPED_S32x16 = 1,
+    SGEMM_GROUPED_S16x64 = 2,
+    SGEMM_GROUPED_S32x64 = 3,
+    SGEMM_GROUPED_T64x64 = 4,
+    SGEMM_GROUPED_T64x64_ANY = 5,
+    SGEMM_GROUPED_T64x64_V1 = 6,
+    SGEMM_GROUPED_T128x128 = 7,
+    SGEMM_GROUPED_COUNT = 8
+};
+enum sgemm_grouped_outer_kernel {
+    SGEMM_GROUPED_OUTER_S16x16 = 0,
+    SGEMM_GROUPED_OUTER_S32x32 = 1,
+    SGEMM_GROUPED_OUTER_T64x64 = 2,
+    SGEMM_GROUPED_OUTER_T64x64_ANY = 3,
+    SGEMM_GROUPED_OUTER_T64x64_V1 = 4,
+    SGEMM_GROUPED_OUTER_T128x128 = 5,
+    SGEMM_GROUPED_OUTER_T128x128_ANY = 6,
+    SGEMM_GROUPED_OUTER_COUNT = 7
+};
+
+/*
+ * Host-side dispatch decisions of sgemm_grouped and sgemm_grouped_outer, exposed
+ * for tests and tuning (no device call): the kernel for this shape, given
+ * whether the 4-float load path is allowed (`vec4_ok`: A, B and their strides as
+ * under Alignment above, extents along the stored rows multiples of 4) and the
+ * device's compute-unit count. -22 or the status of an invalid size otherwise.
+ */
+int sgemm_grouped_select_kernel(int transB, int M, int N, int groups, int vec4_ok, int num_cus);
+int sgemm_grouped_outer_select_kernel(int M, int N, int groups, int vec4_ok, int num_cus);
+
+/*
  * Host-side check of the buffer-range bookkeeping the tile and streaming
  * kernels use while their load window walks an operand (tests; no device
  * call). A window starts `left_bytes` before the end of the operand and moves

@@ -31,6 +31,12 @@ I8GEMM_MAX_K = 131071
 I8GEMM_KERNELS = ("S16x16", "S16x16_W16", "S16x32", "S32x16", "S32x32", "S32x64", "T64x64",
                   "T128x128", "L32x64", "L64x64_R4", "L64x64", "L64x128", "L128x128", "L128x256",
                   "L256x256")
+# The same of the grouped fp32 products (sgemm_grouped_kernel and
+# sgemm_grouped_outer_kernel): S stream, T go through LDS.
+GROUPED_KERNELS = ("S16x16", "S32x16", "S16x64", "S32x64", "T64x64", "T64x64_ANY", "T64x64_V1",
+                   "T128x128")
+GROUPED_OUTER_KERNELS = ("S16x16", "S32x32", "T64x64", "T64x64_ANY", "T64x64_V1", "T128x128",
+                         "T128x128_ANY")
 
 if torch is not None:
     _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
@@ -52,6 +58,8 @@ def declare(lib):
     lib.i8gemm.argtypes = [i, i, i, p, i, p, p, i, p, p, p, i, i, p]
     lib.i8gemm_grouped.argtypes = [i, i, i, i, p, p, i, p, p, i, ll, p, p, p, i, i, p]
     lib.i8gemm_select_kernel.argtypes = [i, i, i, i, i, i]
+    lib.sgemm_grouped_select_kernel.argtypes = [i, i, i, i, i, i]
+    lib.sgemm_grouped_outer_select_kernel.argtypes = [i, i, i, i, i]
     lib.expert_sort.argtypes = [i, i, i, p, i, p, p, p, sz, p]
     lib.expert_sort_workspace_size.argtypes = [i, i, i]
     lib.expert_gather.argtypes = [i, i, i, p, i, i, p, p, i, p]
@@ -61,7 +69,8 @@ def declare(lib):
     lib.sgemm_grouped_outer.argtypes = [i, i, i, i, p, f, p, i, p, i, f, p, i, ll, p]
     for name in ("i8_quantize_rows", "i8gemm", "i8gemm_grouped", "expert_sort", "expert_gather",
                  "expert_combine", "expert_combine_grad", "sgemm_grouped", "sgemm_grouped_outer",
-                 "i8gemm_select_kernel"):
+                 "i8gemm_select_kernel", "sgemm_grouped_select_kernel",
+                 "sgemm_grouped_outer_select_kernel"):
         getattr(lib, name).restype = i
     lib.expert_sort_workspace_size.restype = sz
     _lib = lib
@@ -276,3 +285,19 @@ def sgemm_grouped_outer(M, N, K, groups, offsets, alpha, A, lda, B, ldb, beta, C
                  _at("A", A, _F32, d, _span(K, M, lda)), lda,
                  _at("B", B, _F32, d, _span(K, N, ldb)), ldb, float(beta),
                  _at("C", C, _F32, d, _spans(groups, strideC, M, N, ldc)), ldc, strideC)
+
+
+def sgemm_grouped_select_kernel(transB, M, N, groups, vec4_ok, num_cus) -> int:
+    """C ABI ``sgemm_grouped_select_kernel`` (host-side dispatch decision): an
+    index of GROUPED_KERNELS, or a negative status."""
+    if _lib is None:
+        _pg._load()
+    return _lib.sgemm_grouped_select_kernel(int(transB), M, N, groups, int(bool(vec4_ok)), num_cus)
+
+
+def sgemm_grouped_outer_select_kernel(M, N, groups, vec4_ok, num_cus) -> int:
+    """C ABI ``sgemm_grouped_outer_select_kernel``, as above: an index of
+    GROUPED_OUTER_KERNELS."""
+    if _lib is None:
+        _pg._load()
+    return _lib.sgemm_grouped_outer_select_kernel(M, N, groups, int(bool(vec4_ok)), num_cus)

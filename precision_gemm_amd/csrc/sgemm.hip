@@ -3532,6 +3532,7 @@ struct GroupedTile {
 
 // A kernel with what a round of the CUs costs it.
 struct Choice {
+    int kernel;
     GroupedTile t;
     double round;
     bool fits;
@@ -3540,19 +3541,19 @@ struct Choice {
 // The cheapest by the rounds of `tiles(bm, bn)` tiles; none if the `blocks(bm,
 // bn)` of no choice fit a launch.
 template <int N, typename Tiles, typename Blocks>
-GroupedTile cheapest(const Choice (&choices)[N], const Tiles &tiles, const Blocks &blocks, int cus)
+Choice cheapest(const Choice (&choices)[N], const Tiles &tiles, const Blocks &blocks, int cus)
 {
-    GroupedTile t{};
+    Choice best{-22, {}, 0.0, false};
     double least = 0.0;
     for (const Choice &c : choices) {
         const double cost = c.round * std::ceil(tiles(c.t.bm, c.t.bn) / cus);
         if (c.fits && (double)blocks(c.t.bm, c.t.bn) * c.t.threads <= INT32_MAX &&
-            (t.fn == nullptr || cost < least)) {
-            t = c.t;
+            (best.kernel < 0 || cost < least)) {
+            best = c;
             least = cost;
         }
     }
-    return t;
+    return best;
 }
 
 int launch_grouped(const GroupedTile &t, GroupedParams gp, double blocks, hipStream_t s)
@@ -3560,6 +3561,99 @@ int launch_grouped(const GroupedTile &t, GroupedParams gp, double blocks, hipStr
     void *args[] = {&gp};
     return (int)hipLaunchKernel((const void *)t.fn, dim3((unsigned)blocks), dim3(t.threads), args,
                                 0, s);
+}
+
+// Most tiles of bm x bn that the groups can need.
+double grouped_blocks(int M, int N, int groups, int bm, int bn)
+{
+    return (double)most_tiles(M, groups, bm) * ceil_div(N, bn);
+}
+
+Choice choose_grouped(bool transB, int M, int N, int groups, bool vec4, int cus)
+{
+    // Row tiles as the groups would need with half a tile more than their
+    // average each (one group: what it needs).
+    const double used = groups < M ? groups : M;
+    auto tiles = [&](int bm, int bn) {
+        const double each = groups == 1 ? (double)ceil_div(M, bm) : (double)M / groups / bm + 0.5;
+        return used * (each > 1.0 ? each : 1.0) * (double)ceil_div(N, bn);
+    };
+    // The kernels, with what a round of the CUs costs (us for K = 1024 beyond a
+    // launch, from 1 to 256 rows a group of 1 and 8 groups; the streams' as in
+    // rounds after the first, where they share CUs). Few rows or columns stream
+    // under row tiles of 16 or 32, in 16 or 64 columns a workgroup. One row, one
+    // group, 4096 x 4096: 20.5 us in 16 columns, 33.5 in 64. 256 rows over 16
+    // groups, 1024 x 1024, weights from memory: 20 us in 32 x 64, 28 in 64 x 64
+    // tiles; 64 rows, one group, 1024 x 1024: 7 us in 16 x 16, 9 in 32 x 16, 18
+    // in 64 x 64. Waves of a workgroup: matrix instructions of four waves a SIMD
+    // hold up each other's loads (8 rows, one group, 4096 x 4096: 18.3 us with 8,
+    // 22.1 with 16; 32 rows: 22.6 us with 4, 27.1 with 16), but the wider
+    // tiles need the loads in flight (64 rows: 30 us with 8, 38 with 4). Tiles
+    // of 128 take 16-byte aligned operands only (1060 rows over 6 groups, N =
+    // 3367, K = 2415: 226 us, 64 x 64 190). Loads of one float each (N < 4, B
+    // stored K x N) are left for over 2^28 rows, which the streams' tiles do not
+    // fit a launch with.
+    const Choice choices[] = {
+        {SGEMM_GROUPED_S16x16,
+         {transB ? sgemm_grouped_stream_kernel<1, 1, 8, 2, true>
+                 : sgemm_grouped_stream_kernel<1, 1, 8, 2, false>, 16, 16, 512}, 3.5, true},
+        {SGEMM_GROUPED_S32x16,
+         {transB ? sgemm_grouped_stream_kernel<2, 1, 4, 4, true>
+                 : sgemm_grouped_stream_kernel<2, 1, 4, 4, false>, 32, 16, 256}, 5.0, true},
+        {SGEMM_GROUPED_S16x64,
+         {transB ? sgemm_grouped_stream_kernel<1, 4, 8, 1, true>
+                 : sgemm_grouped_stream_kernel<1, 4, 8, 1, false>, 16, 64, 512},
+         transB ? 8.7 : 7.5, transB || N >= 4},
+        {SGEMM_GROUPED_S32x64,
+         {transB ? sgemm_grouped_stream_kernel<2, 4, 8, 1, true>
+                 : sgemm_grouped_stream_kernel<2, 4, 8, 1, false>, 32, 64, 512},
+         13.5, transB || N >= 4},
+        {SGEMM_GROUPED_T64x64,
+         {transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 4>
+                 : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 4>, 64, 64, 256}, 14.6, vec4},
+        {SGEMM_GROUPED_T64x64_ANY,
+         {transB ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 0>
+                 : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 0>, 64, 64, 256},
+         17.0, !vec4 && (transB || N >= 4)},
+        {SGEMM_GROUPED_T64x64_V1,
+         {sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>, 64, 64, 256}, 17.0,
+         !vec4 && !transB && N < 4},
+        {SGEMM_GROUPED_T128x128,
+         {transB ? sgemm_grouped_kernel<128, 128, 2, 2, 2, true, 4>
+                 : sgemm_grouped_kernel<128, 128, 2, 2, 2, false, 4>, 128, 128, 256}, 54.0, vec4},
+    };
+    return cheapest(choices, tiles,
+                    [&](int bm, int bn) { return grouped_blocks(M, N, groups, bm, bn); }, cus);
+}
+
+Choice choose_grouped_outer(int M, int N, int groups, bool vec4, int cus)
+{
+    auto tiles = [&](int bm, int bn) {
+        return (double)ceil_div(M, bm) * ceil_div(N, bn) * groups;
+    };
+    // As in sgemm_grouped. 1024 x 64 outputs of one group, 8192 rows: 25 us in
+    // 16 x 16 tiles, 40 in 32 x 32, 127 in 64 x 64; 256 x 256 of 2 groups, 8192
+    // rows: 29, 23 and 65; 512 x 512 of 8 groups, 512 rows: 15, 11.5 and 7. Loads of
+    // one float each (fewer than 4 columns of A or B) are left for calls whose
+    // streaming tiles do not fit a launch: M = 1, N = 2^21 - 1, 65 groups.
+    const bool any = !vec4 && M >= 4 && N >= 4;
+    const Choice choices[] = {
+        {SGEMM_GROUPED_OUTER_S16x16,
+         {sgemm_grouped_outer_stream_kernel<1, 1, 4, 8>, 16, 16, 256}, 4.0, true},
+        {SGEMM_GROUPED_OUTER_S32x32,
+         {sgemm_grouped_outer_stream_kernel<2, 2, 4, 4>, 32, 32, 256}, 7.4, M >= 2 && N >= 2},
+        {SGEMM_GROUPED_OUTER_T64x64,
+         {sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 4>, 64, 64, 256}, 14.6, vec4},
+        {SGEMM_GROUPED_OUTER_T64x64_ANY,
+         {sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 0>, 64, 64, 256}, 17.0, any},
+        {SGEMM_GROUPED_OUTER_T64x64_V1,
+         {sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 1>, 64, 64, 256}, 17.0, !vec4 && !any},
+        {SGEMM_GROUPED_OUTER_T128x128,
+         {sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 4>, 128, 128, 256}, 54.0, vec4},
+        {SGEMM_GROUPED_OUTER_T128x128_ANY,
+         {sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 0>, 128, 128, 256}, 60.0, any},
+    };
+    return cheapest(choices, tiles, tiles, cus);
 }
 
 } // namespace
@@ -3612,55 +3706,13 @@ extern "C" int sgemm_grouped(int transB, int M, int N, int K, int groups, const 
     const int st = num_cus_of_current_device(&cus);
     if (st != 0)
         return st;
-    // Row tiles as the groups would need with half a tile more than their
-    // average each (one group: what it needs).
-    const double used = groups < M ? groups : M;
-    auto tiles = [&](int bm, int bn) {
-        const double each = groups == 1 ? (double)ceil_div(M, bm) : (double)M / groups / bm + 0.5;
-        return used * (each > 1.0 ? each : 1.0) * (double)ceil_div(N, bn);
-    };
-    // The kernels, with what a round of the CUs costs (us for K = 1024 beyond a
-    // launch, from 1 to 256 rows a group of 1 and 8 groups; the streams' as in
-    // rounds after the first, where they share CUs). Few rows or columns stream
-    // under row tiles of 16 or 32, in 16 or 64 columns a workgroup. One row, one
-    // group, 4096 x 4096: 20.5 us in 16 columns, 33.5 in 64. 256 rows over 16
-    // groups, 1024 x 1024, weights from memory: 20 us in 32 x 64, 28 in 64 x 64
-    // tiles; 64 rows, one group, 1024 x 1024: 7 us in 16 x 16, 9 in 32 x 16, 18
-    // in 64 x 64. Waves of a workgroup: matrix instructions of four waves a SIMD
-    // hold up each other's loads (8 rows, one group, 4096 x 4096: 18.3 us with 8,
-    // 22.1 with 16; 32 rows: 22.6 us with 4, 27.1 with 16), but the wider
-    // tiles need the loads in flight (64 rows: 30 us with 8, 38 with 4). Tiles
-    // of 128 take 16-byte aligned operands only (1060 rows over 6 groups, N =
-    // 3367, K = 2415: 226 us, 64 x 64 190).
-    const Choice choices[] = {
-        {{transB ? sgemm_grouped_stream_kernel<1, 1, 8, 2, true>
-                 : sgemm_grouped_stream_kernel<1, 1, 8, 2, false>, 16, 16, 512}, 3.5, true},
-        {{transB ? sgemm_grouped_stream_kernel<2, 1, 4, 4, true>
-                 : sgemm_grouped_stream_kernel<2, 1, 4, 4, false>, 32, 16, 256}, 5.0, true},
-        {{transB ? sgemm_grouped_stream_kernel<1, 4, 8, 1, true>
-                 : sgemm_grouped_stream_kernel<1, 4, 8, 1, false>, 16, 64, 512},
-         transB ? 8.7 : 7.5, transB || N >= 4},
-        {{transB ? sgemm_grouped_stream_kernel<2, 4, 8, 1, true>
-                 : sgemm_grouped_stream_kernel<2, 4, 8, 1, false>, 32, 64, 512}, 13.5,
-         transB || N >= 4},
-        {{transB   ? vec4 ? sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 4>
-                          : sgemm_grouped_kernel<64, 64, 2, 2, 4, true, 0>
-          : vec4   ? sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 4>
-          : N >= 4 ? sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 0>
-                   : sgemm_grouped_kernel<64, 64, 2, 2, 4, false, 1>, 64, 64, 256},
-         vec4 ? 14.6 : 17.0, true},
-        {{transB ? sgemm_grouped_kernel<128, 128, 2, 2, 2, true, 4>
-                 : sgemm_grouped_kernel<128, 128, 2, 2, 2, false, 4>, 128, 128, 256}, 54.0, vec4},
-    };
-    auto blocks = [&](int bm, int bn) {
-        return (double)most_tiles(M, groups, bm) * ceil_div(N, bn);
-    };
-    const GroupedTile t = cheapest(choices, tiles, blocks, cus);
-    if (t.fn == nullptr)
-        return -22;
-    gp.p.tiles_n = (int)ceil_div(N, t.bn);
-    gp.band = group_band(M, groups, t.bm);
-    return launch_grouped(t, gp, blocks(t.bm, t.bn), reinterpret_cast<hipStream_t>(stream));
+    const Choice c = choose_grouped(transB, M, N, groups, vec4, cus);
+    if (c.kernel < 0)
+        return c.kernel;
+    gp.p.tiles_n = (int)ceil_div(N, c.t.bn);
+    gp.band = group_band(M, groups, c.t.bm);
+    return launch_grouped(c.t, gp, grouped_blocks(M, N, groups, c.t.bm, c.t.bn),
+                          reinterpret_cast<hipStream_t>(stream));
 }
 
 extern "C" int sgemm_grouped_outer(int M, int N, int K, int groups, const int *offsets,
@@ -3709,29 +3761,32 @@ extern "C" int sgemm_grouped_outer(int M, int N, int K, int groups, const int *o
     const int st = num_cus_of_current_device(&cus);
     if (st != 0)
         return st;
-    auto tiles = [&](int bm, int bn) {
-        return (double)ceil_div(M, bm) * ceil_div(N, bn) * groups;
-    };
-    // As in sgemm_grouped. 1024 x 64 outputs of one group, 8192 rows: 25 us in
-    // 16 x 16 tiles, 40 in 32 x 32, 127 in 64 x 64; 256 x 256 of 2 groups, 8192
-    // rows: 29, 23 and 65; 512 x 512 of 8 groups, 512 rows: 15, 11.5 and 7.
-    const Choice choices[] = {
-        {{sgemm_grouped_outer_stream_kernel<1, 1, 4, 8>, 16, 16, 256}, 4.0, true},
-        {{sgemm_grouped_outer_stream_kernel<2, 2, 4, 4>, 32, 32, 256}, 7.4, M >= 2 && N >= 2},
-        {{vec4               ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 4>
-          : M >= 4 && N >= 4 ? sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 0>
-                             : sgemm_grouped_outer_kernel<64, 64, 2, 2, 4, 1>, 64, 64, 256},
-         vec4 ? 14.6 : 17.0, true},
-        {{vec4 ? sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 4>
-               : sgemm_grouped_outer_kernel<128, 128, 2, 2, 2, 0>, 128, 128, 256},
-         vec4 ? 54.0 : 60.0, M >= 4 && N >= 4},
-    };
-    const GroupedTile t = cheapest(choices, tiles, tiles, cus);
-    if (t.fn == nullptr)
-        return -22;
-    gp.p.tiles_m = (int)ceil_div(M, t.bm);
-    gp.p.tiles_n = (int)ceil_div(N, t.bn);
-    return launch_grouped(t, gp, tiles(t.bm, t.bn), reinterpret_cast<hipStream_t>(stream));
+    const Choice c = choose_grouped_outer(M, N, groups, vec4, cus);
+    if (c.kernel < 0)
+        return c.kernel;
+    gp.p.tiles_m = (int)ceil_div(M, c.t.bm);
+    gp.p.tiles_n = (int)ceil_div(N, c.t.bn);
+    return launch_grouped(c.t, gp, (double)gp.p.tiles_m * gp.p.tiles_n * groups,
+                          reinterpret_cast<hipStream_t>(stream));
+}
+
+extern "C" int sgemm_grouped_select_kernel(int transB, int M, int N, int groups, int vec4_ok,
+                                           int num_cus)
+{
+    if (transB != 0 && transB != 1) return -801;
+    if (M < 0) return -802;
+    if (N < 0) return -803;
+    if (groups < 0 || groups > kMaxGroups) return -805;
+    return choose_grouped(transB, M, N, groups, vec4_ok != 0, num_cus > 1 ? num_cus : 1).kernel;
+}
+
+extern "C" int sgemm_grouped_outer_select_kernel(int M, int N, int groups, int vec4_ok,
+                                                 int num_cus)
+{
+    if (M < 0) return -901;
+    if (N < 0) return -902;
+    if (groups < 0) return -904;
+    return choose_grouped_outer(M, N, groups, vec4_ok != 0, num_cus > 1 ? num_cus : 1).kernel;
 }
 
 extern "C" const char *sgemm_status_string(int status)
