@@ -602,7 +602,6 @@ struct I8Core {
     static constexpr int NA = BM * BK / 1024 / NW, NB = BN * BK / 1024 / NW; // blocks a wave loads
     static_assert(NA >= 1 && NB >= 1, "a wave loads of both operands");
     static constexpr int PATCH = 16 * WN * 4; // bytes of LDS a wave's outputs turn over in
-    static constexpr int STORES = TM * 2 * (WN / 16); // a wave's stores of a whole tile
 
     int lane, wave, wm, wn, chunk, o;
     int at[KH];
@@ -789,8 +788,7 @@ struct I8Core {
         }
     }
 
-    // Returns whether the tile was whole (and its stores one a piece).
-    __device__ __forceinline__ bool outputs(const I8Params &p, const I8Tile &t, float *patch) const
+    __device__ __forceinline__ void outputs(const I8Params &p, const I8Tile &t, float *patch) const
     {
         const bool whole = t.m0 + BM <= t.M && t.n0 + BN <= p.N;
         with_type(p.type, [&](auto type) {
@@ -799,7 +797,6 @@ struct I8Core {
             else
                 turn_over<decltype(type), true>(p, t, patch);
         });
-        return whole;
     }
 };
 
