@@ -79,28 +79,28 @@ def declare(lib):
 _INT_MAX = 2**31 - 1  # sizes and leading dimensions are C ints
 
 
+def _in_int(**sizes):
+    """Refuses what would reach the library as another number. (Numbers that are
+    only negative are the library's to refuse.)"""
+    for name, n in sizes.items():
+        if not -_INT_MAX <= n <= _INT_MAX:
+            raise ValueError(f"{name} is {n}: sizes are below 2**31 and not negative")
+
+
 def _span(rows, cols, ld):
     """Elements from the first to the last of `rows` rows, `ld` apart."""
-    if not (-_INT_MAX <= rows <= _INT_MAX and -_INT_MAX <= cols <= _INT_MAX and
-            -_INT_MAX <= ld <= _INT_MAX):
-        raise ValueError(f"{rows} rows of {cols}, {ld} apart: sizes are below 2**31")
+    if 0 < rows <= _INT_MAX and 0 < cols <= ld <= _INT_MAX:
+        return (rows - 1) * ld + cols
+    _in_int(rows=rows, columns=cols, ld=ld)
     return (rows - 1) * ld + cols if rows > 0 and cols > 0 else 0
 
 
 def _spans(groups, stride, rows, cols, ld):
     """The same for `groups` matrices, `stride` apart."""
-    if groups < -_INT_MAX or stride < -_INT_MAX:
-        raise ValueError(f"{groups} matrices, {stride} apart: neither may be negative")
+    if groups < 0 or stride < 0:
+        _in_int(groups=groups, stride=min(stride, 0))
     n = _span(rows, cols, ld)
     return (groups - 1) * stride + n if groups > 0 and n > 0 else 0
-
-
-def _slots(tokens, topk):
-    """Slots of all tokens. (More than an int holds are more than a tensor of
-    theirs has.)"""
-    if tokens < -_INT_MAX or topk < -_INT_MAX:
-        raise ValueError(f"{tokens} tokens of {topk} slots: sizes are positive")
-    return tokens * topk
 
 
 def _first(name, t):
@@ -210,9 +210,11 @@ def expert_sort(tokens, topk, experts, ids, offsets, row_of_slot, workspace, str
     row_of_slot (int32); workspace: a GPU tensor of any type, or None where
     expert_sort_workspace_size() is 0."""
     d = _first("ids", ids)
-    if experts < -_INT_MAX:
-        raise ValueError(f"{experts} experts: sizes are positive")
-    slots = _slots(tokens, topk)
+    if experts < 0:
+        _in_int(experts=experts)
+    slots = tokens * topk
+    if slots < 0:
+        _in_int(tokens=tokens, topk=topk)
     p_ids = _at("ids", ids, _IDS, d, slots, True)
     ws, ws_bytes = None, 0
     if workspace is not None:
@@ -227,7 +229,9 @@ def expert_gather(tokens, topk, cols, X, ldx, row_of_slot, Y, ldy, stream=None, 
     """C ABI ``expert_gather``: Y[row_of_slot[t, j]] = X[t]; X and Y of one
     type, fp32, fp16, bf16 or int8."""
     d = _first("X", X)
-    slots = _slots(tokens, topk)
+    slots = tokens * topk
+    if slots < 0:
+        _in_int(tokens=tokens, topk=topk)
     return _call(_lib.expert_gather, d, stream, check, tokens, topk, cols,
                  _at("X", X, _ANY, d, _span(tokens, cols, ldx)), _TYPES[X.dtype], ldx,
                  _at("row_of_slot", row_of_slot, _I32, d, slots, True),
@@ -239,7 +243,9 @@ def expert_combine(tokens, topk, cols, Y, ldy, row_of_slot, weights, out, ldo, s
     """C ABI ``expert_combine``: out[t] = sum_j weights[t, j] Y[row_of_slot[t,
     j]]; weights fp32, or None for 1 (the gradient of expert_gather)."""
     d = _first("Y", Y)
-    slots = _slots(tokens, topk)
+    slots = tokens * topk
+    if slots < 0:
+        _in_int(tokens=tokens, topk=topk)
     return _call(_lib.expert_combine, d, stream, check, tokens, topk, cols,
                  _at("Y", Y, _FLOATS, d, _span(slots, cols, ldy)), _TYPES[Y.dtype], ldy,
                  _at("row_of_slot", row_of_slot, _I32, d, slots, True),
@@ -252,7 +258,9 @@ def expert_combine_grad(tokens, topk, cols, dout, ldo, Y, ldy, row_of_slot, weig
     """C ABI ``expert_combine_grad``: dY and dweights (fp32, or None: then Y
     may be None too) from dout."""
     d = _first("dout", dout)
-    slots = _slots(tokens, topk)
+    slots = tokens * topk
+    if slots < 0:
+        _in_int(tokens=tokens, topk=topk)
     return _call(_lib.expert_combine_grad, d, stream, check, tokens, topk, cols,
                  _at("dout", dout, _FLOATS, d, _span(tokens, cols, ldo)), _TYPES[dout.dtype], ldo,
                  None if Y is None else _at("Y", Y, (dout.dtype,), d, _span(slots, cols, ldy)),

@@ -272,7 +272,7 @@ def test_binding_refuses_sizes_below_an_int(pg, on_host):
             lambda: pg.sgemm_grouped_outer(1, 1, 1, n, i, 1.0, x, 1, x, 1, 0.0, x, 1, 1),
             lambda: pg.sgemm_grouped_outer(1, 1, 1, 2, make(3, dtype=torch.int32), 1.0, x, 1, x, 1,
                                            0.0, x, 1, big)):
-        with pytest.raises(ValueError, match="below 2|negative|positive"):
+        with pytest.raises(ValueError, match="below 2"):
             bad()
     assert pg.i8gemm(-1, 1, 2, q, 2, s, q, 2, s, None, x, 1)[0] == -1
 
