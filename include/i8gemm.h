@@ -74,7 +74,8 @@ int i8gemm(int M, int N, int K, const signed char *A, int lda, const float *scal
  * (expert_sort writes one); the host never reads it. Groups may be empty. Rows
  * of C before offsets[0] and from offsets[groups] on are left as they were.
  * Values outside [0, M] are brought into that range, and a group whose end
- * lies before its start is empty.
+ * lies before its start is empty; rows that decreasing values put into two
+ * groups get either's values or stay as they were.
  * Positions: M 1 (rows of A and C), N 2, K 3, groups 4, offsets 5, A 6, lda 7,
  * scaleA 8, B 9, ldb 10, strideB 11 (>= 0; 0 shares one B), scaleB 12, C 14,
  * c_type 15, ldc 16. groups == 0: nothing is launched.

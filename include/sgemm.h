@@ -415,7 +415,8 @@ int sgemm_strided_batched_noalloc(int transA, int transB, int M, int N, int K,
  * of rows]; the host never reads it. Groups may be empty. Rows before
  * offsets[0] and from offsets[groups] on are neither read nor written. Values
  * outside the range are brought into it, and a group whose end lies before its
- * start is empty. alpha == 0 or K == 0: as above, A and B are not read. C_g
+ * start is empty (rows of C that decreasing values put into two groups are
+ * undefined). alpha == 0 or K == 0: as above, A and B are not read. C_g
  * must not overlap each other, A or B.
  *
  * Status codes: minus (a base for the call + the position of the first invalid

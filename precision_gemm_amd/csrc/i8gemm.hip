@@ -556,8 +556,9 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
 // same at every wait. Needs 16-byte-aligned rows, K a multiple of 16 and
 // leading dimensions below 2^22 (32-bit offsets within a tile).
 //
-// What bounds the 256 x 256 tile: power. On 8192^3 it runs at 2.50 POP/s (441
-// us), where the library product makes 2.11; the matrix units are busy 55 % of
+// What bounds the 256 x 256 tile: power. 8192^3 runs at 2.37 POP/s (465 us; the
+// library product of integers alone 470 on the same card; other cards 441 to
+// 490), 4096 x 8192 x 4096 takes 126 us (131); the matrix units are busy 55 % of
 // the cycles of a clock that stands at 1.8 GHz. Without its loads the loop takes
 // 17 % less, without its LDS reads 18 %, and on operands of zeros 30 %. Eight
 // waves of 128 x 64 each beat four of 128 x 128 (4001 x 8192 x 4096: 132 us
@@ -959,9 +960,9 @@ int choose_i8(int M, int N, int K, int groups, bool aligned, bool direct, int cu
     int stream = -1;
     if (groups) {
         // Up to 8 rows a group on average: the weights stream (256 rows over
-        // 64 groups, 2048 x 2048: 48.5 us against 51.5 with the 32 x 64 tile;
-        // 512 over 128, 4096 x 1024: 96 against 102; with 16 rows a group 76
-        // against 58).
+        // 64 groups, 2048 x 2048: 51 us against 53.5 with the 32 x 64 tile;
+        // 512 over 128, 4096 x 1024: 97 against 107; with 16 rows a group 72.5
+        // against 55).
         if (M <= 8LL * groups || (!direct && M <= 16LL * groups))
             stream = I8GEMM_KERNEL_S16x32;
     } else if (M <= 16) {
