@@ -13,10 +13,10 @@
  * Matrices are row-major with element strides (leading dimensions) and hold
  * one type a call (an sgemm_type); sorted matrices have tokens*topk rows, of
  * which the last ones, from offsets[experts] on, belong to no slot: what they
- * hold is not used, and they are not written. All pointers are DEVICE pointers owned by the
- * caller. Calls are asynchronous on `stream`, never synchronise the host,
- * allocate nothing, use no floating-point atomics and are deterministic. They
- * launch on the current device, which has to be the stream's. Outputs must not
+ * hold is not used, and they are not written. All pointers are DEVICE pointers
+ * owned by the caller. Calls are asynchronous on `stream`, never synchronise the
+ * host, allocate nothing, use no floating-point atomics and are deterministic.
+ * They launch on the current device, which has to be the stream's. Outputs must not
  * overlap inputs. Matrices need no alignment beyond their elements'. Entries of
  * row_of_slot outside [0, tokens*topk) count as -1; the others have to differ
  * from each other, as expert_sort makes them, where rows are written

@@ -32,9 +32,10 @@ __all__ = [
     "MAX_DISPATCH_OVERRIDES",
     "library_path",
     "i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "I8GEMM_KERNELS",
-    "i8gemm_select_kernel", "expert_sort", "expert_sort_workspace_size", "expert_gather", "expert_combine", "expert_combine_grad",
-    "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped", "sgemm_grouped_outer", "GROUPED_KERNELS",
-    "GROUPED_OUTER_KERNELS", "sgemm_grouped_select_kernel", "sgemm_grouped_outer_select_kernel",
+    "i8gemm_select_kernel", "expert_sort", "expert_sort_workspace_size", "expert_gather",
+    "expert_combine", "expert_combine_grad", "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped",
+    "sgemm_grouped_outer", "GROUPED_KERNELS", "GROUPED_OUTER_KERNELS",
+    "sgemm_grouped_select_kernel", "sgemm_grouped_outer_select_kernel",
     "VARIANT_AUTO", "VARIANT_L256x128", "VARIANT_M128x128", "VARIANT_S64x64",
     "VARIANT_S64x64_V1", "VARIANT_T64x64", "VARIANT_L256x256", "VARIANT_S64x64_K2",
     "VARIANT_M128x128_DMA", "VARIANT_T32x64", "VARIANT_T64x32", "VARIANT_GEMV",
@@ -433,8 +434,8 @@ def matmul(A, B, C, alpha=1.0, beta=0.0, transA=False, transB=False, stream=None
 # on first use: it imports torch, where there is one, which importing this package
 # does not.
 _EXPERTS = ("i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "I8GEMM_KERNELS",
-            "i8gemm_select_kernel", "expert_sort", "expert_sort_workspace_size", "expert_gather", "expert_combine",
-            "expert_combine_grad", "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped",
+            "i8gemm_select_kernel", "expert_sort", "expert_sort_workspace_size", "expert_gather",
+            "expert_combine", "expert_combine_grad", "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped",
             "sgemm_grouped_outer", "GROUPED_KERNELS", "GROUPED_OUTER_KERNELS",
             "sgemm_grouped_select_kernel", "sgemm_grouped_outer_select_kernel")
 

@@ -221,7 +221,8 @@ def test_binding_refuses_vectors_with_gaps(pg, on_host):
     whole = {n: v.contiguous() for n, v in gaps.items()}
     calls = [
         (lambda v: pg.i8_quantize_rows(T, H, x, H, q, H, v["scale"]), ["scale"]),
-        (lambda v: pg.i8gemm(T, N, H, q, H, v["scaleA"], q, H, v["scaleB"][:1], v["bias"][:1], x, H),
+        (lambda v: pg.i8gemm(T, N, H, q, H, v["scaleA"], q, H, v["scaleB"][:1], v["bias"][:1], x,
+                             H),
          ["scaleA"]),
         (lambda v: pg.i8gemm_grouped(T, N, H, E, v["offsets"], q, H, v["scaleA"], q, H, 0,
                                      v["scaleB"], v["bias"], x, H),
@@ -325,7 +326,8 @@ def test_i8_kernel_numbers(pg):
     text = open(os.path.join(ROOT, "include", "i8gemm.h")).read()
     numbers = dict(re.findall(r"I8GEMM_KERNEL_(\w+) = (\d+)", text))
     assert int(numbers.pop("COUNT")) == len(pg.I8GEMM_KERNELS)
-    assert {n: int(v) for n, v in numbers.items()} == {n: i for i, n in enumerate(pg.I8GEMM_KERNELS)}
+    assert {n: int(v) for n, v in numbers.items()} == \
+        {n: i for i, n in enumerate(pg.I8GEMM_KERNELS)}
 
 
 def test_i8_kernels_whose_tiles_fit_a_launch(pg):
