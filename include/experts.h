@@ -25,9 +25,9 @@
  * tokens*topk is at most 2^31 - 1. Status codes: 0 success, a positive
  * hipError_t, or minus (a base for the call + the position of the first
  * invalid argument): 400 for expert_sort, 500 for expert_gather, 600 for
- * expert_combine, 700 for expert_combine_grad; -22 for more rows than a launch
- * holds (over 2^23 tokens with rows of more than 2048 bytes, twice as many for
- * each halving of that). Nothing is launched on error. sgemm_status_string()
+ * expert_combine, 700 for expert_combine_grad, 1700 for expert_layer; -22 for more
+ * rows than a launch holds (over 2^23 tokens with rows of more than 2048 bytes,
+ * twice as many for each halving of that). Nothing is launched on error. sgemm_status_string()
  * gives the message.
  */
 #ifndef PRECISION_GEMM_AMD_EXPERTS_H
@@ -92,6 +92,52 @@ int expert_combine(int tokens, int topk, int cols, const void *Y, int type, int 
 int expert_combine_grad(int tokens, int topk, int cols, const void *dout, int type, int ldo,
                         const void *Y, int ldy, const int *row_of_slot, const float *weights,
                         void *dY, int lddy, float *dweights, sgemm_stream_t stream);
+
+/* Most slots (tokens * topk) and experts expert_layer takes. */
+#define EXPERT_LAYER_MAX_SLOTS 2048
+#define EXPERT_LAYER_MAX_EXPERTS 1024
+
+/*
+ * A whole layer of experts for a few tokens, without a sort, sorted copies or a
+ * launch for each step: with e = ids[t*topk + j],
+ *   g = W1_e[0:F] X[t],  u = W1_e[F:2F] X[t],  a = silu(g) * u  (silu(x) = x / (1 + exp(-x)))
+ *   out[t] = sum_j weights[t*topk + j] * (W2_e a)
+ * W1_e is 2F x H (first the rows of the gate, then those it multiplies) and W2_e
+ * H x F, both with the products' sums along a row: W1 + e*strideW1 with rows ldw1
+ * apart, W2 + e*strideW2 with rows ldw2 apart. X and out are tokens x H of `type`
+ * (F32, F16 or BF16). w_type is the weights':
+ *   - `type` itself; scale1 and scale2 are not used and may be NULL;
+ *   - SGEMM_I8, one fp32 scale a row: scale1[e*2F + i], scale2[e*H + i];
+ *   - SGEMM_MX4, 4-bit blocks as mx4gemm.h lays them out: leading dimensions and
+ *     strides are BYTES, and expert e's scales stand at scale1 + e*((H + 127)/128
+ *     * 2F * 4) with 2F rows, scale2 + e*((F + 127)/128 * H * 4) with H rows.
+ * Slots whose id is outside [0, experts) take part in nothing; a token without
+ * any gets 0. A token may name an expert twice. weights may be NULL (1
+ * everywhere).
+ * Sums run in fp32. a is held as two 16-bit floating-point numbers that together
+ * carry 16 bits of it (F32: all 24, in fp32 or three of them); out is rounded
+ * once, after the sum over j in its order.
+ * Only the experts that the tokens name are read, each once for up to 16 tokens
+ * (of 64 that name it, four at most); beyond a few rows an expert, the sorted
+ * path of expert_sort to expert_combine is the faster one.
+ * workspace: at least expert_layer_workspace_size() bytes, 16-byte aligned, in
+ * use until the work completes on `stream`: calls that overlap (two streams, two
+ * captured graphs) need one each. Its contents need no preparation.
+ * Positions: tokens 1 (tokens*topk at most EXPERT_LAYER_MAX_SLOTS), topk 2 (>=
+ * 1), experts 3 (1 to EXPERT_LAYER_MAX_EXPERTS), H 4, F 5 (each at most 2^20), X 6, type 7, ldx 8,
+ * ids 9, id_bytes 10 (4: int32, 8: int64; contiguous), W1 12, w_type 13, ldw1 14,
+ * strideW1 15 (>= 0), scale1 16, W2 17, ldw2 18, strideW2 19, scale2 20, out 21,
+ * ldo 22, workspace 23, workspace_bytes 24. tokens == 0 or H == 0: nothing is
+ * launched; F == 0 sets out to 0.
+ */
+int expert_layer(int tokens, int topk, int experts, int H, int F, const void *X, int type, int ldx,
+                 const void *ids, int id_bytes, const float *weights, const void *W1, int w_type,
+                 int ldw1, long long strideW1, const void *scale1, const void *W2, int ldw2,
+                 long long strideW2, const void *scale2, void *out, int ldo, void *workspace,
+                 size_t workspace_bytes, sgemm_stream_t stream);
+
+/* Bytes of workspace of expert_layer (0 for invalid arguments). */
+size_t expert_layer_workspace_size(int tokens, int topk, int H, int F, int type);
 
 #ifdef __cplusplus
 }

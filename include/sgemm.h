@@ -80,8 +80,11 @@ extern "C" {
 
 typedef void *sgemm_stream_t; /* hipStream_t; NULL = the default stream */
 
-/* Element types of the calls that take one (i8gemm.h, experts.h). */
-enum sgemm_type { SGEMM_F32 = 0, SGEMM_F16 = 1, SGEMM_BF16 = 2, SGEMM_I8 = 3 };
+/* Element types of the calls that take one (i8gemm.h, experts.h, norm.h, mx4gemm.h); MX4:
+   4-bit blocks as mx4gemm.h lays them out. */
+enum sgemm_type {
+    SGEMM_F32 = 0, SGEMM_F16 = 1, SGEMM_BF16 = 2, SGEMM_I8 = 3, SGEMM_MX4 = 4
+};
 
 /* C = alpha * op(A) @ op(B) + beta * C for one matrix triple (batch = 1). */
 int sgemm(int transA, int transB, int M, int N, int K,

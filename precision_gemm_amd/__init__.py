@@ -1,8 +1,8 @@
 """precision_gemm_amd — single-precision GEMM on MI355X (gfx950).
 
 A thin ctypes binding over ``libsgemm.so`` (built from ``csrc/``; its C ABI is
-declared in ``include/sgemm.h``, ``include/i8gemm.h`` and
-``include/experts.h``). The functions have the C
+declared in ``include/sgemm.h``, ``include/i8gemm.h``, ``include/experts.h``,
+``include/norm.h`` and ``include/mx4gemm.h``). The functions have the C
 names and argument order; they only marshal arguments (tensor -> device
 pointer, torch's current stream -> hipStream_t) and raise on a nonzero
 status. All arithmetic runs in the library's HIP kernels; there is no CPU or
@@ -14,7 +14,11 @@ Next to it stand the products of a mixture layer's experts: rows sorted by
 expert and back (expert_sort, expert_gather, expert_combine and its gradient),
 their fp32 products (sgemm_grouped, sgemm_grouped_outer), and products in 8-bit
 integers with scales for each token and channel (i8_quantize_rows, i8gemm,
-i8gemm_grouped).
+i8gemm_grouped). Beside those: the root-mean-square norm with the residual's
+addition, its 8-bit output and its gradients (rms_norm, rms_norm_i8,
+rms_norm_grad), products in 4-bit floating point with shared scales
+(mx4_quantize_rows, mx4_dequantize_rows, mx4gemm, mx4gemm_grouped), and a whole
+layer of experts for a few tokens (expert_layer).
 """
 from __future__ import annotations
 
@@ -36,6 +40,10 @@ __all__ = [
     "expert_combine", "expert_combine_grad", "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped",
     "sgemm_grouped_outer", "GROUPED_KERNELS", "GROUPED_OUTER_KERNELS",
     "sgemm_grouped_select_kernel", "sgemm_grouped_outer_select_kernel",
+    "rms_norm", "rms_norm_i8", "rms_norm_grad", "rms_norm_grad_workspace_size",
+    "RMS_NORM_GRAD_MAX_K", "mx4_quantize_rows", "mx4_dequantize_rows", "mx4gemm",
+    "mx4gemm_grouped", "expert_layer", "expert_layer_workspace_size", "EXPERT_LAYER_MAX_SLOTS",
+    "EXPERT_LAYER_MAX_EXPERTS",
     "VARIANT_AUTO", "VARIANT_L256x128", "VARIANT_M128x128", "VARIANT_S64x64",
     "VARIANT_S64x64_V1", "VARIANT_T64x64", "VARIANT_L256x256", "VARIANT_S64x64_K2",
     "VARIANT_M128x128_DMA", "VARIANT_T32x64", "VARIANT_T64x32", "VARIANT_GEMV",
@@ -149,6 +157,8 @@ def _load():
     lib.sgemm_dispatch_override_count.argtypes = []
     from . import _experts
     _experts.declare(lib)
+    from . import _layers
+    _layers.declare(lib)
     _lib = lib
     return lib
 
@@ -438,11 +448,19 @@ _EXPERTS = ("i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "I8G
             "expert_combine", "expert_combine_grad", "EXPERT_SORT_MAX_EXPERTS", "sgemm_grouped",
             "sgemm_grouped_outer", "GROUPED_KERNELS", "GROUPED_OUTER_KERNELS",
             "sgemm_grouped_select_kernel", "sgemm_grouped_outer_select_kernel")
+_LAYERS = ("rms_norm", "rms_norm_i8", "rms_norm_grad", "rms_norm_grad_workspace_size",
+           "RMS_NORM_GRAD_MAX_K", "mx4_quantize_rows", "mx4_dequantize_rows", "mx4gemm",
+           "mx4gemm_grouped", "expert_layer", "expert_layer_workspace_size",
+           "EXPERT_LAYER_MAX_SLOTS", "EXPERT_LAYER_MAX_EXPERTS")
 
 
 def __getattr__(name):
     if name in _EXPERTS:
         from . import _experts
         value = globals()[name] = getattr(_experts, name)
+        return value
+    if name in _LAYERS:
+        from . import _layers
+        value = globals()[name] = getattr(_layers, name)
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -15,7 +15,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("sgemm.hip", "i8gemm.hip", "experts.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("sgemm.hip", "i8gemm.hip", "experts.hip", "norm.hip",
+                                             "mx4gemm.hip", "expert_layer.hip")]
 LIB = os.path.join(PKG, "libsgemm.so")
 INCLUDE = os.path.join(ROOT, "include")
 ARCH = "gfx950"

@@ -335,16 +335,6 @@ __global__ void __launch_bounds__(256) expert_gather_kernel(RowParams p)
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void unpack(i32x4 v, float (&x)[16 / sizeof(T)])
-{
-    typedef T tv __attribute__((ext_vector_type(16 / sizeof(T))));
-    const tv h = __builtin_bit_cast(tv, v);
-#pragma unroll
-    for (int i = 0; i < (int)(16 / sizeof(T)); ++i)
-        x[i] = (float)h[i];
-}
-
 // 16 bytes of a row from byte b on as floats, zeros behind the row's end.
 template <typename T>
 __device__ __forceinline__ void load_chunk(const char *row, int b, int bytes,

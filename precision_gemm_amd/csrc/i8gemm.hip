@@ -5,7 +5,6 @@
 
 #include "i8gemm.h"
 
-#include <atomic>
 #include <type_traits>
 
 namespace {
@@ -13,38 +12,6 @@ namespace {
 // ---------------------------------------------------------------------------
 // Row quantization
 // ---------------------------------------------------------------------------
-
-constexpr float kLeastScale = 1.17549435e-38f; // 2^-126
-
-// The integer nearest to x / s (ties to even), |x / s| < 127.5. r, from a
-// product with the reciprocal, can be one off next to a tie; d = x - r s is
-// exact (for r = 0 it is x, for r = +-1 the subtraction of numbers within a
-// factor of two, or, for x just below s / 2, one that rounds to no less than
-// s / 2; beyond that a multiple of s's last place below 2^24 of them), and so is
-// 2 d, so comparing that with s puts r right. (s / 2 would not be exact: from
-// 2^-126 to 2^-125 half of an odd last place is no number.)
-__device__ __forceinline__ int quantize_one(float x, float s, float inv)
-{
-    float r = __builtin_rintf(x * inv);
-    const float d = __builtin_fmaf(-r, s, x);
-    const float twice = 2.0f * __builtin_fabsf(d);
-    const bool odd = ((int)r) & 1;
-    if (twice > s || (twice == s && odd))
-        r += d > 0.0f ? 1.0f : -1.0f;
-    return (int)r;
-}
-
-// The 16 bytes of a chunk as floats.
-template <typename T>
-__device__ __forceinline__ void unpack(i32x4 v, float (&x)[16 / sizeof(T)])
-{
-    constexpr int VEC = 16 / sizeof(T);
-    typedef T tv __attribute__((ext_vector_type(VEC)));
-    const tv h = __builtin_bit_cast(tv, v);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-        x[i] = (float)h[i];
-}
 
 // NT threads a row (below 256: 256 / NT rows a workgroup), which hold the row
 // in registers, CH chunks of 16 bytes each, between its maximum and its
@@ -268,17 +235,6 @@ __device__ __forceinline__ bool i8_tile_of(const I8Params &p, I8Tile &t)
     return true;
 }
 
-template <typename F>
-__device__ __forceinline__ void with_type(int type, F f)
-{
-    if (type == SGEMM_F32)
-        f(float{});
-    else if (type == SGEMM_F16)
-        f(_Float16{});
-    else
-        f(__bf16{});
-}
-
 __device__ __forceinline__ void store_c(const I8Params &p, long long at, float v)
 {
     with_type(p.type, [&](auto t) { static_cast<decltype(t) *>(p.C)[at] = (decltype(t))v; });
@@ -288,47 +244,6 @@ __device__ __forceinline__ void store_c(const I8Params &p, long long at, float v
 __device__ __forceinline__ float scaled(float acc, float sa, float sb, float bias)
 {
     return __builtin_fmaf(acc * sa, sb, bias);
-}
-
-// Four neighbouring outputs at any address.
-template <typename T>
-__device__ __forceinline__ void store4(T *c, f32x4 x)
-{
-    typedef T t4 __attribute__((ext_vector_type(4)));
-    const t4 h = {(T)x[0], (T)x[1], (T)x[2], (T)x[3]};
-    if constexpr (sizeof(T) == 4)
-        store16(c, __builtin_bit_cast(i32x4, h));
-    else
-        *reinterpret_cast<i32x2_any *>(c) = __builtin_bit_cast(i32x2, h);
-}
-
-// 16 bytes of a row from its byte k on, zeros from byte K on; nothing outside
-// the row's K bytes is read. The chunk that K ends in comes from the row's last
-// 16 bytes, moved down.
-__device__ __forceinline__ i32x4 row_chunk(const signed char *row, int k, int K)
-{
-    if (k + 16 <= K)
-        return load16(row + k);
-    if (k >= K)
-        return i32x4{0, 0, 0, 0};
-    if (K >= 16) {
-        const int n = k + 16 - K; // 1 to 15 bytes down
-        i32x4 v = load16(row + K - 16);
-        if (n & 4)
-            v = i32x4{v[1], v[2], v[3], 0};
-        if (n & 8)
-            v = i32x4{v[2], v[3], 0, 0};
-        return i32x4{(int)__builtin_amdgcn_alignbyte(v[1], v[0], n & 3),
-                     (int)__builtin_amdgcn_alignbyte(v[2], v[1], n & 3),
-                     (int)__builtin_amdgcn_alignbyte(v[3], v[2], n & 3),
-                     (int)__builtin_amdgcn_alignbyte(0, v[3], n & 3)};
-    }
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 15; ++i)
-        if (k + i < K)
-            w[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
-    return i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
 }
 
 // The tile for every alignment: 64 T x 64 T of C by four waves, each one T x T
@@ -564,37 +479,6 @@ __global__ void __launch_bounds__(64 * WAVES) i8_stream_kernel(I8Params p)
 // waves of 128 x 64 each beat four of 128 x 128 (4001 x 8192 x 4096: 132 us
 // against 144), whose outputs leave one wave a SIMD idle.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kOutside = 0x80000000u;
-constexpr int kMaxTileLd = 1 << 22;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const signed char *base, long long bytes)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<signed char *>(base), (short)0,
-                                             (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff),
-                                             0x00020000);
-}
-
-// vmcnt <= N, lgkmcnt and expcnt as they are.
-template <int N>
-__device__ __forceinline__ void wait_loads()
-{
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
-// All waves meet: N of this wave's memory operations may still be under way,
-// its LDS reads are done.
-template <int N>
-__device__ __forceinline__ void meet()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-    wait_loads<N>();
-    __builtin_amdgcn_s_waitcnt(0xc07f); // lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
 template <int BM, int BN, int WAVES_M, int WAVES_N>
 struct I8Core {
     static constexpr int BK = 128, KH = BK / 32, NW = WAVES_M * WAVES_N;
@@ -863,26 +747,6 @@ i8_large_kernel(I8Params p)
     i8_large_tile<BM, BN, WAVES_M, WAVES_N, STAGES>(p, lds);
 }
 
-int current_cus(int *out)
-{
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess)
-        return (int)e;
-    const bool cached = dev >= 0 && dev < 64;
-    int cus = cached ? cache[dev].load(std::memory_order_relaxed) : 0;
-    if (cus == 0) {
-        e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-        if (e != hipSuccess)
-            return (int)e;
-        if (cached)
-            cache[dev].store(cus, std::memory_order_relaxed);
-    }
-    *out = cus;
-    return 0;
-}
-
 typedef void (*I8Fn)(I8Params);
 
 struct I8Variant {
@@ -942,9 +806,6 @@ long long i8_row_tiles(int M, int groups, int bm)
 {
     return groups ? most_tiles(M, groups, bm) : ceil_div_ll(M, bm);
 }
-
-// Whether a launch holds `tiles` workgroups: fewer than 2^32 work-items.
-bool fits_launch(double tiles, int threads) { return tiles * threads <= 4294967295.0; }
 
 // The kernel of a call (an i8gemm_kernel), or -22 if the tiles of none fit a
 // launch. Those whose tiles do not are passed over. Times below are graph
@@ -1052,8 +913,6 @@ int launch_i8(I8Params p, hipStream_t s)
                                 dim3((unsigned)((long long)p.tiles_m * p.tiles_n)),
                                 dim3(v.threads), args, 0, s);
 }
-
-bool c_type_ok(int type) { return type == SGEMM_F32 || type == SGEMM_F16 || type == SGEMM_BF16; }
 
 } // namespace
 
