@@ -102,6 +102,40 @@ int mx4gemm_grouped(int M, int N, int K, int groups, const int *offsets, const u
                     long long strideB, const unsigned char *scaleB, int ldsb, long long strideSB,
                     const float *bias, void *C, int c_type, int ldc, sgemm_stream_t stream);
 
+/*
+ * Kernels the two calls choose among (see mx4gemm_select_kernel): the tile of C
+ * one workgroup owns. The order of a sum, and with it its last bits, depends on
+ * the kernel.
+ */
+enum mx4gemm_kernel {
+    /* B streams from memory into registers, K split over the waves */
+    MX4GEMM_KERNEL_S16x16 = 0, /* 8 waves */
+    MX4GEMM_KERNEL_S16x32 = 1, /* 4 waves */
+    MX4GEMM_KERNEL_S32x16 = 2, /* 8 waves */
+    MX4GEMM_KERNEL_S32x32 = 3, /* 8 waves */
+    MX4GEMM_KERNEL_S32x64 = 4, /* 4 waves */
+    /* K-steps through registers to LDS: rows of any alignment */
+    MX4GEMM_KERNEL_T64x64 = 5,
+    MX4GEMM_KERNEL_T128x128 = 6,
+    /* K-steps straight into LDS: the fast kernels (see Alignment above) */
+    MX4GEMM_KERNEL_L64x64 = 7,
+    MX4GEMM_KERNEL_L64x128 = 8,
+    MX4GEMM_KERNEL_L128x128 = 9,
+    MX4GEMM_KERNEL_L128x256 = 10,
+    MX4GEMM_KERNEL_L256x256 = 11,
+    MX4GEMM_KERNEL_COUNT = 12
+};
+
+/*
+ * Host-side dispatch decision, exposed for tests and tuning (no device call):
+ * the kernel that mx4gemm (groups == 0) or mx4gemm_grouped launches for this
+ * shape, given whether rows start on 16-byte boundaries (`aligned`; leading
+ * dimensions are taken to be below 2^22) and the device's compute-unit count.
+ * Returns an mx4gemm_kernel, -22 for more output tiles than a launch of any
+ * kernel that takes the call holds, or a negative status for invalid sizes.
+ */
+int mx4gemm_select_kernel(int M, int N, int K, int groups, int aligned, int num_cus);
+
 #ifdef __cplusplus
 }
 #endif

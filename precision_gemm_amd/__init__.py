@@ -42,8 +42,8 @@ __all__ = [
     "sgemm_grouped_select_kernel", "sgemm_grouped_outer_select_kernel",
     "rms_norm", "rms_norm_i8", "rms_norm_grad", "rms_norm_grad_workspace_size",
     "RMS_NORM_GRAD_MAX_K", "mx4_quantize_rows", "mx4_dequantize_rows", "mx4gemm",
-    "mx4gemm_grouped", "expert_layer", "expert_layer_workspace_size", "EXPERT_LAYER_MAX_SLOTS",
-    "EXPERT_LAYER_MAX_EXPERTS",
+    "mx4gemm_grouped", "mx4gemm_select_kernel", "MX4GEMM_KERNELS", "expert_layer",
+    "expert_layer_workspace_size", "EXPERT_LAYER_MAX_SLOTS", "EXPERT_LAYER_MAX_EXPERTS",
     "VARIANT_AUTO", "VARIANT_L256x128", "VARIANT_M128x128", "VARIANT_S64x64",
     "VARIANT_S64x64_V1", "VARIANT_T64x64", "VARIANT_L256x256", "VARIANT_S64x64_K2",
     "VARIANT_M128x128_DMA", "VARIANT_T32x64", "VARIANT_T64x32", "VARIANT_GEMV",
@@ -450,8 +450,8 @@ _EXPERTS = ("i8_quantize_rows", "i8gemm", "i8gemm_grouped", "I8GEMM_MAX_K", "I8G
             "sgemm_grouped_select_kernel", "sgemm_grouped_outer_select_kernel")
 _LAYERS = ("rms_norm", "rms_norm_i8", "rms_norm_grad", "rms_norm_grad_workspace_size",
            "RMS_NORM_GRAD_MAX_K", "mx4_quantize_rows", "mx4_dequantize_rows", "mx4gemm",
-           "mx4gemm_grouped", "expert_layer", "expert_layer_workspace_size",
-           "EXPERT_LAYER_MAX_SLOTS", "EXPERT_LAYER_MAX_EXPERTS")
+           "mx4gemm_grouped", "mx4gemm_select_kernel", "MX4GEMM_KERNELS", "expert_layer",
+           "expert_layer_workspace_size", "EXPERT_LAYER_MAX_SLOTS", "EXPERT_LAYER_MAX_EXPERTS")
 
 
 def __getattr__(name):

@@ -18,6 +18,10 @@ from ._experts import _at, _first, _in_int, _span, _spans
 RMS_NORM_GRAD_MAX_K = 16384
 EXPERT_LAYER_MAX_SLOTS = 2048
 EXPERT_LAYER_MAX_EXPERTS = 1024
+# Kernels of the 4-bit product by number (mx4gemm_kernel of the C header): S
+# stream B, T take rows of any alignment, L load straight into LDS.
+MX4GEMM_KERNELS = ("S16x16", "S16x32", "S32x16", "S32x32", "S32x64", "T64x64", "T128x128",
+                   "L64x64", "L64x128", "L128x128", "L128x256", "L256x256")
 
 torch = _experts.torch
 if torch is not None:
@@ -41,11 +45,13 @@ def declare(lib):
     lib.mx4_dequantize_rows.argtypes = [i, i, p, i, p, i, p, i, i, p]
     lib.mx4gemm.argtypes = [i, i, i, p, i, p, i, p, i, p, i, p, p, i, i, p]
     lib.mx4gemm_grouped.argtypes = [i, i, i, i, p, p, i, p, i, p, i, ll, p, i, ll, p, p, i, i, p]
+    lib.mx4gemm_select_kernel.argtypes = [i, i, i, i, i, i]
     lib.expert_layer.argtypes = [i, i, i, i, i, p, i, i, p, i, p, p, i, i, ll, p, p, i, ll, p, p,
                                  i, p, sz, p]
     lib.expert_layer_workspace_size.argtypes = [i, i, i, i, i]
     for name in ("rms_norm", "rms_norm_i8", "rms_norm_grad", "mx4_quantize_rows",
-                 "mx4_dequantize_rows", "mx4gemm", "mx4gemm_grouped", "expert_layer"):
+                 "mx4_dequantize_rows", "mx4gemm", "mx4gemm_grouped", "expert_layer",
+                 "mx4gemm_select_kernel"):
         getattr(lib, name).restype = i
     lib.rms_norm_grad_workspace_size.restype = sz
     lib.expert_layer_workspace_size.restype = sz
@@ -175,6 +181,12 @@ def mx4gemm_grouped(M, N, K, groups, offsets, A, lda, scaleA, ldsa, B, ldb, stri
                  strideSB,
                  None if bias is None else _at("bias", bias, _F32, d, groups * N, True),
                  _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
+
+
+def mx4gemm_select_kernel(M, N, K, groups, aligned, num_cus) -> int:
+    """C ABI ``mx4gemm_select_kernel`` (host-side dispatch decision): an index of
+    MX4GEMM_KERNELS, or a negative status."""
+    return _pg._load().mx4gemm_select_kernel(M, N, K, groups, int(bool(aligned)), num_cus)
 
 
 def expert_layer_workspace_size(tokens, topk, H, F, dtype) -> int:

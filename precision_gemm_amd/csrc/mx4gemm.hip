@@ -412,6 +412,459 @@ __global__ void __launch_bounds__(256) mx4_tile_kernel(Mx4Params p)
     });
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: the weights' bytes bound the call, so they go from memory straight
+// into the matrix instructions' registers, once, and no LDS stage stands
+// between. A workgroup owns 16 * NT channels and up to 16 * MT rows; its WAVES
+// waves take every WAVES-th block of 128 * U of k, so all of a short K is in
+// flight at once, and their sums are added in LDS, in the waves' order.
+// v_mfma_scale_f32_16x16x128: lane l supplies the block l / 16 of row l % 16 and
+// its scale, a byte of the word that the row's four lanes load alike; register v
+// of lane l holds row 4 (l / 16) + v, column l % 16. Rows behind the last repeat
+// it and are not stored.
+// ---------------------------------------------------------------------------
+template <int MT, int NT, int WAVES, int U>
+__global__ void __launch_bounds__(64 * WAVES) mx4_stream_kernel(Mx4Params p)
+{
+    constexpr int BM = 16 * MT, BN = 16 * NT;
+    __shared__ float sums[WAVES][BM][BN];
+    Mx4Tile t;
+    if (!mx4_tile_of<BM, BN>(p, t))
+        return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    const signed char *ra[MT], *rb[NT];
+    const uint32_t *pa[MT], *pb[NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int m = min(t.m0 + 16 * i + r, t.M - 1);
+        ra[i] = t.A + (long long)m * p.lda + 16 * q;
+        pa[i] = t.sA + m;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int n = min(t.n0 + 16 * j + r, p.N - 1);
+        rb[j] = t.B + (long long)n * p.ldb + 16 * q;
+        pb[j] = t.sB + n;
+    }
+
+    f32x4 acc[MT][NT] = {};
+    auto products = [&](const i32x4 (&fa)[MT], const uint32_t (&sa)[MT], const i32x4 (&fb)[NT],
+                        const uint32_t (&sb)[NT]) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    operand(fa[i]), operand(fb[j]), acc[i][j], kFp4, kFp4, 0,
+                    (int)(sa[i] >> (8 * q)), 0, (int)(sb[j] >> (8 * q)));
+    };
+    const int words = (p.K + 127) >> 7, whole = p.K >> 7; // words of scales; full steps
+    int s = wave * U;
+    for (; s + U <= whole; s += WAVES * U) {
+        i32x4 fb[U][NT], fa[U][MT];
+        uint32_t sb[U][NT], sa[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                fb[u][j] = load16(rb[j] + 64LL * (s + u));
+                sb[u][j] = pb[j][(long long)(s + u) * p.ldsb];
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                fa[u][i] = load16(ra[i] + 64LL * (s + u));
+                sa[u][i] = pa[i][(long long)(s + u) * p.ldsa];
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            products(fa[u], sa[u], fb[u], sb[u]);
+    }
+    // The block at the rows' end.
+    for (; s < words && s < (words + U - 1) / U * U; ++s) {
+        if (s >= words || s / U % WAVES != wave)
+            break;
+        i32x4 fb[NT], fa[MT];
+        uint32_t sb[NT], sa[MT];
+        const uint32_t mask = scale_mask(s, p.K);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            fb[j] = mx4_chunk(rb[j] - 16 * q, 64 * s + 16 * q, p.K);
+            sb[j] = pb[j][(long long)s * p.ldsb] & mask;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            fa[i] = mx4_chunk(ra[i] - 16 * q, 64 * s + 16 * q, p.K);
+            sa[i] = pa[i][(long long)s * p.ldsa] & mask;
+        }
+        products(fa, sa, fb, sb);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                sums[wave][16 * i + 4 * q + v][16 * j + r] = acc[i][j][v];
+    __syncthreads();
+    const int rows = min(BM, t.M - t.m0);
+    for (int e = tid; e < rows * BN; e += 64 * WAVES) {
+        const int m = e / BN, n = t.n0 + e % BN;
+        if (n >= p.N)
+            continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            sum += sums[w][m][e % BN];
+        if (t.bias)
+            sum += t.bias[n];
+        const long long at = (t.row0 + t.m0 + m) * p.ldc + n;
+        with_type(p.type, [&](auto type) {
+            static_cast<decltype(type) *>(p.C)[at] = (decltype(type))sum;
+        });
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Larger products: BM x BN of C by WAVES_M x WAVES_N waves, K in steps of 256
+// (128 bytes a row) that go straight from memory to LDS (buffer_load ... lds)
+// through a ring of STAGES stages, as the 8-bit product's do. Lane l of a load
+// fills the l-th 16 bytes of a 1 KiB block, 8 rows of 128 bytes: whole cache
+// lines. LDS rows are 128 bytes, two of them one sweep of the 64 banks: the
+// 16-byte chunk index is XORed with row / 2, on the memory side, for
+// conflict-free reads. Behind a stage's rows stand their scales, two words a
+// row: 64 neighbouring rows' words a load. Lanes of the lower half of a wave
+// take the first four chunks of a row's eight and the first word, those of the
+// upper half the others, so that the k-group's number is the byte of the word
+// that the instruction takes (the order of k within a sum is free). A lane whose
+// chunk or word lies behind K fetches zeros from a 2^31 byte offset, outside the
+// buffer; the bytes of a row's last word that belong to no block are masked.
+// Loads are issued for steps past the last too (of zeros), so that the number in
+// flight is the same at every wait. Needs 16-byte-aligned rows, K a multiple of
+// 32 and leading dimensions below 2^22 (32-bit offsets within a tile).
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WAVES_M, int WAVES_N>
+struct Mx4Core {
+    static constexpr int BK = 128, KH = BK / 32, NW = WAVES_M * WAVES_N; // (bytes of a row)
+    static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 32, TN = WN / 32;
+    static constexpr int WORDS = (BM + BN) * BK; // the scales' offset in a stage
+    static constexpr int STAGE = WORDS + (BM + BN) * 8;
+    static constexpr int NA = BM * BK / 1024 / NW, NB = BN * BK / 1024 / NW; // blocks a wave loads
+    // Loads of 64 words: of A's rows' first words, their second ones, B's. Waves
+    // beyond the last repeat an earlier load, into the same place.
+    static constexpr int SLOADS = (BM + BN) / 32, NS = (SLOADS + NW - 1) / NW;
+    static constexpr int LOADS = NA + NB + NS;
+    static_assert(NA >= 1 && NB >= 1, "a wave loads of both operands");
+    static_assert(BM % 64 == 0 && BN % 64 == 0, "a load's words belong to one operand");
+    static constexpr int PATCH = 16 * WN * 4; // bytes of LDS a wave's outputs turn over in
+
+    int lane, wave, wm, wn, chunk, o, half;
+    int at[KH];
+    // The operands that loads are issued of.
+    const signed char *A, *B;
+    const uint32_t *sA, *sB;
+    long long bytesA, bytesB;
+    int K, words, ldsa, ldsb;
+    uint32_t offA[NA], offB[NB], offS[NS];
+    f32x16 acc[TM][TN];
+    i32x4 fa[2][TM], fb[2][TN]; // of k-groups by parity
+    int wa[TM], wb[TN];         // words of scales of the step
+    float bias[4];              // of the four columns that the lane stores
+
+    __device__ __forceinline__ void init()
+    {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        // (Waves that share a SIMD, four apart, lie above one another in M.)
+        wm = (wave / WAVES_N) * WM;
+        wn = (wave % WAVES_N) * WN;
+        chunk = 16 * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+        // This lane's 16 bytes of k-group q in row 32 i + l % 32 of the wave's
+        // part; 32 rows on is a fixed distance.
+        o = lane & 31;
+        half = lane >> 5;
+#pragma unroll
+        for (int q = 0; q < KH; ++q)
+            at[q] = o * BK + 16 * ((4 * half + q) ^ ((o >> 1) & 7));
+    }
+
+    // Which rows' words load i of this wave holds.
+    __device__ __forceinline__ void word_load(int i, bool &ofA, int &second, int &row) const
+    {
+        int n = (wave + NW * i) % SLOADS;
+        ofA = n < BM / 32;
+        n -= ofA ? 0 : BM / 32;
+        const int each = (ofA ? BM : BN) / 64 > 0 ? (ofA ? BM : BN) / 64 : 1;
+        second = n / each;
+        row = 64 * (n % each);
+    }
+
+    __device__ __forceinline__ void operands(const Mx4Params &p, const Mx4Tile &t)
+    {
+        const int bytes = p.K / 2;
+        A = t.A + (long long)t.m0 * p.lda;
+        B = t.B + (long long)t.n0 * p.ldb;
+        sA = t.sA + t.m0;
+        sB = t.sB + t.n0;
+        bytesA = (long long)(t.M - t.m0 - 1) * p.lda + bytes;
+        bytesB = (long long)(p.N - t.n0 - 1) * p.ldb + bytes;
+        K = bytes;
+        words = (p.K + 127) >> 7;
+        ldsa = p.ldsa;
+        ldsb = p.ldsb;
+        // (Rows behind the last repeat it; they are not stored.)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            offA[i] = (uint32_t)(min(8 * (wave + NW * i) + (lane >> 3), t.M - t.m0 - 1) * p.lda + chunk);
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            offB[i] = (uint32_t)(min(8 * (wave + NW * i) + (lane >> 3), p.N - t.n0 - 1) * p.ldb + chunk);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            bool ofA;
+            int second, row;
+            word_load(i, ofA, second, row);
+            offS[i] = 4u * (uint32_t)min(row + lane, ofA ? t.M - t.m0 - 1 : p.N - t.n0 - 1);
+        }
+    }
+
+    // The loads of a step into a stage; of zeros for a step past the last.
+    __device__ __forceinline__ void issue(int step, signed char *to) const
+    {
+        typedef __attribute__((address_space(3))) void lds_void;
+        const __amdgpu_buffer_rsrc_t rsA = rows_rsrc(A, bytesA), rsB = rows_rsrc(B, bytesB);
+        const int k = step * BK;
+        const uint32_t off = k + chunk < K ? 0u : kOutside;
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsA, (lds_void *)(to + 1024 * (wave + NW * i)), 16, offA[i] | off, k, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsB, (lds_void *)(to + BM * BK + 1024 * (wave + NW * i)), 16, offB[i] | off, k, 0,
+                0);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            bool ofA;
+            int second, row;
+            word_load(i, ofA, second, row);
+            const int word = 2 * step + second;
+            // (The word's row of the scales as the base: no offset grows with K.)
+            const uint32_t *base = (ofA ? sA : sB) + (long long)min(word, words - 1) * (ofA ? ldsa : ldsb);
+            const __amdgpu_buffer_rsrc_t rs =
+                rows_rsrc(reinterpret_cast<const signed char *>(base), 1 << 12);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (lds_void *)(to + WORDS + 256 * ((wave + NW * i) % SLOADS)), 4,
+                offS[i] | (word < words ? 0u : kOutside), 0, 0, 0);
+        }
+    }
+
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = f32x16{};
+    }
+
+    __device__ __forceinline__ void read(const signed char *stage, int q)
+    {
+        const signed char *a = stage + wm * BK + at[q], *b = stage + (BM + wn) * BK + at[q];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa[q & 1][i] = *reinterpret_cast<const i32x4 *>(a + 32 * BK * i);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            fb[q & 1][j] = *reinterpret_cast<const i32x4 *>(b + 32 * BK * j);
+    }
+
+    // The step's words of scales, without the bytes of blocks that are none.
+    __device__ __forceinline__ void read_words(const signed char *stage, int step)
+    {
+        const int left = (K >> 4) - 4 * (2 * step + half); // blocks from the lane's word on
+        const int mask = left >= 4 ? -1 : left <= 0 ? 0 : (1 << (8 * left)) - 1;
+        const int *w = reinterpret_cast<const int *>(stage + WORDS) + half * BM + wm + o;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            wa[i] = w[32 * i] & mask;
+        w = reinterpret_cast<const int *>(stage + WORDS) + 2 * BM + half * BN + wn + o;
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            wb[j] = w[32 * j] & mask;
+    }
+
+    template <int q> __device__ __forceinline__ void products()
+    {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    operand(fa[q & 1][i]), operand(fb[q & 1][j]), acc[i][j], kFp4, kFp4, q, wa[i],
+                    q, wb[j]);
+    }
+
+    // All but the last k-group of the step in `stage` (whose first one is read).
+    __device__ __forceinline__ void step_front(const signed char *stage)
+    {
+        front<0>(stage);
+        front<1>(stage);
+        front<2>(stage);
+    }
+
+    template <int q> __device__ __forceinline__ void front(const signed char *stage)
+    {
+        read(stage, q + 1);
+        products<q>();
+        __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+    }
+
+    // The last k-group, with the first one of the next step's stage read and
+    // the loads of step `ahead` issued under its products.
+    __device__ __forceinline__ void step_back(const signed char *next, int ahead, signed char *to)
+    {
+        read(next, 0);
+        issue(ahead, to);
+        products<KH - 1>();
+        constexpr int GAP = TM * TN / LOADS > 0 ? TM * TN / LOADS : 1;
+        __builtin_amdgcn_sched_group_barrier(0x100, TM + TN, 0);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, GAP, 0);
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    __device__ __forceinline__ void load_bias(const Mx4Params &p, const Mx4Tile &t)
+    {
+        const int n = t.n0 + wn + 4 * (lane % (WN / 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            bias[e] = t.bias ? t.bias[min(n + e, p.N - 1)] : 0.0f;
+    }
+
+    // The wave's outputs, 16 rows at a time through a patch of LDS of its own,
+    // so that a row's leave as 16-byte (fp32) or 8-byte pieces. Rows 4 apart,
+    // which one write instruction holds, are 32 banks apart by the XOR. EDGE:
+    // the tile reaches past M or N.
+    template <typename T, bool EDGE>
+    __device__ __forceinline__ void turn_over(const Mx4Params &p, const Mx4Tile &t, float *patch) const
+    {
+        constexpr int PER = WN / 4, RPI = 64 / PER; // lanes a row, rows a store
+        const int r = lane / PER, c = 4 * (lane % PER);
+        const int n = t.n0 + wn + c;
+        const int left = t.M - (t.m0 + wm); // the wave's rows
+        T *out = static_cast<T *>(p.C) + (t.row0 + t.m0 + wm + r) * p.ldc + n;
+        const long long step = (long long)RPI * p.ldc;
+#pragma unroll
+        for (int h = 0; h < 2 * TM; ++h) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                const int row = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    patch[(row * WN + 32 * j + o) ^ (8 * (row & 4))] = acc[h / 2][j][8 * (h & 1) + v];
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += RPI) {
+                const int row = r0 + r, m = 16 * h + row;
+                f32x4 x = *reinterpret_cast<const f32x4 *>(
+                    patch + ((row * WN + c) ^ (8 * (row & 4))));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] += bias[e];
+                if (!EDGE || (m < left && n + 4 <= p.N)) {
+                    store4(out, x);
+                } else if (m < left) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < p.N)
+                            out[e] = (T)x[e];
+                }
+                out += step;
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+
+    __device__ __forceinline__ void outputs(const Mx4Params &p, const Mx4Tile &t, float *patch) const
+    {
+        const bool whole = t.m0 + BM <= t.M && t.n0 + BN <= p.N;
+        with_type(p.type, [&](auto type) {
+            if (whole)
+                turn_over<decltype(type), false>(p, t, patch);
+            else
+                turn_over<decltype(type), true>(p, t, patch);
+        });
+    }
+};
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+__global__ void
+__attribute__((amdgpu_flat_work_group_size(64 * WAVES_M * WAVES_N, 64 * WAVES_M * WAVES_N)))
+mx4_large_kernel(Mx4Params p)
+{
+    typedef Mx4Core<BM, BN, WAVES_M, WAVES_N> Core;
+    constexpr int LOADS = Core::LOADS;
+    static_assert(STAGES >= 2 && (STAGES - 1) * LOADS <= 63, "loads in flight");
+    static_assert(Core::NW * Core::PATCH <= STAGES * Core::STAGE, "the patches fit in the stages");
+    __shared__ __attribute__((aligned(1024))) signed char lds[STAGES * Core::STAGE];
+
+    Mx4Tile t;
+    if (!mx4_tile_of<BM, BN>(p, t))
+        return;
+    Core c;
+    c.init();
+    c.operands(p, t);
+
+    // Step s in stage s % STAGES: each k-group is read under the products of
+    // the one before. Once the last one is read, all meet: the loads of step
+    // s + 1 have to be there, those of step s + STAGES take the stage just
+    // read, and the first k-group of s + 1 is read under the last products of
+    // s. (After the last step this reads zeros.)
+    const int steps = (c.K + Core::BK - 1) / Core::BK;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        c.issue(s, lds + s * Core::STAGE);
+    meet<(STAGES - 2) * LOADS>();
+    c.issue(STAGES - 1, lds + (STAGES - 1) * Core::STAGE);
+    int cur = 0;
+    if (t.m0 + c.wm < t.M) {
+        c.zero();
+        c.read(lds, 0);
+        for (int s = 0; s < steps; ++s) {
+            signed char *stage = lds + cur * Core::STAGE;
+            c.read_words(stage, s);
+            c.step_front(stage);
+            meet<(STAGES - 2) * LOADS>();
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
+            c.step_back(lds + cur * Core::STAGE, s + STAGES, stage);
+        }
+        c.load_bias(p, t);
+    } else {
+        // A wave whose rows all lie behind the group's last only loads, and
+        // leaves the matrix unit to the other wave of its SIMD.
+        for (int s = 0; s < steps; ++s) {
+            meet<(STAGES - 2) * LOADS>();
+            c.issue(s + STAGES, lds + cur * Core::STAGE);
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
+        }
+    }
+    wait_loads<0>();
+    __syncthreads();
+    if (t.m0 + c.wm < t.M)
+        c.outputs(p, t, reinterpret_cast<float *>(lds + c.wave * Core::PATCH));
+}
+
 typedef void (*Mx4Fn)(Mx4Params);
 
 struct Mx4Variant {
@@ -419,15 +872,122 @@ struct Mx4Variant {
     int bm, bn, threads;
 };
 
+template <int MT, int NT, int WAVES, int U> Mx4Variant stream_variant()
+{
+    return {mx4_stream_kernel<MT, NT, WAVES, U>, 16 * MT, 16 * NT, 64 * WAVES};
+}
+
+Mx4Variant variant_of(int kernel)
+{
+    switch (kernel) {
+    case MX4GEMM_KERNEL_S16x16: return stream_variant<1, 1, 8, 2>();
+    case MX4GEMM_KERNEL_S16x32: return stream_variant<1, 2, 4, 2>();
+    case MX4GEMM_KERNEL_S32x16: return stream_variant<2, 1, 8, 2>();
+    case MX4GEMM_KERNEL_S32x32: return stream_variant<2, 2, 8, 2>();
+    case MX4GEMM_KERNEL_S32x64: return stream_variant<2, 4, 4, 2>();
+    case MX4GEMM_KERNEL_T64x64: return {mx4_tile_kernel<1>, 64, 64, 256};
+    case MX4GEMM_KERNEL_T128x128: return {mx4_tile_kernel<2>, 128, 128, 256};
+    case MX4GEMM_KERNEL_L64x64: return {mx4_large_kernel<64, 64, 2, 2, 3>, 64, 64, 256};
+    case MX4GEMM_KERNEL_L64x128: return {mx4_large_kernel<64, 128, 2, 2, 3>, 64, 128, 256};
+    case MX4GEMM_KERNEL_L128x128: return {mx4_large_kernel<128, 128, 2, 4, 4>, 128, 128, 512};
+    case MX4GEMM_KERNEL_L128x256: return {mx4_large_kernel<128, 256, 2, 4, 3>, 128, 256, 512};
+    default: return {mx4_large_kernel<256, 256, 2, 4, 2>, 256, 256, 512};
+    }
+}
+
+// The tiles that load straight into LDS, with what they cost on 256 CUs
+// (measured, us): a lone tile a CU takes 4.5 and `wait` for 256 of K, its loads'
+// way; a CU with tiles enough takes `fixed` and `step` for 256 of K of each.
+struct Mx4Large {
+    int kernel, bm, bn;
+    float wait, fixed, step;
+};
+const Mx4Large kLarge[] = {
+    {MX4GEMM_KERNEL_L64x64, 64, 64, 0.32f, 1.6f, 0.172f},
+    {MX4GEMM_KERNEL_L64x128, 64, 128, 0.50f, 2.3f, 0.326f},
+    {MX4GEMM_KERNEL_L128x128, 128, 128, 0.76f, 4.2f, 0.64f},
+    {MX4GEMM_KERNEL_L128x256, 128, 256, 1.02f, 6.5f, 1.05f},
+    {MX4GEMM_KERNEL_L256x256, 256, 256, 1.70f, 10.8f, 1.70f},
+};
+
 long long mx4_row_tiles(int M, int groups, int bm)
 {
     return groups ? most_tiles(M, groups, bm) : ceil_div_ll(M, bm);
 }
 
-// (Refused before the device is asked: not even the largest tiles fit a launch.)
+// The kernel of a call (an mx4gemm_kernel), or -22 if the tiles of none fit a
+// launch. Those whose tiles do not are passed over.
+int choose_mx4(int M, int N, int K, int groups, bool direct, int cus)
+{
+    auto takes = [&](int kernel) {
+        const Mx4Variant v = variant_of(kernel);
+        return fits_launch((double)mx4_row_tiles(M, groups, v.bm) * (double)ceil_div_ll(N, v.bn),
+                           v.threads);
+    };
+    const long long n16 = ceil_div_ll(N, 16);
+    int stream = -1;
+    // Times are graph replays over operands that no cache holds.
+    if (groups) {
+        // Up to 4 rows a group on average the weights stream (256 rows over 64
+        // groups, 2048 x 2048: 28.8 us against 29.4 with the 64 x 128 tile; with
+        // 8 rows a group 34.6 against 31.6).
+        if (M <= 4LL * groups || (!direct && M <= 16LL * groups))
+            stream = MX4GEMM_KERNEL_S16x32;
+    } else if (M <= 16) {
+        // One row tile: 16 channels a workgroup, with many of them 32 (16 x 4096
+        // x 4096: 4.8 us against 5.9; 16 x 16384 x 4096: 13.4 against 10.3).
+        stream = n16 >= 4LL * cus ? MX4GEMM_KERNEL_S16x32 : MX4GEMM_KERNEL_S16x16;
+    } else {
+        // Row tiles of 32 as long as every CU gets one workgroup at most (32 x
+        // 4096 x 4096: 5.8 us against 7.9 with the 64 x 64 tile, 64 x 4096 x 4096
+        // 7.4 and 8.4, 128 x 4096 x 4096, more than one a CU, 11.1 and 8.7).
+        const long long m32 = ceil_div_ll(M, 32);
+        if (m32 * n16 <= cus)
+            stream = MX4GEMM_KERNEL_S32x16;
+        else if (m32 * ceil_div_ll(N, 32) <= cus)
+            stream = MX4GEMM_KERNEL_S32x32;
+        else if (m32 * ceil_div_ll(N, 64) <= cus && M <= 32)
+            stream = MX4GEMM_KERNEL_S32x64;
+    }
+    if (stream >= 0 && takes(stream))
+        return stream;
+    const double used = groups < M ? groups : M;
+    // Row tiles: of groups, every one's own and half a tile more, since only
+    // the device knows their rows.
+    auto row_tiles = [&](int bm) {
+        if (!groups)
+            return (double)ceil_div_ll(M, bm);
+        const double each = (double)M / groups / bm + 0.5;
+        return used * (each > 1.0 ? each : 1.0);
+    };
+    if (!direct) {
+        if (row_tiles(128) * (double)ceil_div_ll(N, 128) < cus && takes(MX4GEMM_KERNEL_T64x64))
+            return MX4GEMM_KERNEL_T64x64;
+        return takes(MX4GEMM_KERNEL_T128x128) ? MX4GEMM_KERNEL_T128x128 : -22;
+    }
+    int best = -22;
+    float least = 0.0f;
+    for (const Mx4Large &l : kLarge) {
+        const double tiles = row_tiles(l.bm) * (double)ceil_div_ll(N, l.bn);
+        if (!takes(l.kernel))
+            continue;
+        const float rounds = (float)ceil_div_ll((long long)(tiles + 0.999), cus);
+        const float steps = (float)ceil_div_ll(K, 256);
+        const float lone = 4.5f + steps * l.wait;
+        const float busy = 2.5f + rounds * (l.fixed + steps * l.step);
+        const float cost = lone > busy ? lone : busy;
+        if (best < 0 || cost < least) {
+            best = l.kernel;
+            least = cost;
+        }
+    }
+    return best;
+}
+
+// (Refused before the device is asked: not even 256 x 256 tiles fit a launch.)
 bool too_many_tiles(int M, int N, int groups)
 {
-    return !fits_launch((double)mx4_row_tiles(M, groups, 128) * (double)ceil_div_ll(N, 128), 256);
+    return !fits_launch((double)mx4_row_tiles(M, groups, 256) * (double)ceil_div_ll(N, 256), 512);
 }
 
 int launch_mx4(Mx4Params p, hipStream_t s)
@@ -438,9 +998,13 @@ int launch_mx4(Mx4Params p, hipStream_t s)
     const int st = current_cus(&cus);
     if (st != 0)
         return st;
-    Mx4Variant v = {mx4_tile_kernel<2>, 128, 128, 256};
-    if (mx4_row_tiles(p.M, p.groups, 128) * ceil_div_ll(p.N, 128) < cus)
-        v = {mx4_tile_kernel<1>, 64, 64, 256};
+    const bool direct = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.lda % 16 == 0 &&
+                        p.ldb % 16 == 0 && p.strideB % 16 == 0 && p.K % 32 == 0 &&
+                        p.lda < kMaxTileLd && p.ldb < kMaxTileLd && p.K > 0;
+    const int kernel = choose_mx4(p.M, p.N, p.K, p.groups, direct, cus);
+    if (kernel < 0)
+        return kernel;
+    const Mx4Variant v = variant_of(kernel);
     p.tiles_m = (int)mx4_row_tiles(p.M, p.groups, v.bm);
     p.tiles_n = (int)ceil_div_ll(p.N, v.bn);
     p.band = p.groups ? group_band(p.M, p.groups, v.bm) : 8;
@@ -590,4 +1154,15 @@ extern "C" int mx4gemm_grouped(int M, int N, int K, int groups, const int *offse
     p.type = c_type;
     p.groups = groups;
     return launch_mx4(p, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int mx4gemm_select_kernel(int M, int N, int K, int groups, int aligned, int num_cus)
+{
+    if (M < 0) return -1501;
+    if (N < 0) return -1502;
+    if (!k_ok(K)) return -1503;
+    if (groups < 0 || groups > kMaxGroups) return -1604;
+    if (too_many_tiles(M, N, groups)) return -22;
+    return choose_mx4(M, N, K, groups, aligned != 0 && K > 0 && K % 32 == 0,
+                      num_cus > 1 ? num_cus : 1);
 }

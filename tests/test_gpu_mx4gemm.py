@@ -242,6 +242,34 @@ def test_larger_products(env, M, N, K):
     product_case(env, M, N, K, "bfloat16", bias=True)
 
 
+KERNEL_SIZES = [("S16x16", 7, 300, 480), ("S16x32", 9, 16400, 96), ("S32x16", 45, 600, 352),
+                ("S32x32", 40, 4000, 160), ("S32x64", 20, 10000, 160), ("T64x64", 300, 2000, 1000),
+                ("T128x128", 2050, 2060, 333), ("L64x64", 100, 4100, 352),
+                ("L64x128", 500, 4000, 1056), ("L128x128", 1000, 4000, 1056),
+                ("L128x256", 1500, 3000, 288), ("L256x256", 3900, 2100, 288)]
+
+
+@pytest.mark.parametrize("name,M,N,K", KERNEL_SIZES)
+def test_every_kernel(env, name, M, N, K):
+    """Each with tiles that reach past M and N, and a row's last word of scales
+    partly filled (or, of the others, wholly)."""
+    torch, pg = env
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    for k in (K, -(-K // 128) * 128):
+        chosen = pg.mx4gemm_select_kernel(M, N, k, 0, k % 32 == 0, cus)
+        log(f"{name}: {pg.MX4GEMM_KERNELS[chosen]}")
+        if k == K and cus == 256:
+            assert pg.MX4GEMM_KERNELS[chosen] == name
+        product_case(env, M, N, k, "float16" if k == K else "float32", bias=k == K, spread=3)
+
+
+@pytest.mark.parametrize("counts,N,K", [([700, 0, 1, 300, 1100], 1000, 288),
+                                        ([5000, 64, 300], 2100, 160), ([33] * 32, 520, 512),
+                                        ([4] * 64, 2048, 1024), ([0] * 70 + [300, 200], 96, 96)])
+def test_larger_groups(env, counts, N, K):
+    product_case(env, sum(counts) + 3, N, K, "float32", counts, 2, bias=True)
+
+
 @pytest.mark.parametrize("M", [1, 5, 30, 100, 400])
 def test_strides_and_alignment(env, M):
     product_case(env, M, 70, 192, lda=97, ldb=103, ldsa=M + 1, ldsb=75, shift=1, ldc=77)

@@ -162,6 +162,57 @@ def test_oversize_grids_are_rejected(pg):
                 workspace_bytes=size) == -22
 
 
+MX4_THREADS = dict(S16x16=512, S32x16=512, S32x32=512, L128x128=512, L128x256=512,
+                   L256x256=512)  # others 256
+
+
+def mx4_work_items(name, M, N, groups):
+    """Work-items of a call's launch: every group may have a partly filled row tile."""
+    bm, bn = map(int, re.match(r"[STL](\d+)x(\d+)", name).groups())
+    rows = M // bm + min(groups, M) if groups else -(-M // bm)
+    return rows * -(-N // bn) * MX4_THREADS.get(name, 256)
+
+
+def test_mx4_kernel_numbers(pg):
+    text = open(os.path.join(ROOT, "include", "mx4gemm.h")).read()
+    numbers = dict(re.findall(r"MX4GEMM_KERNEL_(\w+) = (\d+)", text))
+    assert int(numbers.pop("COUNT")) == len(pg.MX4GEMM_KERNELS)
+    assert {n: int(v) for n, v in numbers.items()} == \
+        {n: i for i, n in enumerate(pg.MX4GEMM_KERNELS)}
+
+
+def test_mx4_kernels_whose_tiles_fit_a_launch(pg):
+    """A kernel whose tiles a launch does not hold is passed over for one whose
+    tiles it does; every kernel is some call's."""
+    import random
+    rng = random.Random(7)
+    size = lambda most: int(2 ** rng.uniform(0, most))  # noqa: E731
+    calls = [(524288, 8192, 4096, 65536, 1), (8192, 350000, 32, 1024, 1), (2**30, 1, 32, 0, 1),
+             (1, 2**29, 64, 0, 1), (4, 2**30, 64, 0, 1), (16, 2**30, 64, 0, 0)]
+    calls += [(size(31), size(31), rng.choice([1, 32, 100, 4096]), rng.choice([0, 0, size(16)]),
+               rng.randrange(2)) for _ in range(20000)]
+    calls += [(size(14), size(14), 32 * size(9), rng.choice([0, 0, size(8)]), rng.randrange(2))
+              for _ in range(20000)]
+    refused, seen = 0, set()
+    for M, N, K, groups, aligned in calls:
+        kernel = pg.mx4gemm_select_kernel(M, N, K, groups, aligned, 256)
+        if kernel >= 0:
+            name = pg.MX4GEMM_KERNELS[kernel]
+            seen.add(name)
+            assert mx4_work_items(name, M, N, groups) < 2**32, (M, N, K, groups, aligned, name)
+            assert name[0] != "L" or (aligned and K % 32 == 0)
+            continue
+        refused += 1
+        assert kernel == -22
+        largest = "L256x256" if aligned and K % 32 == 0 else "T128x128"
+        assert mx4_work_items(largest, M, N, groups) >= 2**32, (M, N, K, groups, aligned)
+    assert 0 < refused < 20000 and seen == set(pg.MX4GEMM_KERNELS)
+    for bad, status in (((-1, 1, 1, 0), -1501), ((1, -1, 1, 0), -1502), ((1, 1, -1, 0), -1503),
+                        ((1, 1, 1, 65537), -1604)):
+        assert pg.mx4gemm_select_kernel(*bad, 1, 256) == status
+    assert pg.mx4gemm_select_kernel(0, 0, 0, 0, 0, 0) >= 0
+
+
 def test_workspaces(pg):
     torch = pytest.importorskip("torch")
     size = pg.rms_norm_grad_workspace_size
