@@ -19,15 +19,13 @@ namespace {
 // Weights of 8 and 4 bits and the scales of the latter are exact in bf16, so
 // those products run in bf16 (8-bit weights of fp16 tokens: in fp16) on as many
 // terms as the other operand needs to lose nothing: fp16 tokens are two bf16
-// numbers, fp32 ones three. The layer's inner values, which no one type holds,
-// are stored as two (fp32 layers: three), so they lose nothing that out could
-// show.
+// numbers, fp32 ones three. The layer's inner values, fp32 in memory, are two
+// terms (fp32 layers: three), which lose nothing that out could show. The terms
+// are made once a workgroup, as its columns of activations are brought to LDS.
 
 struct Mx4 {};
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 template <typename E> struct FragOf;
 template <> struct FragOf<float> { typedef float type; };
@@ -63,22 +61,28 @@ __device__ __forceinline__ float rest_of(float x)
     return (bits & 0x7f800000u) == 0x7f800000u ? 0.0f : r;
 }
 
-// Eight numbers as N terms of bf16, each the truncation of what the ones before
-// leave.
+// Eight numbers as N terms of bf16: each the truncation of what the ones before
+// leave, the last one rounded (to 16 bits in all of two; three hold all 24).
 template <int N>
 __device__ __forceinline__ void split8(float (&f)[8], bf16x8 (&to)[N])
 {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        i32x4 v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = upper_halves(f[2 * i], f[2 * i + 1]);
-        to[n] = __builtin_bit_cast(bf16x8, v);
-        if (n + 1 < N)
+        if (n + 1 == N && N > 1) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                f[i] = rest_of(f[i]);
+                to[n][i] = (__bf16)f[i];
+        } else {
+            i32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = upper_halves(f[2 * i], f[2 * i + 1]);
+            to[n] = __builtin_bit_cast(bf16x8, v);
+            if (n + 1 < N)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    f[i] = rest_of(f[i]);
+        }
     }
 }
 
@@ -94,6 +98,7 @@ template <typename X, typename W, bool UP> struct Math {
     static constexpr bool F32 = std::is_same<W, float>::value;
     static constexpr bool MX4 = std::is_same<W, Mx4>::value;
     static constexpr bool I8 = std::is_same<W, signed char>::value;
+    typedef typename std::conditional<UP, X, float>::type In; // the activations in memory
     typedef typename std::conditional<
         F32, float,
         typename std::conditional<UP && std::is_same<X, _Float16>::value && !MX4, _Float16,
@@ -107,84 +112,85 @@ template <typename X, typename W, bool UP> struct Math {
                               : std::is_same<X, float>::value       ? 3
                               : !UP || std::is_same<X, _Float16>::value ? 2
                                                                     : 1;
-    // Loads of 16 bytes of a slot's activations for 16 bytes of weights.
-    static constexpr int NL = UP ? EPC * (int)sizeof(X) / 16 : F32 ? 1 : NX * EPC / 8;
+    static constexpr int VEC = 16 / (int)sizeof(Elem); // elements of 16 bytes in LDS
 
-    static __device__ __forceinline__ void weights(i32x4 v, uint32_t byte, Frag (&to)[NM][NW])
+    // Instruction i's operand of a chunk of weights; s: the scale of its block.
+    static __device__ __forceinline__ void weights(int i, i32x4 v, float s, Frag (&to)[NW])
     {
         if constexpr (F32) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                to[i][0] = __int_as_float(v[i]);
+            to[0] = __int_as_float(v[i]);
         } else if constexpr (MX4) {
-            const float s = mx4_scale(byte);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                i32x4 w;
-                w[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 0));
-                w[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 1));
-                w[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 2));
-                w[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 3));
-                to[i][0] = __builtin_bit_cast(bf16x8, w);
-            }
+            i32x4 w;
+            w[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 0));
+            w[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 1));
+            w[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 2));
+            w[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 3));
+            to[0] = __builtin_bit_cast(bf16x8, w);
         } else if constexpr (I8) {
+            float f[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float f[8];
+            for (int e = 0; e < 8; ++e)
+                f[e] = (float)(signed char)(v[2 * i + e / 4] >> (8 * (e % 4)));
+            if constexpr (BF) {
+                split8<1>(f, to);
+            } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    f[e] = (float)(signed char)(v[2 * i + e / 4] >> (8 * (e % 4)));
-                if constexpr (BF) {
-                    split8<1>(f, to[i]);
-                } else {
-                    f16x8 h;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        h[e] = (_Float16)f[e];
-                    to[i][0] = h;
-                }
+                    to[0][e] = (_Float16)f[e];
             }
         } else if constexpr (NW == 2) {
             float f[8];
             unpack<_Float16>(v, f);
-            split8<2>(f, to[0]);
+            split8<2>(f, to);
         } else {
-            to[0][0] = __builtin_bit_cast(Frag, v);
+            to[0] = __builtin_bit_cast(Frag, v);
         }
     }
 
-    // The activations that belong to a chunk of weights, from their loads.
-    static __device__ __forceinline__ void activations(const i32x4 (&v)[NL], Frag (&to)[NM][NX])
+    // VEC neighbouring activations as they lie, and as terms; zeros behind K.
+    static constexpr int NR = VEC * (int)sizeof(In) / 16;
+
+    static __device__ __forceinline__ void fetch(const In *row, int k, i32x4 (&to)[NR])
     {
-        if constexpr (F32) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                to[i][0] = __int_as_float(v[0][i]);
-        } else if constexpr (!UP) {
+        for (int i = 0; i < NR; ++i)
+            to[i] = load16(row + k + i * (VEC / NR));
+    }
+
+    static __device__ __forceinline__ void fetch_edge(const In *row, int k, int K, i32x4 (&to)[NR])
+    {
+        typedef In iv __attribute__((ext_vector_type(VEC / NR)));
 #pragma unroll
-            for (int i = 0; i < NM; ++i)
+        for (int i = 0; i < NR; ++i) {
+            iv v;
 #pragma unroll
-                for (int n = 0; n < NX; ++n)
-                    to[i][n] = __builtin_bit_cast(Frag, v[n * NM + i]);
-        } else if constexpr (std::is_same<X, Elem>::value) {
-#pragma unroll
-            for (int i = 0; i < NM; ++i)
-                to[i][0] = __builtin_bit_cast(Frag, v[i]);
-        } else {
-            constexpr int VEC = 16 / sizeof(X);
-#pragma unroll
-            for (int i = 0; i < NM; ++i) {
-                float f[8];
-#pragma unroll
-                for (int j = 0; j < 8; j += VEC) {
-                    float x[VEC];
-                    unpack<X>(v[(8 * i + j) / VEC], x);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) // (quiet NaNs, whose truncation is one)
-                        f[j + e] = __builtin_canonicalizef(x[e]);
-                }
-                split8<NX>(f, to[i]);
+            for (int e = 0; e < VEC / NR; ++e) {
+                const int at = k + i * (VEC / NR) + e;
+                v[e] = at < K ? row[at] : (In)0.0f;
             }
+            to[i] = __builtin_bit_cast(i32x4, v);
+        }
+    }
+
+    static __device__ __forceinline__ void terms(const i32x4 (&v)[NR], i32x4 (&to)[NX])
+    {
+        if constexpr (std::is_same<In, Elem>::value) {
+            to[0] = v[0];
+        } else {
+            float f[VEC];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                float x[VEC / NR];
+                unpack<In>(v[i], x);
+#pragma unroll
+                for (int e = 0; e < VEC / NR; ++e) // (quiet NaNs, whose truncation is one)
+                    f[i * (VEC / NR) + e] = __builtin_canonicalizef(x[e]);
+            }
+            bf16x8 b[NX];
+            split8<NX>(f, b);
+#pragma unroll
+            for (int n = 0; n < NX; ++n)
+                to[n] = __builtin_bit_cast(i32x4, b[n]);
         }
     }
 };
@@ -195,19 +201,33 @@ struct LayerParams {
     const void *W1, *W2;
     const void *scale1, *scale2;
     void *out;
-    void *inner;     // the inner values: planes of slots x inner_cols
+    float *inner;    // the inner values, slots x inner_cols
     float *partial;  // W2's products, slots x H
     long long strideW1, strideW2, ldw1, ldw2; // bytes
     long long ldx, ldo;
     int tokens, topk, experts, H, F;
-    int inner_cols; // F rounded up to a step of the widest chunks
+    int inner_cols; // F rounded up to 16 bytes
     int id_bytes;
     int tiles; // row tiles of an expert
+    uint32_t inverse; // of topk
+    int parts; // waves that share a tile, K over them: 1, 2 or 4
 };
 
-constexpr int kLayerWaves = 8;
+constexpr int kLayerWaves = 4;
 constexpr int kLayerThreads = 64 * kLayerWaves;
-constexpr int kTileRows = 32; // rows of weights of a workgroup: two of an instruction's 16
+constexpr int kColumnBytes = 28 << 10; // of LDS for the columns of activations
+
+// Quotients of numbers below 2^16 by one of them, from ceil(2^32 / d): the error is
+// below n / 2^32 < 1 / d. (0 stands for 2^32, the inverse of 1.)
+__host__ __device__ __forceinline__ uint32_t inverse_of(int d)
+{
+    return d == 1 ? 0u : 0xffffffffu / (uint32_t)d + 1u;
+}
+
+__device__ __forceinline__ int divide(int n, uint32_t inverse)
+{
+    return inverse ? (int)__umulhi((uint32_t)n, inverse) : n;
+}
 
 __device__ __forceinline__ int id_of(const LayerParams &p, int slot)
 {
@@ -219,340 +239,533 @@ __device__ __forceinline__ int id_of(const LayerParams &p, int slot)
     return v >= 0 && v < p.experts ? (int)v : -1;
 }
 
+constexpr int kColumns = 16; // slots that are multiplied at a time: an instruction's columns
+
 struct LayerShared {
-    uint32_t named[EXPERT_LAYER_MAX_EXPERTS / 32]; // one bit an expert
-    int count;
-    unsigned short slots[EXPERT_LAYER_MAX_SLOTS];
-    float sums[kLayerWaves][kTileRows][17];
+    int count[EXPERT_LAYER_MAX_EXPERTS]; // slots of each expert
+    int slots[kColumns];
+    // Columns of activations while they are multiplied, then the waves' sums.
+    __attribute__((aligned(16))) signed char columns[kColumnBytes];
 };
 
-// The `nth` expert that some slot names, in the experts' order, and its slots
-// (in any order: a slot's results do not depend on its column); false if there
-// are fewer. Every thread of the workgroup takes part.
-__device__ __forceinline__ bool find_expert(const LayerParams &p, int nth, LayerShared &sh, int &e)
+// The `nth` group of up to 16 slots with one expert, that expert and the group's
+// slots (in sh.slots after the workgroup's next meeting): first each named
+// expert's first 16 slots, in the experts' order, then the second 16 of those
+// that have as many, and so on. False if there are fewer. Every thread of the
+// workgroup takes part.
+__device__ __forceinline__ bool find_slots(const LayerParams &p, int nth, LayerShared &sh, int &e,
+                                           int &cols)
 {
     const int tid = threadIdx.x, lane = tid & 63;
     const int slots = p.tokens * p.topk;
-    if (tid < EXPERT_LAYER_MAX_EXPERTS / 32)
-        sh.named[tid] = 0;
-    if (tid == 0)
-        sh.count = 0;
+    constexpr int HELD = 8;
+    int held[HELD]; // the ids of the first 512 slots, loaded side by side
+    auto hold = [&](auto type) {
+        typedef decltype(type) Id;
+        Id v[HELD];
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            v[i] = static_cast<const Id *>(p.ids)[min(64 * i + lane, slots - 1)];
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            held[i] = 64 * i + lane < slots && v[i] >= 0 && v[i] < (Id)p.experts ? (int)v[i] : -1;
+    };
+    if (p.id_bytes == 4)
+        hold(int{});
+    else
+        hold((long long)0);
+    for (int i = tid; i < p.experts; i += kLayerThreads)
+        sh.count[i] = 0;
     __syncthreads();
-    constexpr int PER = EXPERT_LAYER_MAX_SLOTS / kLayerThreads;
-    int id[PER];
+    // (Each wave counts its share of every 64 * kLayerWaves slots.)
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int s = tid + i * kLayerThreads;
-        id[i] = s < slots ? id_of(p, s) : -1;
+    for (int i = 0; i < HELD; ++i)
+        if (i % kLayerWaves == tid >> 6 && held[i] >= 0)
+            atomicAdd(&sh.count[held[i]], 1);
+    for (int s = 64 * HELD + tid; s < slots; s += kLayerThreads) {
+        const int id = id_of(p, s);
+        if (id >= 0)
+            atomicAdd(&sh.count[id], 1);
     }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (id[i] >= 0)
-            atomicOr(&sh.named[id[i] >> 5], 1u << (id[i] & 31));
     __syncthreads();
-    const uint32_t word = lane < EXPERT_LAYER_MAX_EXPERTS / 32 ? sh.named[lane] : 0;
-    int upto = __popc(word);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(upto, d);
-        if (lane >= d)
-            upto += v;
+    e = -1;
+    int from = 0, total = 0; // the group's first slot among the expert's, and all of those
+    for (bool any = true; any && e < 0; from += kColumns) {
+        any = false;
+        for (int i = 0; i < p.experts; i += 64) {
+            const int n = i + lane < p.experts ? sh.count[i + lane] : 0;
+            unsigned long long left = __ballot(n > from);
+            const int here = __popcll(left);
+            any = any || here > 0;
+            if (nth < here) {
+                for (; nth > 0; --nth)
+                    left &= left - 1;
+                e = i + __builtin_ctzll(left);
+                total = __builtin_amdgcn_readlane(n, __builtin_ctzll(left));
+                break;
+            }
+            nth -= here;
+        }
     }
-    const int before = upto - __popc(word);
-    const unsigned long long who = __ballot(nth >= before && nth < upto);
-    if (who == 0)
+    if (e < 0)
         return false;
-    uint32_t left = word;
-    if (nth >= before && nth < upto)
-        for (int i = before; i < nth; ++i)
-            left &= left - 1;
-    const int src = __builtin_ctzll(who);
-    e = 32 * src + __builtin_ctz((uint32_t)__builtin_amdgcn_readlane((int)left, src));
+    from -= kColumns;
+    cols = min(kColumns, total - from);
+    int n = -from;
+    auto add = [&](int first, int id) {
+        const unsigned long long mine = __ballot(id == e);
+        const int at = n + __popcll(mine & ((1ull << lane) - 1));
+        if (id == e && at >= 0 && at < kColumns)
+            sh.slots[at] = first + lane; // (every wave writes the same)
+        n += __popcll(mine);
+    };
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (id[i] == e)
-            sh.slots[atomicAdd(&sh.count, 1)] = (unsigned short)(tid + i * kLayerThreads);
-    __syncthreads();
+    for (int i = 0; i < HELD; ++i)
+        if (64 * i < slots)
+            add(64 * i, held[i]);
+    for (int s = 64 * HELD; s < slots && n < cols; s += 64)
+        add(s, s + lane < slots ? id_of(p, s + lane) : -1);
     return true;
 }
 
-// A wave's part of the products of two times 16 rows of weights with 16 * CG
-// columns: steps wave, wave + kLayerWaves, ... of K, a step being 4 chunks of 16
-// bytes of a row (lane l: chunk l / 16 of row l % 16; of the activations the same
-// elements of column l % 16). cols: bytes of a row of activations (UP), or the
-// bytes between their planes.
-template <typename M, bool UP, int CG>
-__device__ __forceinline__ void products(const signed char *const (&w)[2], int wbytes,
-                                         const uint32_t *const (&sc)[2], long long ldsc, int K,
-                                         const signed char *const (&x)[CG], long long xbytes,
-                                         f32x4 (&acc)[2][CG])
+// Rows of weights as a wave's lanes load them. Where rows start on 16-byte
+// boundaries, hold a multiple of 16 bytes and lie within 2^31 bytes of each other
+// (`Even`), loads go through a buffer descriptor with 32-bit offsets, one outside
+// it for zeros behind a row's end; others (`Ragged`) chunk by chunk at any address.
+template <int NT> struct Even {
+    __amdgpu_buffer_rsrc_t w[2], sc; // (of W1 the gate's part and the other)
+    uint32_t offw[NT], offs[NT];
+    int wbytes;
+    uint32_t ldsc;
+};
+
+template <int NT> struct Ragged {
+    const signed char *w[NT];
+    const uint32_t *sc[NT];
+    int wbytes;
+    long long ldsc;
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t whole(const void *base)
 {
-    const int lane = threadIdx.x & 63, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int steps = (wbytes + 63) / 64;
-    constexpr int XB = UP ? M::NL * 16 : M::F32 ? 16 : M::EPC * 2; // of a chunk, a plane
-    auto one = [&](int s, auto load_w, auto load_x) {
+    return rows_rsrc(static_cast<const signed char *>(base), 0x7fffffff);
+}
+
+// The products of NT times 16 rows of weights a wave with the workgroup's `cols`
+// columns of activations (up to 16; column c is row_of(c) of `in`), as much
+// of K at a time as LDS holds of the columns. A step is 4 chunks of 16 bytes of a
+// row of weights (lane l: chunk l / 16 of row l % 16); a wave takes the steps
+// part, part + parts, ... The first steps' weights are loaded before the columns
+// are, and DEPTH steps' loads are under way at once. A column's terms stand one
+// behind the other, 16 bytes further in each column than a multiple of 256, so
+// that the 16 columns that are read together lie in different banks.
+template <typename M, bool UP, int NT, bool EVEN, typename Row>
+__device__ __forceinline__ void
+products(const typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type &rows,
+         const typename M::In *in, Row row_of, int K, int cols, bool live, int part, int parts,
+         LayerShared &sh, f32x4 (&acc)[NT])
+{
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
+    constexpr int SPAN = 4 * M::EPC;            // elements of a step
+    constexpr int ES = (int)sizeof(typename M::Elem);
+    constexpr int DEPTH = NT == 2 ? 2 : 1;
+    struct Step {
+        i32x4 w[NT];
+        uint32_t word[NT];
+    };
+    auto load = [&](int s, Step &to) {
         const int c = 4 * s + q;
-        i32x4 vw[2], vx[CG][M::NL];
-        uint32_t byte[2] = {0, 0};
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            vw[t] = load_w(w[t], 16 * c);
+        for (int t = 0; t < NT; ++t) {
+            if constexpr (EVEN) {
+                to.w[t] = __builtin_bit_cast(
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                               rows.w[UP ? t / (NT / 2) : 0],
+                               16 * c < rows.wbytes ? rows.offw[t] + 16u * c : kOutside, 0, 0));
+                if constexpr (M::MX4)
+                    to.word[t] = __builtin_amdgcn_raw_buffer_load_b32(
+                        rows.sc, rows.offs[t] + s * rows.ldsc, 0, 0);
+            } else {
+                to.w[t] = row_chunk(rows.w[t], 16 * c, rows.wbytes);
+                if constexpr (M::MX4)
+                    to.word[t] = rows.sc[t][s * rows.ldsc];
+            }
+        }
+    };
+    const int room = (kColumnBytes / cols - 16) / (ES * M::NX) / 128 * 128;
+    const int chunk = min(room, (K + 127) / 128 * 128), steps = (K + SPAN - 1) / SPAN;
+    const int plane = chunk * ES, column = M::NX * plane + 16;
+    for (int k0 = 0; k0 < K; k0 += chunk) {
+        const int first = k0 / SPAN, end = live ? min(steps, first + chunk / SPAN) : 0;
+        Step ring[DEPTH + 1];
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (first + part + d * parts < end)
+                load(first + part + d * parts, ring[d]);
+        __syncthreads(); // (what stood in LDS has been read)
+        const int here = min(chunk, (K - k0 + 127) / 128 * 128);
+        // A wave takes every kLayerWaves-th of the columns' pieces of 64 * VEC
+        // elements, AT of them at a time.
+        constexpr int AT = 4 / M::NR > 0 ? 4 / M::NR : 1, PIECE = 64 * M::VEC;
+        const int each = (here + PIECE - 1) / PIECE, pieces = cols * each;
+        const uint32_t inverse = inverse_of(each);
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        for (int i = wave; i < pieces; i += AT * kLayerWaves) {
+            i32x4 raw[AT][M::NR];
+            int c[AT], k[AT];
+#pragma unroll
+            for (int a = 0; a < AT; ++a) {
+                const int at = min(i + a * kLayerWaves, pieces - 1);
+                c[a] = divide(at, inverse);
+                k[a] = (at - c[a] * each) * PIECE + lane * M::VEC;
+            }
+            if (k0 + here <= K) { // (K a multiple of 128, or not its end yet)
+#pragma unroll
+                for (int a = 0; a < AT; ++a)
+                    M::fetch(in + row_of(c[a]), k0 + min(k[a], here - M::VEC), raw[a]);
+            } else {
+#pragma unroll
+                for (int a = 0; a < AT; ++a)
+                    M::fetch_edge(in + row_of(c[a]), k0 + k[a], K, raw[a]);
+            }
+#pragma unroll
+            for (int a = 0; a < AT; ++a) {
+                i32x4 v[M::NX];
+                M::terms(raw[a], v);
+                if (k[a] < here)
+#pragma unroll
+                    for (int n = 0; n < M::NX; ++n)
+                        *reinterpret_cast<i32x4 *>(sh.columns + c[a] * column + n * plane +
+                                                   k[a] * ES) = v[n];
+            }
+        }
+        __syncthreads();
+        const signed char *x = sh.columns + min(lane & 15, cols - 1) * column;
+        auto multiply = [&](int s, const Step &v) {
+            float scale[NT] = {};
             if constexpr (M::MX4)
-                byte[t] = sc[t][s * ldsc];
-        }
 #pragma unroll
-        for (int g = 0; g < CG; ++g)
+                for (int t = 0; t < NT; ++t) // (Bytes of blocks behind K may hold anything.)
+                    scale[t] = mx4_scale(32 * (4 * s + q) < K ? v.word[t] >> (8 * q) & 255u : 0u);
+            const int at = ((s - first) * SPAN + q * M::EPC) * ES;
 #pragma unroll
-            for (int i = 0; i < M::NL; ++i) {
-                if constexpr (UP || M::F32)
-                    vx[g][i] = load_x(x[g], XB * c + 16 * i);
-                else
-                    vx[g][i] = load16(x[g] + (i / M::NM) * xbytes + XB * c + 16 * (i % M::NM));
+            for (int i = 0; i < M::NM; ++i) {
+                typename M::Frag fw[NT][M::NW];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    M::weights(i, v.w[t], scale[t], fw[t]);
+#pragma unroll
+                for (int b = 0; b < M::NX; ++b) {
+                    const typename M::Frag fx = *reinterpret_cast<const typename M::Frag *>(
+                        x + b * plane + at + (int)sizeof(typename M::Frag) * i);
+#pragma unroll
+                    for (int a = 0; a < M::NW; ++a)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            acc[t] = mfma(fw[t][a], fx, acc[t]);
+                }
             }
-        typename M::Frag fw[2][M::NM][M::NW];
+        };
+        for (int s = first + part; s < end; s += (DEPTH + 1) * parts) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            if constexpr (M::MX4) {
-                // (Bytes of blocks behind K may hold anything.)
-                const bool there = 32 * c < K;
-                byte[t] = there ? byte[t] >> (8 * q) & 255u : 0u;
+            for (int d = 0; d <= DEPTH; ++d) {
+                const int now = s + d * parts, ahead = now + DEPTH * parts;
+                if (now >= end)
+                    break;
+                if (ahead < end)
+                    load(ahead, ring[(d + DEPTH) % (DEPTH + 1)]);
+                multiply(now, ring[d]);
             }
-            M::weights(vw[t], byte[t], fw[t]);
         }
-#pragma unroll
-        for (int g = 0; g < CG; ++g) {
-            typename M::Frag fx[M::NM][M::NX];
-            M::activations(vx[g], fx);
-#pragma unroll
-            for (int i = 0; i < M::NM; ++i)
-#pragma unroll
-                for (int a = 0; a < M::NW; ++a)
-#pragma unroll
-                    for (int b = 0; b < M::NX; ++b)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            acc[t][g] = mfma(fw[t][i][a], fx[i][b], acc[t][g]);
-        }
-    };
-    auto whole = [](const signed char *row, int k) { return load16(row + k); };
-    auto edge_w = [&](const signed char *row, int k) { return row_chunk(row, k, wbytes); };
-    auto edge_x = [&](const signed char *row, int k) {
-        return UP ? row_chunk(row, k, (int)xbytes) : load16(row + k);
-    };
-    const int full = wbytes / 64 - (M::MX4 && K % 128 != 0 && wbytes % 64 == 0 ? 1 : 0);
-    int s = wave;
-    for (; s < full; s += kLayerWaves)
-        one(s, whole, whole);
-    for (; s < steps; s += kLayerWaves)
-        one(s, edge_w, edge_x);
-}
-
-// acc of all waves added, through LDS, in the waves' order: thread i < 512 gets
-// row i / 16, column i % 16 of the 32 rows.
-__device__ __forceinline__ float join(const f32x4 &a0, const f32x4 &a1, LayerShared &sh)
-{
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    __syncthreads(); // (the last sums have been read)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        sh.sums[wave][4 * (lane >> 4) + v][lane & 15] = a0[v];
-        sh.sums[wave][16 + 4 * (lane >> 4) + v][lane & 15] = a1[v];
     }
-    __syncthreads();
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kLayerWaves; ++w)
-        sum += sh.sums[w][tid >> 4][tid & 15];
-    return sum;
 }
 
-// W1: the gate's and the other 16 rows of 16 inner values, for all slots of an
-// expert.
-template <typename X, typename W>
+// The waves' sums through LDS: the `parts` waves that share a tile each get the
+// subtiles t = part, part + parts, ... of its sum, added in the waves' order;
+// alone, a wave has them already.
+template <int NT>
+__device__ __forceinline__ f32x4 joined(const f32x4 (&acc)[NT], int t, int parts,
+                                        const f32x4 (*sums)[NT][64])
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (parts == 1)
+        return acc[t];
+    const int first = wave & ~(parts - 1);
+    f32x4 v = sums[first][t][lane];
+    for (int i = 1; i < parts; ++i)
+        v += sums[first + i][t][lane];
+    return v;
+}
+
+template <int NT>
+__device__ __forceinline__ void give(const f32x4 (&acc)[NT], int parts, f32x4 (*sums)[NT][64])
+{
+    if (parts == 1)
+        return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads(); // (the columns have been read)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        sums[wave][t][lane] = acc[t];
+    __syncthreads();
+}
+
+// W1: NT / 2 times 16 rows of the gate and as many of the other part a tile, for
+// up to 16 slots of an expert.
+template <typename X, typename W, int NT, bool EVEN>
 __global__ void __launch_bounds__(kLayerThreads) layer_up_kernel(LayerParams p)
 {
     typedef Math<X, W, true> M;
+    constexpr int HALF = NT / 2;
     __shared__ LayerShared sh;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int f0 = (int)(blockIdx.x % p.tiles) * 16;
-    int e;
-    if (!find_expert(p, blockIdx.x / p.tiles, sh, e))
+    f32x4(*sums)[NT][64] = reinterpret_cast<f32x4(*)[NT][64]>(sh.columns);
+    static_assert(sizeof(f32x4[kLayerWaves][NT][64]) <= kColumnBytes, "the sums fit");
+    const int lane = threadIdx.x & 63, r = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int part = wave & (p.parts - 1), each = kLayerWaves / p.parts; // tiles of a workgroup
+    const int blocks = (p.tiles + each - 1) / each;
+    const int f0 = ((int)(blockIdx.x % blocks) * each + wave / p.parts) * 16 * HALF;
+    int e, cols;
+    if (!find_slots(p, blockIdx.x / blocks, sh, e, cols))
         return;
-    const int n = sh.count;
-    const int wbytes = M::MX4 ? (p.H + 1) / 2 : p.H * (M::I8 ? 1 : (int)sizeof(X));
-    const signed char *w[2];
-    const uint32_t *sc[2] = {nullptr, nullptr};
-    const int row = min(f0 + (lane & 15), p.F - 1);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        w[t] = static_cast<const signed char *>(p.W1) + e * p.strideW1 +
-               (row + (long long)t * p.F) * p.ldw1;
-        if constexpr (M::MX4)
-            sc[t] = static_cast<const uint32_t *>(p.scale1) +
-                    (long long)e * ((p.H + 127) / 128) * 2 * p.F + row + (long long)t * p.F;
+    const bool live = f0 < p.F; // (a wave without a tile still meets the others)
+    typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type rows;
+    rows.wbytes = M::MX4 ? (p.H + 1) / 2 : p.H * (M::I8 ? 1 : (int)sizeof(X));
+    const signed char *w1 = static_cast<const signed char *>(p.W1) + e * p.strideW1;
+    const long long ldsc = 2LL * p.F;
+    const uint32_t *sc = static_cast<const uint32_t *>(p.scale1) +
+                         (M::MX4 ? e * ((p.H + 127LL) / 128) * ldsc : 0);
+    const int base = min(f0, p.F - 1);
+    if constexpr (EVEN) {
+        rows.w[0] = whole(w1 + base * p.ldw1);
+        rows.w[1] = whole(w1 + (base + (long long)p.F) * p.ldw1);
+        rows.sc = whole(sc);
+        rows.ldsc = (uint32_t)ldsc * 4;
+    } else {
+        rows.ldsc = ldsc;
     }
-    const int slots = p.tokens * p.topk;
-    auto columns = [&](int c0, auto groups) {
-        constexpr int CG = decltype(groups)::value;
-        const signed char *x[CG];
 #pragma unroll
-        for (int g = 0; g < CG; ++g) {
-            const int slot = sh.slots[min(c0 + 16 * g + (lane & 15), n - 1)];
-            x[g] = static_cast<const signed char *>(p.X) + (slot / p.topk) * p.ldx * sizeof(X);
+    for (int t = 0; t < NT; ++t) {
+        const int row = min(f0 + 16 * (t % HALF) + r, p.F - 1);
+        const int at = row + (t / HALF) * p.F;
+        if constexpr (EVEN) {
+            rows.offw[t] = (uint32_t)((row - base) * (int)p.ldw1);
+            rows.offs[t] = 4u * at;
+        } else {
+            rows.w[t] = w1 + at * p.ldw1;
+            rows.sc[t] = sc + at;
         }
-        f32x4 acc[2][CG] = {};
-        products<M, true, CG>(w, wbytes, sc, 2LL * p.F, p.H, x, (long long)p.H * sizeof(X), acc);
+    }
+    f32x4 acc[NT] = {};
+    products<M, true, NT, EVEN>(
+        rows, static_cast<const X *>(p.X),
+        [&](int c) { return divide(sh.slots[c], p.inverse) * p.ldx; }, p.H, cols, live, part,
+        p.parts, sh, acc);
+    give(acc, p.parts, sums);
+    if (!live || r >= cols)
+        return;
+    float *to = p.inner + (long long)sh.slots[r] * p.inner_cols;
 #pragma unroll
-        for (int g = 0; g < CG; ++g) {
-            const float mine = join(acc[0][g], acc[1][g], sh);
-            // Thread i < 256 holds the gate's row i / 16, thread 256 + i the other's.
-            __syncthreads();
-            if (tid >= 256)
-                sh.sums[0][(tid >> 4) - 16][tid & 15] = mine;
-            __syncthreads();
-            const int f = f0 + (tid >> 4), c = c0 + 16 * g + (tid & 15);
-            if (tid < 256 && c < n) {
-                const int slot = sh.slots[c];
-                float gate = mine, up = sh.sums[0][tid >> 4][tid & 15], a = 0.0f;
-                if (f < p.F) {
-                    if constexpr (M::I8) {
-                        const float *s = static_cast<const float *>(p.scale1) + 2LL * p.F * e;
-                        gate *= s[f];
-                        up *= s[p.F + f];
-                    }
-                    a = gate / (1.0f + expf(-gate)) * up;
-                }
-                // The last tile fills the columns behind F with zeros.
-                const int end = f0 + 16 < p.F ? f0 + 16 : p.inner_cols;
-                for (int k = f; k < end; k += 16) {
-                    float v = k < p.F ? a : 0.0f;
-                    const long long at = (long long)slot * p.inner_cols + k;
-                    const long long plane = (long long)slots * p.inner_cols;
-                    if constexpr (M::F32) {
-                        static_cast<float *>(p.inner)[at] = v;
-                    } else {
-                        constexpr int N = Math<X, W, false>::NX;
-                        uint16_t *to = static_cast<uint16_t *>(p.inner) + at;
+    for (int t = 0; t < HALF; ++t) {
+        if ((t & (p.parts - 1)) != part)
+            continue;
+        // The lane's four inner values, one behind the other.
+        const f32x4 gate = joined(acc, t, p.parts, sums);
+        const f32x4 up = joined(acc, HALF + t, p.parts, sums);
+        const int f = f0 + 16 * t + 4 * (lane >> 4);
+        f32x4 a;
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            // Two terms: the second is rounded, to 16 bits in all;
-                            // three hold all 24.
-                            to[i * plane] = i + 1 < N
-                                                ? (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16)
-                                                : __builtin_bit_cast(uint16_t, (__bf16)v);
-                            v = rest_of(v);
-                        }
-                    }
-                }
+        for (int v = 0; v < 4; ++v) {
+            float x0 = gate[v], x1 = up[v];
+            if constexpr (M::I8) {
+                const float *s = static_cast<const float *>(p.scale1) + 2LL * p.F * e;
+                x0 *= s[min(f + v, p.F - 1)];
+                x1 *= s[p.F + min(f + v, p.F - 1)];
             }
+            a[v] = x0 / (1.0f + expf(-x0)) * x1;
         }
-    };
-    int c0 = 0;
-    for (; n - c0 > 32; c0 += 64)
-        columns(c0, std::integral_constant<int, 4>{});
-    if (n - c0 > 16)
-        columns(c0, std::integral_constant<int, 2>{});
-    else if (n - c0 > 0)
-        columns(c0, std::integral_constant<int, 1>{});
+        if (f < p.F) // (a row holds a multiple of four)
+            store16(to + f, __builtin_bit_cast(i32x4, a));
+    }
 }
 
-// W2: 32 rows of it for all slots of an expert.
-template <typename X, typename W>
+// W2: NT times 16 rows of it a tile, for up to 16 slots of an expert.
+template <typename X, typename W, int NT, bool EVEN>
 __global__ void __launch_bounds__(kLayerThreads) layer_down_kernel(LayerParams p)
 {
     typedef Math<X, W, false> M;
     __shared__ LayerShared sh;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int h0 = (int)(blockIdx.x % p.tiles) * kTileRows;
-    int e;
-    if (!find_expert(p, blockIdx.x / p.tiles, sh, e))
+    f32x4(*sums)[NT][64] = reinterpret_cast<f32x4(*)[NT][64]>(sh.columns);
+    const int lane = threadIdx.x & 63, r = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int part = wave & (p.parts - 1), each = kLayerWaves / p.parts;
+    const int blocks = (p.tiles + each - 1) / each;
+    const int h0 = ((int)(blockIdx.x % blocks) * each + wave / p.parts) * 16 * NT;
+    int e, cols;
+    if (!find_slots(p, blockIdx.x / blocks, sh, e, cols))
         return;
-    const int n = sh.count;
-    const int wbytes = M::MX4 ? (p.F + 1) / 2 : p.F * (M::I8 ? 1 : (int)sizeof(X));
-    const signed char *w[2];
-    const uint32_t *sc[2] = {nullptr, nullptr};
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int row = min(h0 + 16 * t + (lane & 15), p.H - 1);
-        w[t] = static_cast<const signed char *>(p.W2) + e * p.strideW2 + row * p.ldw2;
-        if constexpr (M::MX4)
-            sc[t] = static_cast<const uint32_t *>(p.scale2) +
-                    (long long)e * ((p.F + 127) / 128) * p.H + row;
+    const bool live = h0 < p.H;
+    typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type rows;
+    rows.wbytes = M::MX4 ? (p.F + 1) / 2 : p.F * (M::I8 ? 1 : (int)sizeof(X));
+    const signed char *w2 = static_cast<const signed char *>(p.W2) + e * p.strideW2;
+    const uint32_t *sc = static_cast<const uint32_t *>(p.scale2) +
+                         (M::MX4 ? e * ((p.F + 127LL) / 128) * p.H : 0);
+    const int base = min(h0, p.H - 1);
+    if constexpr (EVEN) {
+        rows.w[0] = rows.w[1] = whole(w2 + base * p.ldw2);
+        rows.sc = whole(sc);
+        rows.ldsc = (uint32_t)p.H * 4;
+    } else {
+        rows.ldsc = p.H;
     }
-    const int slots = p.tokens * p.topk;
-    constexpr int ES = M::F32 ? 4 : 2; // bytes of an inner value's term
-    auto columns = [&](int c0, auto groups) {
-        constexpr int CG = decltype(groups)::value;
-        const signed char *x[CG];
 #pragma unroll
-        for (int g = 0; g < CG; ++g) {
-            const int slot = sh.slots[min(c0 + 16 * g + (lane & 15), n - 1)];
-            x[g] = static_cast<const signed char *>(p.inner) +
-                   (long long)slot * p.inner_cols * ES;
+    for (int t = 0; t < NT; ++t) {
+        const int row = min(h0 + 16 * t + r, p.H - 1);
+        if constexpr (EVEN) {
+            rows.offw[t] = (uint32_t)((row - base) * (int)p.ldw2);
+            rows.offs[t] = 4u * row;
+        } else {
+            rows.w[t] = w2 + row * p.ldw2;
+            rows.sc[t] = sc + row;
         }
-        f32x4 acc[2][CG] = {};
-        products<M, false, CG>(w, wbytes, sc, p.H, p.F, x, (long long)slots * p.inner_cols * ES,
-                               acc);
+    }
+    f32x4 acc[NT] = {};
+    products<M, false, NT, EVEN>(
+        rows, p.inner, [&](int c) { return (long long)sh.slots[c] * p.inner_cols; }, p.F, cols,
+        live, part, p.parts, sh, acc);
+    give(acc, p.parts, sums);
+    if (!live || r >= cols)
+        return;
+    float *to = p.partial + (long long)sh.slots[r] * p.H;
 #pragma unroll
-        for (int g = 0; g < CG; ++g) {
-            float mine = join(acc[0][g], acc[1][g], sh);
-            const int h = h0 + (tid >> 4), c = c0 + 16 * g + (tid & 15);
-            if (h < p.H && c < n) {
-                if constexpr (M::I8)
-                    mine *= static_cast<const float *>(p.scale2)[(long long)e * p.H + h];
-                p.partial[(long long)sh.slots[c] * p.H + h] = mine;
-            }
+    for (int t = 0; t < NT; ++t) {
+        if ((t & (p.parts - 1)) != part)
+            continue;
+        f32x4 y = joined(acc, t, p.parts, sums);
+        const int h = h0 + 16 * t + 4 * (lane >> 4);
+        if constexpr (M::I8) {
+            const float *s = static_cast<const float *>(p.scale2) + (long long)e * p.H;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                y[v] *= s[min(h + v, p.H - 1)];
         }
-    };
-    int c0 = 0;
-    for (; n - c0 > 32; c0 += 64)
-        columns(c0, std::integral_constant<int, 4>{});
-    if (n - c0 > 16)
-        columns(c0, std::integral_constant<int, 2>{});
-    else if (n - c0 > 0)
-        columns(c0, std::integral_constant<int, 1>{});
+        if (h + 4 <= p.H) {
+            store16(to + h, __builtin_bit_cast(i32x4, y));
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (h + v < p.H)
+                    to[h + v] = y[v];
+        }
+    }
 }
 
-// out[t] = sum_j mix[t, j] partial[t, j]
+// out[t] = sum_j mix[t, j] partial[t, j]. (A slot without an expert has no
+// products: what is read in their place is not used, so that no read waits for
+// the ids.)
 template <typename X>
 __global__ void __launch_bounds__(256) layer_join_kernel(LayerParams p)
 {
     const long long at = blockIdx.x * 256LL + threadIdx.x;
     if (at >= (long long)p.tokens * p.H)
         return;
-    const int t = (int)(at / p.H), h = (int)(at % p.H);
+    const int t = (int)(at / p.H), h = (int)(at - (long long)t * p.H);
     float sum = 0.0f;
-    for (int j = 0; j < p.topk; ++j) {
-        const int slot = t * p.topk + j;
-        if (p.F > 0 && id_of(p, slot) >= 0)
-            sum = __builtin_fmaf(p.mix ? p.mix[slot] : 1.0f,
-                                 p.partial[(long long)slot * p.H + h], sum);
+    if (p.F > 0) {
+        constexpr int AT = 8;
+        for (int j0 = 0; j0 < p.topk; j0 += AT) {
+            float y[AT], w[AT];
+            bool there[AT];
+#pragma unroll
+            for (int j = 0; j < AT; ++j) {
+                const int slot = t * p.topk + min(j0 + j, p.topk - 1);
+                y[j] = p.partial[(long long)slot * p.H + h];
+                w[j] = p.mix ? p.mix[slot] : 1.0f;
+                there[j] = j0 + j < p.topk && id_of(p, slot) >= 0;
+            }
+#pragma unroll
+            for (int j = 0; j < AT; ++j)
+                sum = there[j] ? __builtin_fmaf(w[j], y[j], sum) : sum;
+        }
     }
     static_cast<X *>(p.out)[t * p.ldo + h] = (X)sum;
 }
 
+typedef void (*LayerFn)(LayerParams);
+
+// One of the two kernels: tiles of `rows` rows of `total`, a workgroup's waves
+// sharing them, K over them, as far as it takes for enough waves for the card.
+struct LayerStep {
+    LayerFn fn;
+    int tiles, parts;
+    long long blocks;
+};
+
+LayerStep layer_step(LayerFn fn, int total, int rows, double experts, int most, long long steps)
+{
+    LayerStep l{fn, (int)ceil_div_ll(total, rows), 1, 0};
+    while (l.parts < kLayerWaves && 2 * l.parts <= steps && experts * l.tiles * l.parts < 3000)
+        l.parts *= 2;
+    l.blocks = most * ceil_div_ll(l.tiles, kLayerWaves / l.parts);
+    return l;
+}
+
+hipError_t launch_step(const LayerStep &l, LayerParams p, hipStream_t s)
+{
+    p.tiles = l.tiles;
+    p.parts = l.parts;
+    void *args[] = {&p};
+    return hipLaunchKernel((const void *)l.fn, dim3((unsigned)l.blocks), dim3(kLayerThreads), args,
+                           0, s);
+}
+
 template <typename X, typename W> int launch_layer(LayerParams p, hipStream_t s)
 {
-    const int slots = p.tokens * p.topk, most = slots < p.experts ? slots : p.experts;
-    void *args[] = {&p};
-    hipError_t e = hipSuccess;
+    typedef Math<X, W, true> M;
+    const int slots = p.tokens * p.topk;
+    // Most groups of up to 16 slots of an expert: every named one may have one that
+    // is not full.
+    const int named = slots < p.experts ? slots : p.experts;
+    const int most = named + (slots - named) / kColumns;
+    p.inverse = inverse_of(p.topk);
     if (p.F > 0) {
-        p.tiles = (p.F + 15) / 16;
-        if (!fits_launch((double)most * p.tiles, kLayerThreads) ||
-            !fits_launch((double)most * ((p.H + kTileRows - 1) / kTileRows), kLayerThreads))
+        // Experts that even choices reach on average.
+        double missed = 1.0;
+        for (int i = 0; i < slots && missed > 1e-3; ++i)
+            missed *= 1.0 - 1.0 / p.experts;
+        const double reached = p.experts * (1.0 - missed) < 1.0 ? 1.0 : p.experts * (1.0 - missed);
+        auto row_bytes = [](long long K) {
+            return M::MX4 ? (K + 1) / 2 : M::I8 ? K : K * (long long)sizeof(X);
+        };
+        auto even = [&](const void *w, long long ld, long long stride, long long K, long long R) {
+            return (((uintptr_t)w | ld | stride | row_bytes(K)) & 15) == 0 && ld < 1 << 24 &&
+                   (!M::MX4 || (K % 32 == 0 && ceil_div_ll(K, 128) * 4 * R < INT32_MAX));
+        };
+        const bool even1 = even(p.W1, p.ldw1, p.strideW1, p.H, 2LL * p.F);
+        const bool even2 = even(p.W2, p.ldw2, p.strideW2, p.F, p.H);
+        const bool wide1 = even1 && reached * ceil_div_ll(p.F, 32) * kLayerWaves >= 3000;
+        const bool wide2 = even2 && reached * ceil_div_ll(p.H, 64) * kLayerWaves >= 3000;
+        const LayerFn up = !even1  ? layer_up_kernel<X, W, 2, false>
+                           : wide1 ? layer_up_kernel<X, W, 4, true>
+                                   : layer_up_kernel<X, W, 2, true>;
+        const LayerFn down = !even2  ? layer_down_kernel<X, W, 2, false>
+                             : wide2 ? layer_down_kernel<X, W, 4, true>
+                                     : layer_down_kernel<X, W, 2, true>;
+        const LayerStep a = layer_step(up, p.F, wide1 ? 32 : 16, reached, most,
+                                       ceil_div_ll(row_bytes(p.H), 64));
+        const LayerStep b = layer_step(down, p.H, wide2 ? 64 : 32, reached, most,
+                                       ceil_div_ll(row_bytes(p.F), 64));
+        if (!fits_launch((double)a.blocks, kLayerThreads) ||
+            !fits_launch((double)b.blocks, kLayerThreads))
             return -22;
-        e = hipLaunchKernel((const void *)layer_up_kernel<X, W>, dim3((unsigned)(most * p.tiles)),
-                            dim3(kLayerThreads), args, 0, s);
-        if (e != hipSuccess)
-            return (int)e;
-        p.tiles = (p.H + kTileRows - 1) / kTileRows;
-        e = hipLaunchKernel((const void *)layer_down_kernel<X, W>,
-                            dim3((unsigned)(most * p.tiles)), dim3(kLayerThreads), args, 0, s);
+        hipError_t e = launch_step(a, p, s);
+        if (e == hipSuccess)
+            e = launch_step(b, p, s);
         if (e != hipSuccess)
             return (int)e;
     }
     const long long items = (long long)p.tokens * p.H;
+    void *args[] = {&p};
     return (int)hipLaunchKernel((const void *)layer_join_kernel<X>,
                                 dim3((unsigned)ceil_div_ll(items, 256)), dim3(256), args, 0, s);
 }
@@ -573,13 +786,9 @@ bool layer_slots_ok(int tokens, int topk)
     return tokens >= 0 && (long long)tokens * (topk > 0 ? topk : 1) <= EXPERT_LAYER_MAX_SLOTS;
 }
 
-long long padded_cols(int F) { return ((long long)F + 127) / 128 * 128; }
+long long padded_cols(int F) { return ((long long)F + 3) / 4 * 4; }
 
-// Bytes of the inner values, a multiple of 16 (inner_cols is one of 128).
-size_t inner_bytes(long long slots, int F, int type)
-{
-    return (size_t)slots * padded_cols(F) * (type == SGEMM_F32 ? 6 : 4);
-}
+size_t inner_bytes(long long slots, int F) { return (size_t)slots * padded_cols(F) * sizeof(float); }
 
 // Bytes of a row of weights; ldw has to reach as far.
 long long weight_row(int K, int w_type)
@@ -595,7 +804,7 @@ extern "C" size_t expert_layer_workspace_size(int tokens, int topk, int H, int F
         F > kMaxWidth || !c_type_ok(type))
         return 0;
     const long long slots = (long long)tokens * topk;
-    return inner_bytes(slots, F, type) + (size_t)slots * H * sizeof(float);
+    return inner_bytes(slots, F) + (size_t)slots * H * sizeof(float);
 }
 
 extern "C" int expert_layer(int tokens, int topk, int experts, int H, int F, const void *X,
@@ -646,9 +855,9 @@ extern "C" int expert_layer(int tokens, int topk, int experts, int H, int F, con
     p.scale1 = scale1;
     p.scale2 = scale2;
     p.out = out;
-    p.inner = workspace;
+    p.inner = static_cast<float *>(workspace);
     p.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                          inner_bytes((long long)tokens * topk, F, type));
+                                          inner_bytes((long long)tokens * topk, F));
     p.strideW1 = strideW1 * es;
     p.strideW2 = strideW2 * es;
     p.ldw1 = (long long)ldw1 * es;

@@ -158,7 +158,7 @@ def test_oversize_grids_are_rejected(pg):
     assert call(pg, "mx4gemm_grouped", groups=65536, M=n, N=n, ldsa=n, ldsb=n, ldc=n) == -22
     size = pg._load().expert_layer_workspace_size(256, 8, 1 << 20, 1 << 20, 2)
     assert call(pg, "expert_layer", tokens=256, topk=8, experts=1024, H=1 << 20, F=1 << 20,
-                ldx=1 << 20, ldw1=1 << 20, ldw2=1 << 20, ldo=1 << 20,
+                ldx=1 << 20, ldw1=(1 << 20) + 1, ldw2=1 << 20, ldo=1 << 20,
                 workspace_bytes=size) == -22
 
 
