@@ -121,9 +121,10 @@ enum mx4gemm_kernel {
     MX4GEMM_KERNEL_L64x64 = 7,
     MX4GEMM_KERNEL_L64x128 = 8,
     MX4GEMM_KERNEL_L128x128 = 9,
-    MX4GEMM_KERNEL_L128x256 = 10,
-    MX4GEMM_KERNEL_L256x256 = 11,
-    MX4GEMM_KERNEL_COUNT = 12
+    MX4GEMM_KERNEL_L128x128_R2 = 10, /* two stages of LDS instead of four */
+    MX4GEMM_KERNEL_L128x256 = 11,
+    MX4GEMM_KERNEL_L256x256 = 12,
+    MX4GEMM_KERNEL_COUNT = 13
 };
 
 /*

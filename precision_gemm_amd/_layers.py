@@ -21,7 +21,7 @@ EXPERT_LAYER_MAX_EXPERTS = 1024
 # Kernels of the 4-bit product by number (mx4gemm_kernel of the C header): S
 # stream B, T take rows of any alignment, L load straight into LDS.
 MX4GEMM_KERNELS = ("S16x16", "S16x32", "S32x16", "S32x32", "S32x64", "T64x64", "T128x128",
-                   "L64x64", "L64x128", "L128x128", "L128x256", "L256x256")
+                   "L64x64", "L64x128", "L128x128", "L128x128_R2", "L128x256", "L256x256")
 
 torch = _experts.torch
 if torch is not None:

@@ -18,25 +18,43 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // a block of 32, a wave 512 elements of a row.
 // ---------------------------------------------------------------------------
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *row, int k, int K, float (&f)[8])
-{
-    if (k + 8 <= K) {
-        constexpr int VEC = 16 / sizeof(T);
+// A lane's eight elements as they lie in memory (WHOLE: the wave's 512 are all
+// there, so that no load stands in a branch), zeros behind the row's end.
+template <typename T> struct Eight {
+    static constexpr int VEC = 16 / (int)sizeof(T), N = 8 / VEC;
+    i32x4 raw[N];
+
+    template <bool WHOLE> __device__ __forceinline__ void load(const T *row, int k, int K)
+    {
+        if (WHOLE || k + 8 <= K) {
 #pragma unroll
-        for (int i = 0; i < 8; i += VEC) {
+            for (int i = 0; i < N; ++i)
+                raw[i] = load16(row + k + i * VEC);
+        } else {
+            typedef T tv __attribute__((ext_vector_type(VEC)));
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                tv v;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    v[e] = k + i * VEC + e < K ? row[k + i * VEC + e] : (T)0.0f;
+                raw[i] = __builtin_bit_cast(i32x4, v);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void floats(float (&f)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
             float v[VEC];
-            unpack<T>(load16(row + k + i), v);
+            unpack<T>(raw[i], v);
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                f[i + e] = v[e];
+                f[i * VEC + e] = v[e];
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = k + i < K ? (float)row[k + i] : 0.0f;
     }
-}
+};
 
 // The four bytes of eight elements' codes at q + k / 2, as far as the row goes.
 __device__ __forceinline__ void store_codes(unsigned char *q, int k, int K, uint32_t codes)
@@ -51,8 +69,10 @@ __device__ __forceinline__ void store_codes(unsigned char *q, int k, int K, uint
     }
 }
 
-// 32 rows (RW of each of the 32 / RW waves) of 512 elements a workgroup, so that
-// the scales leave as whole lines of neighbouring rows.
+// ROWS rows of 512 elements a workgroup, RW a wave, all loaded before the first is
+// rounded; the scales leave as neighbouring rows' words. Bound by memory: 16 rows,
+// 4 a wave (8192 x 4092 in fp32 40 us, 3.8 TB/s; 32 rows, 8 a wave, 44), few rows
+// one a wave (16 x 4096 in bf16 2.6 us, a launch and one trip to memory).
 // A block's scale byte is the exponent field of its largest magnitude less 2
 // (fields are offset by 127 as the bytes are; subnormal ones have field 0), and
 // 2^-e is the number of field 254 - byte, so the quotient is an exact product
@@ -66,19 +86,27 @@ mx4_quantize_kernel(int M, int K, const T *X, long long ldx, unsigned char *Q, l
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int k = blockIdx.x * 512 + 8 * lane;
     const long long m0 = (long long)blockIdx.y * ROWS;
-    float f[RW][8];
+    Eight<T> held[RW];
+    auto load = [&](auto whole) {
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            const long long m = m0 + wave * RW + r;
+            held[r].template load<decltype(whole)::value>(X + (m < M ? m : M - 1) * ldx, k, K);
+        }
+    };
+    if ((int)blockIdx.x * 512 + 512 <= K)
+        load(std::true_type{});
+    else
+        load(std::false_type{});
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
         const long long m = m0 + wave * RW + r;
-        load8<T>(X + (m < M ? m : M - 1) * ldx, k, K, f[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < RW; ++r) {
-        const long long m = m0 + wave * RW + r;
+        float f[8];
+        held[r].floats(f);
         uint32_t peak = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            peak = max(peak, __builtin_bit_cast(uint32_t, f[r][i]) & 0x7fffffffu);
+            peak = max(peak, __builtin_bit_cast(uint32_t, f[i]) & 0x7fffffffu);
         peak = max(peak, (uint32_t)__shfl_xor((int)peak, 1));
         peak = max(peak, (uint32_t)__shfl_xor((int)peak, 2));
         const int field = (int)(peak >> 23);
@@ -86,10 +114,10 @@ mx4_quantize_kernel(int M, int K, const T *X, long long ldx, unsigned char *Q, l
         const int byte = finite ? max(field - 2, 0) : 255;
         const float up = __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23);
         uint32_t codes = 0;
-        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[r][0] * up, f[r][1] * up, 1.0f, 0);
-        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[r][2] * up, f[r][3] * up, 1.0f, 1);
-        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[r][4] * up, f[r][5] * up, 1.0f, 2);
-        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[r][6] * up, f[r][7] * up, 1.0f, 3);
+        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[0] * up, f[1] * up, 1.0f, 0);
+        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[2] * up, f[3] * up, 1.0f, 1);
+        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[4] * up, f[5] * up, 1.0f, 2);
+        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, f[6] * up, f[7] * up, 1.0f, 3);
         if (m < M && k < K)
             store_codes(Q + m * ldq, k, K, finite ? codes : 0u);
         // Four blocks' bytes in one word; 0 for blocks behind the row's last.
@@ -116,8 +144,8 @@ int launch_mx4_quantize(int M, int K, const void *X, long long ldx, unsigned cha
     typedef void (*Fn)(int, int, const T *, long long, unsigned char *, long long, unsigned char *,
                        long long);
     const bool few = M <= 64;
-    const Fn fn = few ? mx4_quantize_kernel<T, 4, 1> : mx4_quantize_kernel<T, 32, 8>;
-    const int rows = few ? 4 : 32;
+    const Fn fn = few ? mx4_quantize_kernel<T, 4, 1> : mx4_quantize_kernel<T, 16, 4>;
+    const int rows = few ? 4 : 16;
     const unsigned columns = (unsigned)ceil_div_ll(K, 512);
     // Rows in launches of fewer than 2^32 work-items and 65536 rows of workgroups.
     long long most = (1LL << 23) / columns;
@@ -558,6 +586,7 @@ struct Mx4Core {
     static constexpr int SLOADS = (BM + BN) / 32, NS = (SLOADS + NW - 1) / NW;
     static constexpr int LOADS = NA + NB + NS;
     static_assert(NA >= 1 && NB >= 1, "a wave loads of both operands");
+    static_assert(STAGE == (BM + BN) * 136, "a row's bytes and its words");
     static_assert(BM % 64 == 0 && BN % 64 == 0, "a load's words belong to one operand");
     static constexpr int PATCH = 16 * WN * 4; // bytes of LDS a wave's outputs turn over in
 
@@ -809,15 +838,12 @@ struct Mx4Core {
 };
 
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
-__global__ void
-__attribute__((amdgpu_flat_work_group_size(64 * WAVES_M * WAVES_N, 64 * WAVES_M * WAVES_N)))
-mx4_large_kernel(Mx4Params p)
+__device__ __forceinline__ void mx4_large_tile(const Mx4Params &p, signed char *lds)
 {
     typedef Mx4Core<BM, BN, WAVES_M, WAVES_N> Core;
     constexpr int LOADS = Core::LOADS;
     static_assert(STAGES >= 2 && (STAGES - 1) * LOADS <= 63, "loads in flight");
     static_assert(Core::NW * Core::PATCH <= STAGES * Core::STAGE, "the patches fit in the stages");
-    __shared__ __attribute__((aligned(1024))) signed char lds[STAGES * Core::STAGE];
 
     Mx4Tile t;
     if (!mx4_tile_of<BM, BN>(p, t))
@@ -865,6 +891,15 @@ mx4_large_kernel(Mx4Params p)
         c.outputs(p, t, reinterpret_cast<float *>(lds + c.wave * Core::PATCH));
 }
 
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+__global__ void
+__attribute__((amdgpu_flat_work_group_size(64 * WAVES_M * WAVES_N, 64 * WAVES_M * WAVES_N)))
+mx4_large_kernel(Mx4Params p)
+{
+    __shared__ __attribute__((aligned(1024))) signed char lds[STAGES * (BM + BN) * 136];
+    mx4_large_tile<BM, BN, WAVES_M, WAVES_N, STAGES>(p, lds);
+}
+
 typedef void (*Mx4Fn)(Mx4Params);
 
 struct Mx4Variant {
@@ -890,6 +925,7 @@ Mx4Variant variant_of(int kernel)
     case MX4GEMM_KERNEL_L64x64: return {mx4_large_kernel<64, 64, 2, 2, 3>, 64, 64, 256};
     case MX4GEMM_KERNEL_L64x128: return {mx4_large_kernel<64, 128, 2, 2, 3>, 64, 128, 256};
     case MX4GEMM_KERNEL_L128x128: return {mx4_large_kernel<128, 128, 2, 4, 4>, 128, 128, 512};
+    case MX4GEMM_KERNEL_L128x128_R2: return {mx4_large_kernel<128, 128, 2, 4, 2>, 128, 128, 512};
     case MX4GEMM_KERNEL_L128x256: return {mx4_large_kernel<128, 256, 2, 4, 3>, 128, 256, 512};
     default: return {mx4_large_kernel<256, 256, 2, 4, 2>, 256, 256, 512};
     }
@@ -897,15 +933,19 @@ Mx4Variant variant_of(int kernel)
 
 // The tiles that load straight into LDS, with what they cost on 256 CUs
 // (measured, us): a lone tile a CU takes 4.5 and `wait` for 256 of K, its loads'
-// way; a CU with tiles enough takes `fixed` and `step` for 256 of K of each.
+// way; a CU with tiles enough takes `fixed` and `step` for 256 of K of each. (The
+// 128 x 128 tile with two stages of LDS for four has two workgroups a CU, whose
+// outputs and first loads run under each other's products: 2048 x 4096 x 4096
+// 28 us against 32, a tile a CU, 1024 x 4096 x 4096, 20.4 against 17.7.)
 struct Mx4Large {
     int kernel, bm, bn;
     float wait, fixed, step;
 };
 const Mx4Large kLarge[] = {
-    {MX4GEMM_KERNEL_L64x64, 64, 64, 0.32f, 1.6f, 0.172f},
-    {MX4GEMM_KERNEL_L64x128, 64, 128, 0.50f, 2.3f, 0.326f},
+    {MX4GEMM_KERNEL_L64x64, 64, 64, 0.32f, 2.2f, 0.15f},
+    {MX4GEMM_KERNEL_L64x128, 64, 128, 0.50f, 3.2f, 0.29f},
     {MX4GEMM_KERNEL_L128x128, 128, 128, 0.76f, 4.2f, 0.64f},
+    {MX4GEMM_KERNEL_L128x128_R2, 128, 128, 0.99f, 4.0f, 0.52f},
     {MX4GEMM_KERNEL_L128x256, 128, 256, 1.02f, 6.5f, 1.05f},
     {MX4GEMM_KERNEL_L256x256, 256, 256, 1.70f, 10.8f, 1.70f},
 };

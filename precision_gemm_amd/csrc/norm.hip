@@ -61,30 +61,36 @@ __device__ __forceinline__ void load_weights(const float *w, int k, int K, float
     }
 }
 
-// N values of every thread added over the NT threads of a row, in a fixed
-// order. `shared`: N * NT / 64 floats where NT > 64.
+// N values of every thread added over the NT threads of a row, in a fixed order,
+// and the largest of their peaks. `shared`: (N + 1) * NT / 64 words where NT > 64,
+// which the caller's last row has left.
 template <int NT, int N>
-__device__ __forceinline__ void add_row(float (&v)[N], float *shared)
+__device__ __forceinline__ void over_row(float (&v)[N], uint32_t &peak, uint32_t *shared)
 {
 #pragma unroll
-    for (int d = 1; d < (NT < 64 ? NT : 64); d <<= 1)
+    for (int d = 1; d < (NT < 64 ? NT : 64); d <<= 1) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             v[i] += __shfl_xor(v[i], d);
+        peak = max(peak, (uint32_t)__shfl_xor((int)peak, d));
+    }
     if constexpr (NT > 64) {
         const int wave = threadIdx.x >> 6;
-        __syncthreads(); // (the last row's values have been read)
-        if ((threadIdx.x & 63) == 0)
+        if ((threadIdx.x & 63) == 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                shared[wave * N + i] = v[i];
+                shared[wave * (N + 1) + i] = __builtin_bit_cast(uint32_t, v[i]);
+            shared[wave * (N + 1) + N] = peak;
+        }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v[i] = shared[i];
+        for (int w = 0; w < NT / 64; ++w) {
 #pragma unroll
-            for (int w = 1; w < NT / 64; ++w)
-                v[i] += shared[w * N + i];
+            for (int i = 0; i < N; ++i) {
+                const float f = __uint_as_float(shared[w * (N + 1) + i]);
+                v[i] = w == 0 ? f : v[i] + f;
+            }
+            peak = max(peak, shared[w * (N + 1) + N]);
         }
     }
 }
@@ -115,8 +121,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(NormParams p)
     constexpr bool I8 = std::is_same<Out, signed char>::value;
     constexpr int ROWS = NT < 256 ? 256 / NT : 1, WAVES = NT / 64;
     static_assert(NT <= 64 || ROWS == 1, "a row is a part of a wave, a wave or a workgroup");
-    __shared__ float sums[NT > 64 ? WAVES : 1];
-    __shared__ uint32_t peaks[NT > 64 ? WAVES : 1];
+    __shared__ uint32_t shared[NT > 64 ? 2 * WAVES : 1];
     const int t = threadIdx.x % NT;
     const long long m = (long long)blockIdx.x * ROWS + threadIdx.x / NT;
     if (m >= p.M)
@@ -138,52 +143,48 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(NormParams p)
     };
     float squares[1] = {0.0f};
     uint32_t peak = 0; // of |t| as ordered integers: NaN above infinity
-    auto take = [&](int k, const float (&h)[VEC]) {
-        if (hrow && k < p.K)
-            store_row<T>(hrow, k, p.K, h);
+    auto take = [&](int k, const float (&h)[VEC], const float (&w)[VEC]) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
             squares[0] = __builtin_fmaf(h[i], h[i], squares[0]);
-        if constexpr (I8) {
-            float w[VEC];
-            load_weights<VEC>(p.weight, k, p.K, w);
+        if constexpr (I8)
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
                 peak = max(peak, __builtin_bit_cast(uint32_t, h[i] * w[i]) & 0x7fffffffu);
-        }
     };
-    float held[CH > 0 ? CH : 1][VEC];
+    // The weights are loaded along with the row, one trip to memory, where there
+    // are registers for both.
+    constexpr bool EARLY = CH > 0 && CH * VEC <= 32;
+    float held[CH > 0 ? CH : 1][VEC], weights[EARLY ? CH : 1][VEC];
     if constexpr (CH > 0) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c) {
             sum_of((c * NT + t) * VEC, held[c]);
+            if constexpr (EARLY)
+                load_weights<VEC>(p.weight, (c * NT + t) * VEC, p.K, weights[c]);
+        }
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-            take((c * NT + t) * VEC, held[c]);
+        for (int c = 0; c < CH; ++c) {
+            if constexpr (!EARLY && I8)
+                load_weights<VEC>(p.weight, (c * NT + t) * VEC, p.K, weights[0]);
+            take((c * NT + t) * VEC, held[c], weights[EARLY ? c : 0]);
+        }
     } else {
         for (int k = t * VEC; k < p.K; k += NT * VEC) {
-            float h[VEC];
+            float h[VEC], w[VEC] = {};
             sum_of(k, h);
-            take(k, h);
+            if constexpr (I8)
+                load_weights<VEC>(p.weight, k, p.K, w);
+            if (hrow)
+                store_row<T>(hrow, k, p.K, h);
+            take(k, h, w);
         }
     }
-    add_row<NT, 1>(squares, sums);
+    over_row<NT, 1>(squares, peak, shared);
     const float rstd = rstd_of(squares[0], p.K, p.eps);
     float s = 0.0f, inv = 0.0f;
     bool finite = true;
     if constexpr (I8) {
-#pragma unroll
-        for (int d = 1; d < (NT < 64 ? NT : 64); d <<= 1)
-            peak = max(peak, (uint32_t)__shfl_xor((int)peak, d));
-        if constexpr (NT > 64) {
-            if ((t & 63) == 0)
-                peaks[t >> 6] = peak;
-            __syncthreads();
-            peak = peaks[0];
-#pragma unroll
-            for (int w = 1; w < WAVES; ++w)
-                peak = max(peak, peaks[w]);
-        }
         const float top = __builtin_bit_cast(float, peak);
         finite = peak < 0x7f800000u;
         s = finite ? __builtin_fmaxf(top / 127.0f, kLeastScale) : __builtin_nanf("");
@@ -192,9 +193,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(NormParams p)
             p.scale[m] = s * rstd;
     }
 
-    auto put = [&](int k, const float (&h)[VEC]) {
-        float w[VEC];
-        load_weights<VEC>(p.weight, k, p.K, w);
+    auto put = [&](int k, const float (&h)[VEC], const float (&w)[VEC]) {
         if constexpr (I8) {
             uint32_t b[VEC / 4];
 #pragma unroll
@@ -226,17 +225,23 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(NormParams p)
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int k = (c * NT + t) * VEC;
-            if (k < p.K)
-                put(k, held[c]);
+            if constexpr (!EARLY)
+                load_weights<VEC>(p.weight, k, p.K, weights[0]);
+            if (k >= p.K)
+                continue;
+            if (hrow) // (behind the meeting, which would wait for it)
+                store_row<T>(hrow, k, p.K, held[c]);
+            put(k, held[c], weights[EARLY ? c : 0]);
         }
     } else {
         for (int k = t * VEC; k < p.K; k += NT * VEC) {
-            float h[VEC];
+            float h[VEC], w[VEC];
+            load_weights<VEC>(p.weight, k, p.K, w);
             if (hrow)
                 load_row<T>(hrow, k, p.K, h);
             else
                 sum_of(k, h);
-            put(k, h);
+            put(k, h, w);
         }
     }
 }
@@ -263,8 +268,14 @@ int launch_norm(NormParams p, hipStream_t s)
         fn = norm_kernel<T, Out, 64, 1>;
         rows = 4;
     } else if (chunks <= 256) {
-        fn = norm_kernel<T, Out, 64, 4>;
-        rows = 4;
+        // (A wave with four chunks a lane: 16384 x 2048 in bf16 62 us against 52,
+        // 64 x 2048 7.8 against 4.0.)
+        fn = norm_kernel<T, Out, 256, 1>;
+    } else if (chunks <= 512 && p.M <= 1024) {
+        // Few rows: half the work a thread (4 x 4096 in bf16: 3.9 us against 5.3;
+        // 16384 rows 104 against 99).
+        fn = norm_kernel<T, Out, 512, 1>;
+        threads = 512;
     } else if (chunks <= 512) {
         fn = norm_kernel<T, Out, 256, 2>;
     } else if (chunks <= 1024) {
@@ -328,23 +339,26 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_grad_kernel(GradPara
 {
     constexpr int VEC = kVec<T>;
     constexpr int ROWS = NT < 256 ? 256 / NT : 1, WAVES = NT / 64;
-    __shared__ float sums[NT > 64 ? 2 * WAVES : 1];
+    __shared__ uint32_t shared[2][NT > 64 ? 3 * WAVES : 1]; // of rows by parity
     const int t = threadIdx.x % NT;
     const long long group = (long long)blockIdx.x * ROWS + threadIdx.x / NT;
     float w[CH][VEC], dw[CH][VEC] = {};
 #pragma unroll
     for (int c = 0; c < CH; ++c)
         load_weights<VEC>(p.weight, (c * NT + t) * VEC, p.K, w[c]);
+    int turn = 0;
     for (long long m = group; m < p.M; m += (long long)gridDim.x * ROWS) {
         const T *dy = static_cast<const T *>(p.dY) + m * p.lddy;
         const T *h = static_cast<const T *>(p.H) + m * p.ldh;
         const T *dh = p.dH ? static_cast<const T *>(p.dH) + m * p.lddh : nullptr;
         T *dx = static_cast<T *>(p.dX) + m * p.lddx;
-        float g[CH][VEC], x[CH][VEC], v[2] = {0.0f, 0.0f};
+        float g[CH][VEC], x[CH][VEC], d[CH][VEC] = {}, v[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             load_row<T>(dy, (c * NT + t) * VEC, p.K, g[c]);
             load_row<T>(h, (c * NT + t) * VEC, p.K, x[c]);
+            if (dh)
+                load_row<T>(dh, (c * NT + t) * VEC, p.K, d[c]);
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -353,7 +367,8 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_grad_kernel(GradPara
                 v[0] = __builtin_fmaf(x[c][i], x[c][i], v[0]);
                 v[1] = __builtin_fmaf(w[c][i] * g[c][i], x[c][i], v[1]);
             }
-        add_row<NT, 2>(v, sums);
+        uint32_t none = 0;
+        over_row<NT, 2>(v, none, shared[turn ^= 1]);
         const float rstd = rstd_of(v[0], p.K, p.eps);
         const float along = v[1] / (float)p.K * rstd * rstd;
 #pragma unroll
@@ -361,15 +376,12 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_grad_kernel(GradPara
             const int k = (c * NT + t) * VEC;
             if (k >= p.K)
                 continue;
-            float d[VEC] = {};
-            if (dh)
-                load_row<T>(dh, k, p.K, d);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 dw[c][i] = __builtin_fmaf(g[c][i], x[c][i] * rstd, dw[c][i]);
-                d[i] = __builtin_fmaf(rstd, w[c][i] * g[c][i] - x[c][i] * along, d[i]);
+                d[c][i] = __builtin_fmaf(rstd, w[c][i] * g[c][i] - x[c][i] * along, d[c][i]);
             }
-            store_row<T>(dx, k, p.K, d);
+            store_row<T>(dx, k, p.K, d[c]);
         }
     }
     if (p.partial == nullptr)
@@ -385,29 +397,39 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_grad_kernel(GradPara
         }
 }
 
-// dweight[k] = sum of the row groups' sums: 32 columns a workgroup, the groups
-// over its 32 waves' halves.
-constexpr int kAddThreads = 1024;
+// dweight[k] = sum of the row groups' sums: 16 columns a workgroup, the groups
+// over 64 threads each.
+constexpr int kAddThreads = 1024, kAddColumns = 16;
 
 __global__ void __launch_bounds__(kAddThreads)
 norm_grad_add_kernel(const float *partial, int groups, int K, float *dweight)
 {
-    constexpr int PARTS = kAddThreads / 32;
-    __shared__ float part[PARTS][33];
-    const int c = threadIdx.x & 31, at = threadIdx.x >> 5;
-    const int k = blockIdx.x * 32 + c;
+    constexpr int PARTS = kAddThreads / kAddColumns;
+    __shared__ float part[PARTS][kAddColumns + 1];
+    const int c = threadIdx.x % kAddColumns, at = threadIdx.x / kAddColumns;
+    const int k = blockIdx.x * kAddColumns + c;
     float sum = 0.0f;
-    if (k < K)
-        for (int g = at; g < groups; g += PARTS)
+    if (k < K) {
+        int g = at;
+        for (; g + 3 * PARTS < groups; g += 4 * PARTS) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = partial[(long long)(g + i * PARTS) * K + k];
+            sum += (v[0] + v[1]) + (v[2] + v[3]);
+        }
+        for (; g < groups; g += PARTS)
             sum += partial[(long long)g * K + k];
+    }
     part[at][c] = sum;
     __syncthreads();
-    if (at == 0 && k < K) {
-#pragma unroll
-        for (int i = 1; i < PARTS; ++i)
-            sum += part[i][c];
-        dweight[k] = sum;
+    for (int n = PARTS / 2; n > 0; n >>= 1) {
+        if (at < n)
+            part[at][c] += part[at + n][c];
+        __syncthreads();
     }
+    if (at == 0 && k < K)
+        dweight[k] = part[0][c];
 }
 
 typedef void (*GradFn)(GradParams);
@@ -417,6 +439,10 @@ struct GradPlan {
     int threads, rows; // a workgroup
     int blocks;
 };
+
+static_assert(RMS_NORM_GRAD_MAX_K <= 1024 * 2 * kVec<_Float16> &&
+                  RMS_NORM_GRAD_MAX_K <= 1024 * 4 * kVec<float>,
+              "the widest kernels hold a row");
 
 template <typename T>
 GradPlan grad_plan_of(int M, int K)
@@ -435,9 +461,9 @@ GradPlan grad_plan_of(int M, int K)
         g = {norm_grad_kernel<T, 256, 2>, 256, 1, 0};
     else if (chunks <= 1024)
         g = {norm_grad_kernel<T, 512, 2>, 512, 1, 0};
-    else if (chunks <= 2048)
+    else if (chunks <= 2048 || sizeof(T) == 2)
         g = {norm_grad_kernel<T, 1024, 2>, 1024, 1, 0};
-    else
+    else if constexpr (sizeof(T) == 4)
         g = {norm_grad_kernel<T, 1024, 4>, 1024, 1, 0};
     const long long blocks = ceil_div_ll(M, g.rows);
     g.blocks = (int)(blocks < 1024 ? blocks : 1024);
@@ -562,5 +588,5 @@ extern "C" int rms_norm_grad(int M, int K, const void *dY, int type, int lddy, c
     int groups = g.blocks * g.rows;
     void *args[] = {&partial, &groups, &K, &dweight};
     return (int)hipLaunchKernel((const void *)norm_grad_add_kernel,
-                                dim3((unsigned)ceil_div_ll(K, 32)), dim3(kAddThreads), args, 0, s);
+                                dim3((unsigned)ceil_div_ll(K, kAddColumns)), dim3(kAddThreads), args, 0, s);
 }

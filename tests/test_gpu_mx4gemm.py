@@ -245,7 +245,8 @@ def test_larger_products(env, M, N, K):
 KERNEL_SIZES = [("S16x16", 7, 300, 480), ("S16x32", 9, 16400, 96), ("S32x16", 45, 600, 352),
                 ("S32x32", 40, 4000, 160), ("S32x64", 20, 10000, 160), ("T64x64", 300, 2000, 1000),
                 ("T128x128", 2050, 2060, 333), ("L64x64", 100, 4100, 352),
-                ("L64x128", 500, 4000, 1056), ("L128x128", 1000, 4000, 1056),
+                ("L64x128", 500, 4000, 1056), ("L128x128", 500, 4100, 2080),
+                ("L128x128_R2", 1000, 4000, 1056),
                 ("L128x256", 1500, 3000, 288), ("L256x256", 3900, 2100, 288)]
 
 

@@ -162,8 +162,8 @@ def test_oversize_grids_are_rejected(pg):
                 workspace_bytes=size) == -22
 
 
-MX4_THREADS = dict(S16x16=512, S32x16=512, S32x32=512, L128x128=512, L128x256=512,
-                   L256x256=512)  # others 256
+MX4_THREADS = dict(S16x16=512, S32x16=512, S32x32=512, L128x128=512, L128x128_R2=512,
+                   L128x256=512, L256x256=512)  # others 256
 
 
 def mx4_work_items(name, M, N, groups):
