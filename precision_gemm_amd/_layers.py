@@ -58,10 +58,6 @@ def declare(lib):
     _lib = lib
 
 
-def _call(*args):
-    return _experts._call(*args)
-
-
 def _workspace(workspace, device):
     if workspace is None:
         return None, 0
@@ -84,29 +80,30 @@ def _scales(K, lds, rows):
     return 0
 
 
-def _norm_operands(M, K, X, ldx, R, ldr, weight, eps, H, ldh):
-    d = _first("X", X)
-    return d, (_at("X", X, _FLOATS, d, _span(M, K, ldx)), _TYPES[X.dtype], ldx,
-               None if R is None else _at("R", R, (X.dtype,), d, _span(M, K, ldr)), ldr,
-               _at("weight", weight, _F32, d, K, True), float(eps),
-               None if H is None else _at("H", H, (X.dtype,), d, _span(M, K, ldh)), ldh)
-
-
 def rms_norm(M, K, X, ldx, R, ldr, weight, eps, H, ldh, Y, ldy, stream=None, check=True) -> int:
     """C ABI ``rms_norm``: H = X + R, Y = H / sqrt(mean(H^2) + eps) * weight; X,
     R, H and Y of one type (fp32, fp16 or bf16), R and H may be None."""
-    d, args = _norm_operands(M, K, X, ldx, R, ldr, weight, eps, H, ldh)
-    return _call(_lib.rms_norm, d, stream, check, M, K, *args,
-                 _at("Y", Y, (X.dtype,), d, _span(M, K, ldy)), ldy)
+    d = _first("X", X)
+    dt = (X.dtype,)
+    return _experts._call(
+        _lib.rms_norm, d, stream, check, M, K, _at("X", X, _FLOATS, d, _span(M, K, ldx)),
+        _TYPES[X.dtype], ldx, None if R is None else _at("R", R, dt, d, _span(M, K, ldr)), ldr,
+        _at("weight", weight, _F32, d, K, True), float(eps),
+        None if H is None else _at("H", H, dt, d, _span(M, K, ldh)), ldh,
+        _at("Y", Y, dt, d, _span(M, K, ldy)), ldy)
 
 
 def rms_norm_i8(M, K, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, scale, stream=None,
                 check=True) -> int:
     """C ABI ``rms_norm_i8``: the same in int8 with one fp32 scale a row."""
-    d, args = _norm_operands(M, K, X, ldx, R, ldr, weight, eps, H, ldh)
-    return _call(_lib.rms_norm_i8, d, stream, check, M, K, *args,
-                 _at("Q", Q, _INT8, d, _span(M, K, ldq)), ldq,
-                 _at("scale", scale, _F32, d, M, True))
+    d = _first("X", X)
+    dt = (X.dtype,)
+    return _experts._call(
+        _lib.rms_norm_i8, d, stream, check, M, K, _at("X", X, _FLOATS, d, _span(M, K, ldx)),
+        _TYPES[X.dtype], ldx, None if R is None else _at("R", R, dt, d, _span(M, K, ldr)), ldr,
+        _at("weight", weight, _F32, d, K, True), float(eps),
+        None if H is None else _at("H", H, dt, d, _span(M, K, ldh)), ldh,
+        _at("Q", Q, _INT8, d, _span(M, K, ldq)), ldq, _at("scale", scale, _F32, d, M, True))
 
 
 def rms_norm_grad_workspace_size(M, K, dtype) -> int:
@@ -120,32 +117,36 @@ def rms_norm_grad(M, K, dY, lddy, H, ldh, weight, eps, dH, lddh, dX, lddx, dweig
     (or None); workspace: a GPU tensor of any type, or None without dweight."""
     d = _first("dY", dY)
     dt = (dY.dtype,)
-    args = (_at("dY", dY, _FLOATS, d, _span(M, K, lddy)), _TYPES[dY.dtype], lddy,
-            _at("H", H, dt, d, _span(M, K, ldh)), ldh, _at("weight", weight, _F32, d, K, True),
-            float(eps), None if dH is None else _at("dH", dH, dt, d, _span(M, K, lddh)), lddh,
-            _at("dX", dX, dt, d, _span(M, K, lddx)), lddx,
-            None if dweight is None else _at("dweight", dweight, _F32, d, K, True))
-    return _call(_lib.rms_norm_grad, d, stream, check, M, K, *args, *_workspace(workspace, d))
+    return _experts._call(
+        _lib.rms_norm_grad, d, stream, check, M, K, _at("dY", dY, _FLOATS, d, _span(M, K, lddy)),
+        _TYPES[dY.dtype], lddy, _at("H", H, dt, d, _span(M, K, ldh)), ldh,
+        _at("weight", weight, _F32, d, K, True), float(eps),
+        None if dH is None else _at("dH", dH, dt, d, _span(M, K, lddh)), lddh,
+        _at("dX", dX, dt, d, _span(M, K, lddx)), lddx,
+        None if dweight is None else _at("dweight", dweight, _F32, d, K, True),
+        *_workspace(workspace, d))
 
 
 def mx4_quantize_rows(M, K, X, ldx, Q, ldq, scale, lds, stream=None, check=True) -> int:
     """C ABI ``mx4_quantize_rows``: rows of X (fp32, fp16 or bf16) to 4-bit
     blocks, two elements a byte of Q, with their scales."""
     d = _first("X", X)
-    return _call(_lib.mx4_quantize_rows, d, stream, check, M, K,
-                 _at("X", X, _FLOATS, d, _span(M, K, ldx)), _TYPES[X.dtype], ldx,
-                 _at("Q", Q, _MX4, d, _span(M, _bytes(K), ldq)), ldq,
-                 _at("scale", scale, _MX4_SCALE, d, _scales(K, lds, M), True), lds)
+    return _experts._call(
+        _lib.mx4_quantize_rows, d, stream, check, M, K,
+        _at("X", X, _FLOATS, d, _span(M, K, ldx)), _TYPES[X.dtype], ldx,
+        _at("Q", Q, _MX4, d, _span(M, _bytes(K), ldq)), ldq,
+        _at("scale", scale, _MX4_SCALE, d, _scales(K, lds, M), True), lds)
 
 
 def mx4_dequantize_rows(M, K, Q, ldq, scale, lds, Y, ldy, stream=None, check=True) -> int:
     """C ABI ``mx4_dequantize_rows``: the blocks' values in Y (fp32, fp16 or
     bf16)."""
     d = _first("Q", Q)
-    return _call(_lib.mx4_dequantize_rows, d, stream, check, M, K,
-                 _at("Q", Q, _MX4, d, _span(M, _bytes(K), ldq)), ldq,
-                 _at("scale", scale, _MX4_SCALE, d, _scales(K, lds, M), True), lds,
-                 _at("Y", Y, _FLOATS, d, _span(M, K, ldy)), _TYPES[Y.dtype], ldy)
+    return _experts._call(
+        _lib.mx4_dequantize_rows, d, stream, check, M, K,
+        _at("Q", Q, _MX4, d, _span(M, _bytes(K), ldq)), ldq,
+        _at("scale", scale, _MX4_SCALE, d, _scales(K, lds, M), True), lds,
+        _at("Y", Y, _FLOATS, d, _span(M, K, ldy)), _TYPES[Y.dtype], ldy)
 
 
 def mx4gemm(M, N, K, A, lda, scaleA, ldsa, B, ldb, scaleB, ldsb, bias, C, ldc, stream=None,
@@ -154,13 +155,14 @@ def mx4gemm(M, N, K, A, lda, scaleA, ldsa, B, ldb, scaleB, ldsb, bias, C, ldc, s
     blocks, bias fp32 or None, C fp32, fp16 or bf16."""
     d = _first("A", A)
     width = _bytes(K)
-    return _call(_lib.mx4gemm, d, stream, check, M, N, K,
-                 _at("A", A, _MX4, d, _span(M, width, lda)), lda,
-                 _at("scaleA", scaleA, _MX4_SCALE, d, _scales(K, ldsa, M), True), ldsa,
-                 _at("B", B, _MX4, d, _span(N, width, ldb)), ldb,
-                 _at("scaleB", scaleB, _MX4_SCALE, d, _scales(K, ldsb, N), True), ldsb,
-                 None if bias is None else _at("bias", bias, _F32, d, N, True),
-                 _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
+    return _experts._call(
+        _lib.mx4gemm, d, stream, check, M, N, K,
+        _at("A", A, _MX4, d, _span(M, width, lda)), lda,
+        _at("scaleA", scaleA, _MX4_SCALE, d, _scales(K, ldsa, M), True), ldsa,
+        _at("B", B, _MX4, d, _span(N, width, ldb)), ldb,
+        _at("scaleB", scaleB, _MX4_SCALE, d, _scales(K, ldsb, N), True), ldsb,
+        None if bias is None else _at("bias", bias, _F32, d, N, True),
+        _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
 
 
 def mx4gemm_grouped(M, N, K, groups, offsets, A, lda, scaleA, ldsa, B, ldb, strideB, scaleB, ldsb,
@@ -171,16 +173,17 @@ def mx4gemm_grouped(M, N, K, groups, offsets, A, lda, scaleA, ldsa, B, ldb, stri
     width = _bytes(K)
     _in_int(strideSB=min(strideSB, 0))
     n = _scales(K, ldsb, N)
-    return _call(_lib.mx4gemm_grouped, d, stream, check, M, N, K, groups,
-                 _at("offsets", offsets, _I32, d, groups + 1, True),
-                 _at("A", A, _MX4, d, _span(M, width, lda)), lda,
-                 _at("scaleA", scaleA, _MX4_SCALE, d, _scales(K, ldsa, M), True), ldsa,
-                 _at("B", B, _MX4, d, _spans(groups, strideB, N, width, ldb)), ldb, strideB,
-                 _at("scaleB", scaleB, _MX4_SCALE, d,
-                     (groups - 1) * strideSB + n if groups > 0 and n > 0 else 0, True), ldsb,
-                 strideSB,
-                 None if bias is None else _at("bias", bias, _F32, d, groups * N, True),
-                 _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
+    return _experts._call(
+        _lib.mx4gemm_grouped, d, stream, check, M, N, K, groups,
+        _at("offsets", offsets, _I32, d, groups + 1, True),
+        _at("A", A, _MX4, d, _span(M, width, lda)), lda,
+        _at("scaleA", scaleA, _MX4_SCALE, d, _scales(K, ldsa, M), True), ldsa,
+        _at("B", B, _MX4, d, _spans(groups, strideB, N, width, ldb)), ldb, strideB,
+        _at("scaleB", scaleB, _MX4_SCALE, d,
+            (groups - 1) * strideSB + n if groups > 0 and n > 0 else 0, True), ldsb,
+        strideSB,
+        None if bias is None else _at("bias", bias, _F32, d, groups * N, True),
+        _at("C", C, _FLOATS, d, _span(M, N, ldc)), _TYPES[C.dtype], ldc)
 
 
 def mx4gemm_select_kernel(M, N, K, groups, aligned, num_cus) -> int:
@@ -220,11 +223,12 @@ def expert_layer(tokens, topk, experts, H, F, X, ldx, ids, weights, W1, ldw1, st
     elif w_type == 4:
         s1 = _at("scale1", scale1, _MX4_SCALE, d, experts * _scales(H, 2 * F, 2 * F), True)
         s2 = _at("scale2", scale2, _MX4_SCALE, d, experts * _scales(F, H, H), True)
-    return _call(_lib.expert_layer, d, stream, check, tokens, topk, experts, H, F,
-                 px, _TYPES[X.dtype], ldx,
-                 _at("ids", ids, _IDS, d, slots, True), ids.element_size(),
-                 None if weights is None else _at("weights", weights, _F32, d, slots, True),
-                 p1, w_type, ldw1, strideW1, s1,
-                 _at("W2", W2, (W1.dtype,), d, _spans(experts, strideW2, H, width2, ldw2)), ldw2,
-                 strideW2, s2, _at("out", out, (X.dtype,), d, _span(tokens, H, ldo)), ldo,
-                 *_workspace(workspace, d))
+    return _experts._call(
+        _lib.expert_layer, d, stream, check, tokens, topk, experts, H, F,
+        px, _TYPES[X.dtype], ldx,
+        _at("ids", ids, _IDS, d, slots, True), ids.element_size(),
+        None if weights is None else _at("weights", weights, _F32, d, slots, True),
+        p1, w_type, ldw1, strideW1, s1,
+        _at("W2", W2, (W1.dtype,), d, _spans(experts, strideW2, H, width2, ldw2)), ldw2,
+        strideW2, s2, _at("out", out, (X.dtype,), d, _span(tokens, H, ldo)), ldo,
+        *_workspace(workspace, d))

@@ -248,6 +248,30 @@ struct LayerShared {
     __attribute__((aligned(16))) signed char columns[kColumnBytes];
 };
 
+// The experts that up to 16 slots name, a bit each at its first slot; id: the
+// lane's slot's, or -1. Every lane of the wave gets the same.
+__device__ __forceinline__ unsigned long long first_slots(const LayerParams &p, int &id)
+{
+    const int lane = threadIdx.x & 63, slots = p.tokens * p.topk;
+    id = id_of(p, min(lane, slots - 1));
+    if (lane >= slots)
+        id = -1;
+    bool first = id >= 0;
+    for (int i = 0; i + 1 < slots; ++i) {
+        const int other = __builtin_amdgcn_readlane(id, i);
+        first = first & !((i < lane) & (other == id));
+    }
+    return __ballot(first);
+}
+
+// The lane of the nth bit.
+__device__ __forceinline__ int nth_bit(unsigned long long bits, int nth)
+{
+    for (; nth > 0; --nth)
+        bits &= bits - 1;
+    return __builtin_ctzll(bits);
+}
+
 // The `nth` group of up to 16 slots with one expert, that expert and the group's
 // slots (in sh.slots after the workgroup's next meeting): first each named
 // expert's first 16 slots, in the experts' order, then the second 16 of those
@@ -258,6 +282,18 @@ __device__ __forceinline__ bool find_slots(const LayerParams &p, int nth, LayerS
 {
     const int tid = threadIdx.x, lane = tid & 63;
     const int slots = p.tokens * p.topk;
+    if (slots <= kColumns) { // (few enough for each wave to find them in its registers)
+        int id;
+        const unsigned long long experts = first_slots(p, id);
+        if (nth >= __popcll(experts))
+            return false;
+        e = __builtin_amdgcn_readlane(id, nth_bit(experts, nth));
+        const unsigned long long mine = __ballot(id == e);
+        cols = __popcll(mine);
+        if (id == e)
+            sh.slots[__popcll(mine & ((1ull << lane) - 1))] = lane;
+        return true;
+    }
     constexpr int HELD = 8;
     int held[HELD]; // the ids of the first 512 slots, loaded side by side
     auto hold = [&](auto type) {
@@ -359,16 +395,17 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t whole(const void *base)
 // are, and DEPTH steps' loads are under way at once. A column's terms stand one
 // behind the other, 16 bytes further in each column than a multiple of 256, so
 // that the 16 columns that are read together lie in different banks.
-template <typename M, bool UP, int NT, bool EVEN, typename Row>
+template <typename M, bool UP, int NT, bool EVEN, int WAVES, typename Row, typename Shared>
 __device__ __forceinline__ void
 products(const typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type &rows,
          const typename M::In *in, Row row_of, int K, int cols, bool live, int part, int parts,
-         LayerShared &sh, f32x4 (&acc)[NT])
+         Shared &sh, f32x4 (&acc)[NT])
 {
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
     constexpr int SPAN = 4 * M::EPC;            // elements of a step
     constexpr int ES = (int)sizeof(typename M::Elem);
-    constexpr int DEPTH = NT == 2 ? 2 : 1;
+    constexpr int DEPTH = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+    constexpr int HALF = NT > 1 ? NT / 2 : 1;
     struct Step {
         i32x4 w[NT];
         uint32_t word[NT];
@@ -380,7 +417,7 @@ products(const typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type &rows
             if constexpr (EVEN) {
                 to.w[t] = __builtin_bit_cast(
                     i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                               rows.w[UP ? t / (NT / 2) : 0],
+                               rows.w[UP ? t / HALF : 0],
                                16 * c < rows.wbytes ? rows.offw[t] + 16u * c : kOutside, 0, 0));
                 if constexpr (M::MX4)
                     to.word[t] = __builtin_amdgcn_raw_buffer_load_b32(
@@ -392,7 +429,7 @@ products(const typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type &rows
             }
         }
     };
-    const int room = (kColumnBytes / cols - 16) / (ES * M::NX) / 128 * 128;
+    const int room = ((int)sizeof(sh.columns) / cols - 16) / (ES * M::NX) / 128 * 128;
     const int chunk = min(room, (K + 127) / 128 * 128), steps = (K + SPAN - 1) / SPAN;
     const int plane = chunk * ES, column = M::NX * plane + 16;
     for (int k0 = 0; k0 < K; k0 += chunk) {
@@ -404,18 +441,18 @@ products(const typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type &rows
                 load(first + part + d * parts, ring[d]);
         __syncthreads(); // (what stood in LDS has been read)
         const int here = min(chunk, (K - k0 + 127) / 128 * 128);
-        // A wave takes every kLayerWaves-th of the columns' pieces of 64 * VEC
+        // A wave takes every WAVES-th of the columns' pieces of 64 * VEC
         // elements, AT of them at a time.
         constexpr int AT = 4 / M::NR > 0 ? 4 / M::NR : 1, PIECE = 64 * M::VEC;
         const int each = (here + PIECE - 1) / PIECE, pieces = cols * each;
         const uint32_t inverse = inverse_of(each);
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        for (int i = wave; i < pieces; i += AT * kLayerWaves) {
+        for (int i = wave; i < pieces; i += AT * WAVES) {
             i32x4 raw[AT][M::NR];
             int c[AT], k[AT];
 #pragma unroll
             for (int a = 0; a < AT; ++a) {
-                const int at = min(i + a * kLayerWaves, pieces - 1);
+                const int at = min(i + a * WAVES, pieces - 1);
                 c[a] = divide(at, inverse);
                 k[a] = (at - c[a] * each) * PIECE + lane * M::VEC;
             }
@@ -510,13 +547,13 @@ __device__ __forceinline__ void give(const f32x4 (&acc)[NT], int parts, f32x4 (*
     __syncthreads();
 }
 
-// W1: NT / 2 times 16 rows of the gate and as many of the other part a tile, for
-// up to 16 slots of an expert.
+// W1: NT / 2 times 16 rows of the gate and as many of the other part a tile (NT =
+// 1: 8 and 8, in one instruction's rows), for up to 16 slots of an expert.
 template <typename X, typename W, int NT, bool EVEN>
 __global__ void __launch_bounds__(kLayerThreads) layer_up_kernel(LayerParams p)
 {
     typedef Math<X, W, true> M;
-    constexpr int HALF = NT / 2;
+    constexpr int HALF = NT > 1 ? NT / 2 : 1, ROWS = NT > 1 ? 16 * HALF : 8;
     __shared__ LayerShared sh;
     f32x4(*sums)[NT][64] = reinterpret_cast<f32x4(*)[NT][64]>(sh.columns);
     static_assert(sizeof(f32x4[kLayerWaves][NT][64]) <= kColumnBytes, "the sums fit");
@@ -524,7 +561,7 @@ __global__ void __launch_bounds__(kLayerThreads) layer_up_kernel(LayerParams p)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int part = wave & (p.parts - 1), each = kLayerWaves / p.parts; // tiles of a workgroup
     const int blocks = (p.tiles + each - 1) / each;
-    const int f0 = ((int)(blockIdx.x % blocks) * each + wave / p.parts) * 16 * HALF;
+    const int f0 = ((int)(blockIdx.x % blocks) * each + wave / p.parts) * ROWS;
     int e, cols;
     if (!find_slots(p, blockIdx.x / blocks, sh, e, cols))
         return;
@@ -546,10 +583,11 @@ __global__ void __launch_bounds__(kLayerThreads) layer_up_kernel(LayerParams p)
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int row = min(f0 + 16 * (t % HALF) + r, p.F - 1);
-        const int at = row + (t / HALF) * p.F;
+        const bool other = NT > 1 ? t / HALF : r >= 8;
+        const int row = min(f0 + 16 * (t % HALF) + (NT > 1 ? r : r & 7), p.F - 1);
+        const int at = row + (other ? p.F : 0);
         if constexpr (EVEN) {
-            rows.offw[t] = (uint32_t)((row - base) * (int)p.ldw1);
+            rows.offw[t] = (uint32_t)(((NT > 1 ? row : at) - base) * (int)p.ldw1);
             rows.offs[t] = 4u * at;
         } else {
             rows.w[t] = w1 + at * p.ldw1;
@@ -557,7 +595,7 @@ __global__ void __launch_bounds__(kLayerThreads) layer_up_kernel(LayerParams p)
         }
     }
     f32x4 acc[NT] = {};
-    products<M, true, NT, EVEN>(
+    products<M, true, NT, EVEN, kLayerWaves>(
         rows, static_cast<const X *>(p.X),
         [&](int c) { return divide(sh.slots[c], p.inverse) * p.ldx; }, p.H, cols, live, part,
         p.parts, sh, acc);
@@ -571,7 +609,16 @@ __global__ void __launch_bounds__(kLayerThreads) layer_up_kernel(LayerParams p)
             continue;
         // The lane's four inner values, one behind the other.
         const f32x4 gate = joined(acc, t, p.parts, sums);
-        const f32x4 up = joined(acc, HALF + t, p.parts, sums);
+        f32x4 up;
+        if constexpr (NT > 1) {
+            up = joined(acc, HALF + t, p.parts, sums);
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                up[v] = __shfl_down(gate[v], 32);
+            if (lane >= 32)
+                continue;
+        }
         const int f = f0 + 16 * t + 4 * (lane >> 4);
         f32x4 a;
 #pragma unroll
@@ -630,7 +677,7 @@ __global__ void __launch_bounds__(kLayerThreads) layer_down_kernel(LayerParams p
         }
     }
     f32x4 acc[NT] = {};
-    products<M, false, NT, EVEN>(
+    products<M, false, NT, EVEN, kLayerWaves>(
         rows, p.inner, [&](int c) { return (long long)sh.slots[c] * p.inner_cols; }, p.F, cols,
         live, part, p.parts, sh, acc);
     give(acc, p.parts, sums);
@@ -658,6 +705,72 @@ __global__ void __launch_bounds__(kLayerThreads) layer_down_kernel(LayerParams p
                     to[h + v] = y[v];
         }
     }
+}
+
+// Up to 8 slots: 16 rows of W2 a workgroup with the whole sum over a token's
+// slots, so that no partial products are written and read again. A column is a
+// slot; each of 8 waves takes an expert, or a part of one's K.
+constexpr int kFewSlots = 8;
+
+struct FewShared {
+    f32x4 sums[kFewSlots][4][kFewSlots]; // by part of K, four rows and slot
+    __attribute__((aligned(16))) signed char columns[56 << 10];
+};
+
+template <typename X, typename W>
+__global__ void __launch_bounds__(64 * kFewSlots) layer_down_few_kernel(LayerParams p)
+{
+    typedef Math<X, W, false> M;
+    __shared__ FewShared sh;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int slots = p.tokens * p.topk, h0 = (int)blockIdx.x * 16;
+    int id; // (of the lane's slot, as is its weight)
+    const unsigned long long experts = first_slots(p, id);
+    const float mix = p.mix ? p.mix[min(lane, slots - 1)] : 1.0f;
+    const int named = __popcll(experts);
+    int parts = 1; // (no expert may be named at all)
+    while (2 * parts * max(named, 1) <= kFewSlots)
+        parts *= 2;
+    const int nth = wave / parts, part = wave & (parts - 1);
+    const bool live = nth < named;
+    const int e = live ? __builtin_amdgcn_readlane(id, nth_bit(experts, nth)) : 0;
+    const int row = min(h0 + r, p.H - 1);
+    Even<1> rows;
+    rows.wbytes = M::MX4 ? (p.F + 1) / 2 : p.F * (M::I8 ? 1 : (int)sizeof(X));
+    rows.w[0] = rows.w[1] =
+        whole(static_cast<const signed char *>(p.W2) + e * p.strideW2 + h0 * p.ldw2);
+    rows.sc = whole(static_cast<const uint32_t *>(p.scale2) +
+                    (M::MX4 ? e * ((p.F + 127LL) / 128) * p.H : 0));
+    rows.ldsc = (uint32_t)p.H * 4;
+    rows.offw[0] = (uint32_t)((row - h0) * (int)p.ldw2);
+    rows.offs[0] = 4u * row;
+    f32x4 acc[1] = {};
+    // (Slots without an expert hold no inner values: a column of theirs is some
+    // bits that no one uses.)
+    products<M, false, 1, true, kFewSlots>(
+        rows, p.inner, [&](int c) { return (long long)c * p.inner_cols; }, p.F, slots, live, part,
+        parts, sh, acc);
+    if (live && __shfl(id, r) == e && r < slots)
+        sh.sums[part][q][r] = acc[0];
+    __syncthreads();
+    // Thread i < 16 * tokens: row i % 16 of token i / 16.
+    const int t = min(tid >> 4, p.tokens - 1), h = min(h0 + (tid & 15), p.H - 1);
+    float sum = 0.0f;
+    for (int j = 0; j < p.topk; ++j) {
+        const int slot = t * p.topk + j, expert = __shfl(id, slot);
+        const float w = __shfl(mix, slot);
+        if (expert < 0)
+            continue;
+        float y = 0.0f;
+        for (int i = 0; i < parts; ++i)
+            y += sh.sums[i][(tid & 15) >> 2][slot][tid & 3];
+        if constexpr (M::I8)
+            y *= static_cast<const float *>(p.scale2)[(long long)expert * p.H + h];
+        sum = __builtin_fmaf(w, y, sum);
+    }
+    if (tid >> 4 < p.tokens && h0 + (tid & 15) < p.H)
+        static_cast<X *>(p.out)[t * p.ldo + h] = (X)sum;
 }
 
 // out[t] = sum_j mix[t, j] partial[t, j]. (A slot without an expert has no
@@ -743,24 +856,59 @@ template <typename X, typename W> int launch_layer(LayerParams p, hipStream_t s)
         };
         const bool even1 = even(p.W1, p.ldw1, p.strideW1, p.H, 2LL * p.F);
         const bool even2 = even(p.W2, p.ldw2, p.strideW2, p.F, p.H);
-        const bool wide1 = even1 && reached * ceil_div_ll(p.F, 32) * kLayerWaves >= 3000;
-        const bool wide2 = even2 && reached * ceil_div_ll(p.H, 64) * kLayerWaves >= 3000;
-        const LayerFn up = !even1  ? layer_up_kernel<X, W, 2, false>
-                           : wide1 ? layer_up_kernel<X, W, 4, true>
-                                   : layer_up_kernel<X, W, 2, true>;
-        const LayerFn down = !even2  ? layer_down_kernel<X, W, 2, false>
-                             : wide2 ? layer_down_kernel<X, W, 4, true>
-                                     : layer_down_kernel<X, W, 2, true>;
-        const LayerStep a = layer_step(up, p.F, wide1 ? 32 : 16, reached, most,
+        int cus = 0;
+        const int st = current_cus(&cus);
+        if (st != 0)
+            return st;
+        // Tiles: 64 rows where there are enough of them for the card, 32 or, with a
+        // few a CU, 16, where the CUs' shares come out more even (one token through 8
+        // experts, 768 x 2048 in bf16: 384 workgroups on 256 CUs take as long as 512
+        // would, 16.2 us, 768 of half the rows 13.5); but not of narrow weights, of
+        // which the activations' share grows (2 tokens, 2880 x 2880 in 4 bits: 29 us
+        // against 34).
+        auto tile = [&](bool even, int total, int rows) {
+            const double n = reached * ceil_div_ll(total, rows);
+            if (!even)
+                return 2;
+            if (n / 2 * kLayerWaves >= 3000)
+                return 4;
+            auto rounds = [&](double tiles) { return (double)(long long)(tiles / cus + 0.999); };
+            return !M::MX4 && !M::I8 && n <= 3.0 * cus && rounds(2 * n) < 2 * rounds(n) ? 1 : 2;
+        };
+        const int nt1 = tile(even1 && (p.F + 64LL) * p.ldw1 < INT32_MAX, p.F, 16);
+        const int nt2 = tile(even2, p.H, 32);
+        constexpr int NARROW = M::MX4 || M::I8 ? 2 : 1; // the narrowest tile
+        const LayerFn up = !even1     ? layer_up_kernel<X, W, 2, false>
+                           : nt1 == 4 ? layer_up_kernel<X, W, 4, true>
+                           : nt1 == 2 ? layer_up_kernel<X, W, 2, true>
+                                      : layer_up_kernel<X, W, NARROW, true>;
+        const LayerFn down = !even2     ? layer_down_kernel<X, W, 2, false>
+                             : nt2 == 4 ? layer_down_kernel<X, W, 4, true>
+                             : nt2 == 2 ? layer_down_kernel<X, W, 2, true>
+                                        : layer_down_kernel<X, W, NARROW, true>;
+        const LayerStep a = layer_step(up, p.F, 8 * nt1, reached, most,
                                        ceil_div_ll(row_bytes(p.H), 64));
-        const LayerStep b = layer_step(down, p.H, wide2 ? 64 : 32, reached, most,
+        const LayerStep b = layer_step(down, p.H, 16 * nt2, reached, most,
                                        ceil_div_ll(row_bytes(p.F), 64));
         if (!fits_launch((double)a.blocks, kLayerThreads) ||
             !fits_launch((double)b.blocks, kLayerThreads))
             return -22;
         hipError_t e = launch_step(a, p, s);
-        if (e == hipSuccess)
-            e = launch_step(b, p, s);
+        if (e != hipSuccess)
+            return (int)e;
+        // The whole sum in 16 rows a workgroup, unless that leaves CUs idle for
+        // longer than the partial products' way takes (4 us): a CU draws some 20 KB a
+        // us from memory.
+        const double drawn = reached * row_bytes(p.F) / 20e3;
+        const double tiles = (double)ceil_div_ll(p.H, 16);
+        const double whole = (double)ceil_div_ll((long long)tiles, cus) * 16 * drawn;
+        if (slots <= kFewSlots && even2 && whole < tiles / cus * 16 * drawn + 4.0) {
+            void *args[] = {&p};
+            return (int)hipLaunchKernel((const void *)layer_down_few_kernel<X, W>,
+                                        dim3((unsigned)ceil_div_ll(p.H, 16)),
+                                        dim3(64 * kFewSlots), args, 0, s);
+        }
+        e = launch_step(b, p, s);
         if (e != hipSuccess)
             return (int)e;
     }

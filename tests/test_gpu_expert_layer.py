@@ -138,6 +138,18 @@ def test_layer(env, T, k, E, H, F, dtype, kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,k,E,H,F", [(16, 2, 20, 960, 480), (64, 8, 64, 64, 416),
+                                       (64, 8, 128, 64, 800), (64, 8, 128, 1600, 32),
+                                       (1, 8, 16, 4160, 96), (2, 4, 8, 4160, 1056),
+                                       (8, 1, 2, 2080, 1312)])
+def test_every_tile(env, T, k, E, H, F, dtype, kind):
+    """Sizes at which the choice of tiles, of waves that share one and of the second
+    kernel falls each way."""
+    layer_case(env, T, k, E, H, F, dtype, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", TYPES)
 def test_odd_rows(env, dtype, kind):
     """Rows off any boundary, odd lengths, gaps between rows and experts."""
     layer_case(env, 4, 2, 5, 129, 67, dtype, kind, pads=(3, 5, 1, 7), shift=1)
