@@ -114,12 +114,14 @@ int expert_combine_grad(int tokens, int topk, int cols, const void *dout, int ty
  * Slots whose id is outside [0, experts) take part in nothing; a token without
  * any gets 0. A token may name an expert twice. weights may be NULL (1
  * everywhere).
- * Sums run in fp32. a is held as two 16-bit floating-point numbers that together
- * carry 16 bits of it (F32: all 24, in fp32 or three of them); out is rounded
- * once, after the sum over j in its order.
- * Only the experts that the tokens name are read, each once for up to 16 tokens
- * (of 64 that name it, four at most); beyond a few rows an expert, the sorted
- * path of expert_sort to expert_combine is the faster one.
+ * Sums run in fp32. a is multiplied as two 16-bit floating-point numbers that
+ * together carry 16 bits of it (F32: all 24, in fp32 or three of them); out is
+ * rounded once, after the sum over j in its order. An infinity among the weights
+ * may give NaN where it would give an infinity.
+ * Only the experts that the tokens name are read, each once for up to 16 of its
+ * slots; beyond that the sorted path of expert_sort to expert_combine is the
+ * faster one. Rows on 16-byte boundaries that hold a multiple of 16 bytes (MX4:
+ * of 32 elements) run the fast kernels.
  * workspace: at least expert_layer_workspace_size() bytes, 16-byte aligned, in
  * use until the work completes on `stream`: calls that overlap (two streams, two
  * captured graphs) need one each. Its contents need no preparation.

@@ -5,6 +5,7 @@
 
 #include "experts.h"
 
+#include <cmath>
 #include <type_traits>
 
 namespace {
@@ -843,10 +844,8 @@ template <typename X, typename W> int launch_layer(LayerParams p, hipStream_t s)
     p.inverse = inverse_of(p.topk);
     if (p.F > 0) {
         // Experts that even choices reach on average.
-        double missed = 1.0;
-        for (int i = 0; i < slots && missed > 1e-3; ++i)
-            missed *= 1.0 - 1.0 / p.experts;
-        const double reached = p.experts * (1.0 - missed) < 1.0 ? 1.0 : p.experts * (1.0 - missed);
+        const double even_reach = p.experts * (1.0 - std::pow(1.0 - 1.0 / p.experts, slots));
+        const double reached = even_reach < 1.0 ? 1.0 : even_reach;
         auto row_bytes = [](long long K) {
             return M::MX4 ? (K + 1) / 2 : M::I8 ? K : K * (long long)sizeof(X);
         };
@@ -856,6 +855,14 @@ template <typename X, typename W> int launch_layer(LayerParams p, hipStream_t s)
         };
         const bool even1 = even(p.W1, p.ldw1, p.strideW1, p.H, 2LL * p.F);
         const bool even2 = even(p.W2, p.ldw2, p.strideW2, p.F, p.H);
+        const long long steps1 = ceil_div_ll(row_bytes(p.H), 64);
+        const long long steps2 = ceil_div_ll(row_bytes(p.F), 64);
+        // (Refused before the device is asked: narrower tiles are for fewer of them.)
+        const LayerStep least1 = layer_step(nullptr, p.F, even1 ? 32 : 16, reached, most, steps1);
+        const LayerStep least2 = layer_step(nullptr, p.H, even2 ? 64 : 32, reached, most, steps2);
+        if (!fits_launch((double)least1.blocks, kLayerThreads) ||
+            !fits_launch((double)least2.blocks, kLayerThreads))
+            return -22;
         int cus = 0;
         const int st = current_cus(&cus);
         if (st != 0)
@@ -886,14 +893,7 @@ template <typename X, typename W> int launch_layer(LayerParams p, hipStream_t s)
                              : nt2 == 4 ? layer_down_kernel<X, W, 4, true>
                              : nt2 == 2 ? layer_down_kernel<X, W, 2, true>
                                         : layer_down_kernel<X, W, NARROW, true>;
-        const LayerStep a = layer_step(up, p.F, 8 * nt1, reached, most,
-                                       ceil_div_ll(row_bytes(p.H), 64));
-        const LayerStep b = layer_step(down, p.H, 16 * nt2, reached, most,
-                                       ceil_div_ll(row_bytes(p.F), 64));
-        if (!fits_launch((double)a.blocks, kLayerThreads) ||
-            !fits_launch((double)b.blocks, kLayerThreads))
-            return -22;
-        hipError_t e = launch_step(a, p, s);
+        hipError_t e = launch_step(layer_step(up, p.F, 8 * nt1, reached, most, steps1), p, s);
         if (e != hipSuccess)
             return (int)e;
         // The whole sum in 16 rows a workgroup, unless that leaves CUs idle for
@@ -908,7 +908,7 @@ template <typename X, typename W> int launch_layer(LayerParams p, hipStream_t s)
                                         dim3((unsigned)ceil_div_ll(p.H, 16)),
                                         dim3(64 * kFewSlots), args, 0, s);
         }
-        e = launch_step(b, p, s);
+        e = launch_step(layer_step(down, p.H, 16 * nt2, reached, most, steps2), p, s);
         if (e != hipSuccess)
             return (int)e;
     }

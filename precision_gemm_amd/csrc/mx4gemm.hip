@@ -512,9 +512,7 @@ __global__ void __launch_bounds__(64 * WAVES) mx4_stream_kernel(Mx4Params p)
             products(fa[u], sa[u], fb[u], sb[u]);
     }
     // The block at the rows' end.
-    for (; s < words && s < (words + U - 1) / U * U; ++s) {
-        if (s >= words || s / U % WAVES != wave)
-            break;
+    for (; s < words && s / U % WAVES == wave; ++s) {
         i32x4 fb[NT], fa[MT];
         uint32_t sb[NT], sa[MT];
         const uint32_t mask = scale_mask(s, p.K);

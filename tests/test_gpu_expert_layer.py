@@ -227,6 +227,35 @@ def test_infinities_stay_with_their_token(env, dtype):
         assert bool(outs[0][3].isnan().all()) and not bool(outs[0][1].isfinite().any())
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_subnormal_weights(env, dtype):
+    """Weights below the type's normal numbers count as what they are."""
+    torch, pg = env
+    T, H, F = 3, 64, 48
+    g = torch.Generator().manual_seed(2)
+    dt = getattr(torch, dtype)
+    small = 2.0 ** -17 if dtype == "float16" else 2.0 ** -129
+    x = (torch.randn(T, H, generator=g) * (2.0 ** 12 if dtype == "float16" else 2.0 ** 124)).to(dt)
+    w1 = (torch.randn(2 * F, H, generator=g) * small).to(dt)
+    w2 = (torch.randn(H, F, generator=g) * small).to(dt)
+    ids = torch.zeros(T, 1, dtype=torch.int32).cuda()
+    mix = torch.full((T, 1), 1 / small).cuda()
+    out = torch.zeros(T, H, dtype=dt).cuda()
+    ws = torch.zeros(pg.expert_layer_workspace_size(T, 1, H, F, dt), dtype=torch.uint8).cuda()
+    pg.expert_layer(T, 1, 1, H, F, x.cuda(), H, ids, mix, w1.cuda(), H, 0, None, w2.cuda(), F, 0,
+                    None, out, H, ws)
+    s = x.double() @ w1.double().T
+    a = s[:, :F] * torch.sigmoid(s[:, :F]) * s[:, F:]
+    want = a @ w2.double().T / small
+    size = a.abs() @ w2.double().abs().T / small
+    f = torch.finfo(dt)
+    # The sums' errors are those of test_layer at these sizes: 14 * 2^-22 of magnitudes
+    # (some 8 times a value here) twice, and the inner values' 2^-16.
+    allowed = size * (2.0 ** -16 + 2 * 8 * 14 * 2.0 ** -22) + want.abs() * f.eps
+    assert float(w1.double().abs().max()) < f.smallest_normal * 4 and bool(out.any())
+    assert bool(((out.cpu().double() - want).abs() <= allowed).all())
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_graph_and_streams(env, kind):
     """Captured after a norm and replayed with other ids between; the same on two
