@@ -239,15 +239,16 @@ def test_subnormal_weights(env, dtype):
     w1 = (torch.randn(2 * F, H, generator=g) * small).to(dt)
     w2 = (torch.randn(H, F, generator=g) * small).to(dt)
     ids = torch.zeros(T, 1, dtype=torch.int32).cuda()
-    mix = torch.full((T, 1), 1 / small).cuda()
+    weight = min(1 / small, 2.0 ** 100)
+    mix = torch.full((T, 1), weight).cuda()
     out = torch.zeros(T, H, dtype=dt).cuda()
     ws = torch.zeros(pg.expert_layer_workspace_size(T, 1, H, F, dt), dtype=torch.uint8).cuda()
     pg.expert_layer(T, 1, 1, H, F, x.cuda(), H, ids, mix, w1.cuda(), H, 0, None, w2.cuda(), F, 0,
                     None, out, H, ws)
     s = x.double() @ w1.double().T
     a = s[:, :F] * torch.sigmoid(s[:, :F]) * s[:, F:]
-    want = a @ w2.double().T / small
-    size = a.abs() @ w2.double().abs().T / small
+    want = a @ w2.double().T * weight
+    size = a.abs() @ w2.double().abs().T * weight
     f = torch.finfo(dt)
     # The sums' errors are those of test_layer at these sizes: 14 * 2^-22 of magnitudes
     # (some 8 times a value here) twice, and the inner values' 2^-16.
