@@ -196,6 +196,15 @@ template <typename X, typename W, bool UP> struct Math {
     }
 };
 
+constexpr int kColumns = 16; // slots that are multiplied at a time: an instruction's columns
+
+// Slots of one expert that a workgroup multiplies: the first kernel finds them and
+// leaves them for the second.
+struct LayerGroup {
+    int e, cols; // e: -1 for none
+    int slots[kColumns];
+};
+
 struct LayerParams {
     const void *X, *ids;
     const float *mix;
@@ -204,6 +213,7 @@ struct LayerParams {
     void *out;
     float *inner;    // the inner values, slots x inner_cols
     float *partial;  // W2's products, slots x H
+    LayerGroup *groups;
     long long strideW1, strideW2, ldw1, ldw2; // bytes
     long long ldx, ldo;
     int tokens, topk, experts, H, F;
@@ -239,8 +249,6 @@ __device__ __forceinline__ int id_of(const LayerParams &p, int slot)
     const long long v = static_cast<const long long *>(p.ids)[slot];
     return v >= 0 && v < p.experts ? (int)v : -1;
 }
-
-constexpr int kColumns = 16; // slots that are multiplied at a time: an instruction's columns
 
 struct LayerShared {
     int count[EXPERT_LAYER_MAX_EXPERTS]; // slots of each expert
@@ -563,8 +571,18 @@ __global__ void __launch_bounds__(kLayerThreads) layer_up_kernel(LayerParams p)
     const int part = wave & (p.parts - 1), each = kLayerWaves / p.parts; // tiles of a workgroup
     const int blocks = (p.tiles + each - 1) / each;
     const int f0 = ((int)(blockIdx.x % blocks) * each + wave / p.parts) * ROWS;
-    int e, cols;
-    if (!find_slots(p, blockIdx.x / blocks, sh, e, cols))
+    int e, cols = 0;
+    const bool any = find_slots(p, blockIdx.x / blocks, sh, e, cols);
+    if (blockIdx.x % blocks == 0 && wave == 0) { // (which wrote all slots itself)
+        LayerGroup &to = p.groups[blockIdx.x / blocks];
+        if (lane == 0) {
+            to.e = any ? e : -1;
+            to.cols = cols;
+        }
+        if (lane < cols)
+            to.slots[lane] = sh.slots[lane];
+    }
+    if (!any)
         return;
     const bool live = f0 < p.F; // (a wave without a tile still meets the others)
     typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type rows;
@@ -649,9 +667,12 @@ __global__ void __launch_bounds__(kLayerThreads) layer_down_kernel(LayerParams p
     const int part = wave & (p.parts - 1), each = kLayerWaves / p.parts;
     const int blocks = (p.tiles + each - 1) / each;
     const int h0 = ((int)(blockIdx.x % blocks) * each + wave / p.parts) * 16 * NT;
-    int e, cols;
-    if (!find_slots(p, blockIdx.x / blocks, sh, e, cols))
+    const LayerGroup &group = p.groups[blockIdx.x / blocks];
+    const int e = group.e, cols = group.cols;
+    if (e < 0)
         return;
+    if ((int)threadIdx.x < cols) // (read after the workgroup's next meeting)
+        sh.slots[threadIdx.x] = group.slots[threadIdx.x];
     const bool live = h0 < p.H;
     typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type rows;
     rows.wbytes = M::MX4 ? (p.F + 1) / 2 : p.F * (M::I8 ? 1 : (int)sizeof(X));
@@ -938,6 +959,10 @@ long long padded_cols(int F) { return ((long long)F + 3) / 4 * 4; }
 
 size_t inner_bytes(long long slots, int F) { return (size_t)slots * padded_cols(F) * sizeof(float); }
 
+// As many groups as slots at most, on a 16-byte boundary behind the inner values,
+// then the partial products.
+size_t group_bytes(long long slots) { return ((size_t)slots * sizeof(LayerGroup) + 15) / 16 * 16; }
+
 // Bytes of a row of weights; ldw has to reach as far.
 long long weight_row(int K, int w_type)
 {
@@ -952,7 +977,7 @@ extern "C" size_t expert_layer_workspace_size(int tokens, int topk, int H, int F
         F > kMaxWidth || !c_type_ok(type))
         return 0;
     const long long slots = (long long)tokens * topk;
-    return inner_bytes(slots, F) + (size_t)slots * H * sizeof(float);
+    return inner_bytes(slots, F) + group_bytes(slots) + (size_t)slots * H * sizeof(float);
 }
 
 extern "C" int expert_layer(int tokens, int topk, int experts, int H, int F, const void *X,
@@ -1004,8 +1029,10 @@ extern "C" int expert_layer(int tokens, int topk, int experts, int H, int F, con
     p.scale2 = scale2;
     p.out = out;
     p.inner = static_cast<float *>(workspace);
-    p.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                          inner_bytes((long long)tokens * topk, F));
+    const long long slots = (long long)tokens * topk;
+    char *at = static_cast<char *>(workspace) + inner_bytes(slots, F);
+    p.groups = reinterpret_cast<LayerGroup *>(at);
+    p.partial = reinterpret_cast<float *>(at + group_bytes(slots));
     p.strideW1 = strideW1 * es;
     p.strideW2 = strideW2 * es;
     p.ldw1 = (long long)ldw1 * es;

@@ -222,7 +222,8 @@ def test_workspaces(pg):
     assert size(4, 16385, torch.float16) == 0 and size(-1, 4, torch.float16) == 0
     size = pg.expert_layer_workspace_size
     assert size(1, 1, 1, 1, torch.float32) > 0
-    assert size(64, 8, 2048, 768, torch.bfloat16) == 512 * (768 * 4 + 2048 * 4)
+    values = 512 * (768 * 4 + 2048 * 4)  # the inner values and the partial products
+    assert values <= size(64, 8, 2048, 768, torch.bfloat16) <= values + 512 * 128
     for bad in ((-1, 1, 4, 4), (1, 0, 4, 4), (2049, 1, 4, 4), (1, 1, -1, 4), (1, 1, 4, 2**20 + 1)):
         assert size(*bad, torch.float32) == 0
     # without dweight the gradient takes none
