@@ -115,7 +115,7 @@ struct NormParams {
 // one pass over memory. CH = 0: rows of any length, read twice (h from H where
 // it is kept, which each thread wrote itself). Bound by memory: 16384 x 4096 in
 // bf16 to 8 bits takes 92 us (5.1 TB/s, a large copy's rate), 16384 x 2048 in
-// bf16 46 us (5.8, a part of it cached); 4 x 4096 3.7 us, a launch, one trip to
+// bf16 40 us (a part of it cached); 4 x 4096 3.5 us, a launch, one trip to
 // memory and one meeting of the row's waves, with the sum and the largest value
 // at once.
 template <typename T, typename Out, int NT, int CH>
@@ -283,9 +283,23 @@ int launch_norm(NormParams p, hipStream_t s)
     } else if (chunks <= 512) {
         fn = norm_kernel<T, Out, 256, 2>;
     } else if (chunks <= 1024) {
-        fn = norm_kernel<T, Out, 256, 4>;
+        // From here on as many threads as leave each two chunks, or more with
+        // 1024: a row is one trip to memory, and its arithmetic is short. 16 x 8192
+        // in bf16 with int8 out 5.3 us against 7.5 of 256 threads with four, 4096
+        // rows 44 against 48; slower at worst for 1024 x 8192 in fp32, 21.3
+        // against 19.9.
+        fn = norm_kernel<T, Out, 512, 2>;
+        threads = 512;
     } else if (chunks <= 2048) {
-        fn = norm_kernel<T, Out, 256, 8>;
+        // (256 threads with eight: 16 x 14915 in bf16 8.2 us against 15.6,
+        // 4096 x 16384 121 against 143.)
+        fn = norm_kernel<T, Out, 1024, 2>;
+        threads = 1024;
+    } else if (chunks <= 4096) {
+        // (With eight: 16 x 30000 in bf16 9.4 us against 15.1, 2048 rows 121
+        // against 164.)
+        fn = norm_kernel<T, Out, 1024, 4>;
+        threads = 1024;
     } else if (chunks <= 8192) {
         fn = norm_kernel<T, Out, 1024, 8>;
         threads = 1024;
@@ -338,7 +352,8 @@ struct GradParams {
 // As norm_kernel, but a row group (NT threads) takes every gridDim.x * ROWS-th
 // row, so that it can add up its rows' part of dweight in registers; the second
 // kernel adds the groups' sums. Rows come in a fixed order, so do the sums. Bound
-// by memory: 16384 x 2048 in bf16 takes 57 us (4.7 TB/s), 500 x 1000 in fp32 5.6.
+// by memory: 16384 x 2048 in bf16 takes 57 us (4.7 TB/s), 500 x 1000 in fp32 8.6,
+// of which the second kernel 5.
 template <typename T, int NT, int CH>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_grad_kernel(GradParams p)
 {

@@ -104,6 +104,13 @@ def test_sizes(env, M, K, dtype, i8):
 
 
 @pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K", [(3, 8192), (3, 8193), (5, 14915), (3, 20001), (2, 32768)])
+def test_long_rows(env, M, K, dtype, i8):
+    run_norm(env, M, K, dtype, i8=i8)
+
+
+@pytest.mark.parametrize("i8", [False, True])
 @pytest.mark.parametrize("residual,keep", [(False, False), (False, True), (True, False)])
 def test_without_parts(env, residual, keep, i8):
     run_norm(env, 9, 513, "bfloat16", residual, keep, i8=i8)
