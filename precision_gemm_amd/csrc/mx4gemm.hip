@@ -71,8 +71,9 @@ __device__ __forceinline__ void store_codes(unsigned char *q, int k, int K, uint
 
 // ROWS rows of 512 elements a workgroup, RW a wave, all loaded before the first is
 // rounded; the scales leave as neighbouring rows' words. Bound by memory: 16 rows,
-// 4 a wave (8192 x 4092 in fp32 40 us, 3.8 TB/s; 32 rows, 8 a wave, 44), few rows
-// one a wave (16 x 4096 in bf16 2.6 us, a launch and one trip to memory).
+// 4 a wave (8192 x 4092 in fp32 33 us, 4.6 TB/s; behind a pass that left its writes
+// to go to memory 40, with 32 rows, 8 a wave, 44), few rows one a wave (16 x 4096 in
+// bf16 2.4 us, a launch and one trip to memory).
 // A block's scale byte is the exponent field of its largest magnitude less 2
 // (fields are offset by 127 as the bytes are; subnormal ones have field 0), and
 // 2^-e is the number of field 254 - byte, so the quotient is an exact product
@@ -171,53 +172,78 @@ __device__ __forceinline__ float scale_of(uint32_t byte)
     return __builtin_bit_cast(float, bits);
 }
 
-// And back: two rows of 512 elements a wave. Bound by memory: 8192 x 4092 to fp32
-// takes 28 us (5.4 TB/s).
+// And back: kBackRows rows of 512 elements a wave, with a store of 16 bytes a lane,
+// so that neighbouring lanes fill whole lines. Bound by memory: 8192 x 4096 to fp32
+// that no cache holds takes 30.5 us (5 TB/s; 41 with two stores of a lane side by
+// side), 8192 x 4092, rows off a line, 36 (47). More rows a wave gain nothing there
+// and cost the few their latency (16 x 4096 in bf16: 2, 4 and 8 rows 2.4, 2.8, 3.8).
+constexpr int kBackRows = 2;
+
 template <typename T>
 __global__ void __launch_bounds__(256)
 mx4_dequantize_kernel(int M, int K, const unsigned char *Q, long long ldq,
                       const unsigned char *scale, long long lds, T *Y, long long ldy)
 {
+    constexpr int VEC = 16 / sizeof(T), PARTS = 8 / VEC;
+    typedef T tv __attribute__((ext_vector_type(VEC)));
+    typedef unsigned short u16_any __attribute__((aligned(1)));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int k = blockIdx.x * 512 + 8 * lane;
-    if (k >= K)
-        return;
+    const int k0 = blockIdx.x * 512 + VEC * lane;
+    const long long m0 = ((long long)blockIdx.y * 4 + wave) * kBackRows;
+    uint32_t codes[kBackRows][PARTS], bytes[kBackRows][PARTS];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const long long m = (long long)blockIdx.y * 8 + 2 * wave + r;
-        if (m >= M)
-            return;
-        const unsigned char *q = Q + m * ldq;
-        const float s = scale_of(scale[((k >> 7) * lds + m) * 4 + ((k >> 5) & 3)]);
-        uint32_t codes = 0;
-        if (k + 8 <= K) {
-            codes = (uint32_t)*reinterpret_cast<const i32_any *>(q + (k >> 1));
-        } else {
+    for (int r = 0; r < kBackRows; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (k + 2 * i < K)
-                    codes |= (uint32_t)q[(k >> 1) + i] << (8 * i);
+        for (int c = 0; c < PARTS; ++c) {
+            const long long m = m0 + r;
+            const int k = k0 + c * 64 * VEC;
+            codes[r][c] = bytes[r][c] = 0;
+            if (m >= M || k >= K)
+                continue;
+            const unsigned char *q = Q + m * ldq + (k >> 1);
+            bytes[r][c] = scale[((k >> 7) * lds + m) * 4 + ((k >> 5) & 3)];
+            if (k + VEC <= K) {
+                if constexpr (VEC == 4)
+                    codes[r][c] = *reinterpret_cast<const u16_any *>(q);
+                else
+                    codes[r][c] = (uint32_t)*reinterpret_cast<const i32_any *>(q);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC / 2; ++i)
+                    if (k + 2 * i < K)
+                        codes[r][c] |= (uint32_t)q[i] << (8 * i);
+            }
         }
-        float f[8];
-        auto pair = [&](f32x2 v, int i) {
-            f[i] = v[0];
-            f[i + 1] = v[1];
-        };
-        pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 0), 0);
-        pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 1), 2);
-        pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 2), 4);
-        pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, s, 3), 6);
-        T *y = Y + m * ldy + k;
-        if (k + 8 <= K) {
-            store4<T>(y, f32x4{f[0], f[1], f[2], f[3]});
-            store4<T>(y + 4, f32x4{f[4], f[5], f[6], f[7]});
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (k + i < K)
-                    y[i] = (T)f[i];
+    for (int r = 0; r < kBackRows; ++r)
+#pragma unroll
+        for (int c = 0; c < PARTS; ++c) {
+            const long long m = m0 + r;
+            const int k = k0 + c * 64 * VEC;
+            if (m >= M || k >= K)
+                continue;
+            const float s = scale_of(bytes[r][c]);
+            tv v;
+            auto pair = [&](f32x2 f, int i) {
+                v[i] = (T)f[0];
+                v[i + 1] = (T)f[1];
+            };
+            pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[r][c], s, 0), 0);
+            pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[r][c], s, 1), 2);
+            if constexpr (VEC == 8) {
+                pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[r][c], s, 2), 4);
+                pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[r][c], s, 3), 6);
+            }
+            T *y = Y + m * ldy + k;
+            if (k + VEC <= K) {
+                store16(y, __builtin_bit_cast(i32x4, v));
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (k + i < K)
+                        y[i] = v[i];
+            }
         }
-    }
 }
 
 template <typename T>
@@ -227,14 +253,15 @@ int launch_mx4_dequantize(int M, int K, const unsigned char *Q, long long ldq,
 {
     const unsigned columns = (unsigned)ceil_div_ll(K, 512);
     long long most = (1LL << 23) / columns;
-    most = 8 * (most < 1 ? 1 : most < 65535 ? most : 65535);
+    constexpr int rows = 4 * kBackRows; // a workgroup
+    most = rows * (most < 1 ? 1 : most < 65535 ? most : 65535);
     for (long long m0 = 0; m0 < M; m0 += most) {
         int n = (int)(M - m0 < most ? M - m0 : most);
         const unsigned char *q = Q + m0 * ldq, *sc = scale + 4 * m0;
         T *y = static_cast<T *>(Y) + m0 * ldy;
         void *args[] = {&n, &K, &q, &ldq, &sc, &lds, &y, &ldy};
         const hipError_t e = hipLaunchKernel((const void *)mx4_dequantize_kernel<T>,
-                                             dim3(columns, (unsigned)ceil_div_ll(n, 8)), dim3(256),
+                                             dim3(columns, (unsigned)ceil_div_ll(n, rows)), dim3(256),
                                              args, 0, s);
         if (e != hipSuccess)
             return (int)e;
