@@ -114,10 +114,9 @@ int expert_combine_grad(int tokens, int topk, int cols, const void *dout, int ty
  * Slots whose id is outside [0, experts) take part in nothing; a token without
  * any gets 0. A token may name an expert twice. weights may be NULL (1
  * everywhere).
- * Sums run in fp32. a is multiplied as two 16-bit floating-point numbers that
- * together carry 16 bits of it (F32: all 24, in fp32 or three of them); out is
+ * Sums run in fp32, and so is a held and multiplied, in all its 24 bits; out is
  * rounded once, after the sum over j in its order. An infinity among the weights
- * may give NaN where it would give an infinity.
+ * or the values of a may give NaN where it would give an infinity.
  * Only the experts that the tokens name are read, each once for up to 16 of its
  * slots; beyond that the sorted path of expert_sort to expert_combine is the
  * faster one. Rows on 16-byte boundaries that hold a multiple of 16 bytes (MX4:
