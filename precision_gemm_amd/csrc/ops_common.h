@@ -50,7 +50,9 @@ __device__ __forceinline__ void group_rows(const int *offsets, int g, int rows, 
 // wanted, or -1 for none. Every lane of the wave returns the same group, its
 // first row and row count, and the tile's first row within the group; false if
 // there is no such tile. A wave's lanes take groups/64 consecutive groups each
-// and add up their tiles with a scan over the lanes.
+// and add up their tiles with a scan over the lanes. Sums stop at the most tiles
+// that nondecreasing offsets give, so that decreasing ones, whose groups can hold
+// all rows each, do not pass what an int holds.
 template <typename Pick>
 __device__ __forceinline__ bool find_tile(const int *offsets, int groups, int rows, int bm,
                                           Pick pick, int &g_out, int &lo_out, int &n_out,
@@ -60,21 +62,24 @@ __device__ __forceinline__ bool find_tile(const int *offsets, int groups, int ro
     const unsigned per = ((unsigned)groups + 63u) >> 6;
     const int g0 = (int)min(lane * per, (unsigned)groups);
     const int g1 = (int)min(g0 + per, (unsigned)groups);
+    const int most = rows / bm + min(groups, rows);
     int tiles = 0;
     for (int g = g0; g < g1; ++g) {
         int lo, hi;
         group_rows(offsets, g, rows, lo, hi);
-        tiles += (hi - lo + bm - 1) / bm;
+        tiles = min(tiles + (hi - lo + bm - 1) / bm, most);
     }
     int upto = tiles; // tiles of lanes 0..lane
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int v = __shfl_up(upto, d);
         if (lane >= d)
-            upto += v;
+            upto = min(upto + v, most);
     }
     const int slot = pick(__builtin_amdgcn_readlane(upto, 63));
-    const int before = upto - tiles;
+    int before = __shfl_up(upto, 1);
+    if (lane == 0)
+        before = 0;
     const bool mine = slot >= before && slot < upto;
     const unsigned long long who = __ballot(mine);
     if (who == 0)
