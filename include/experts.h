@@ -27,8 +27,10 @@
  * invalid argument): 400 for expert_sort, 500 for expert_gather, 600 for
  * expert_combine, 700 for expert_combine_grad, 1700 for expert_layer; -22 for more
  * rows than a launch holds (over 2^23 tokens with rows of more than 2048 bytes,
- * twice as many for each halving of that). Nothing is launched on error. sgemm_status_string()
- * gives the message.
+ * twice as many for each halving of that; expert_layer: where F, or H / 2, times the
+ * experts that the slots can name and a 16th of the other slots passes some 2^30,
+ * with weights off its fast path). Nothing is launched on error.
+ * sgemm_status_string() gives the message.
  */
 #ifndef PRECISION_GEMM_AMD_EXPERTS_H
 #define PRECISION_GEMM_AMD_EXPERTS_H

@@ -886,7 +886,8 @@ template <typename X, typename W> int launch_layer(LayerParams p, hipStream_t s)
         const bool even2 = even(p.W2, p.ldw2, p.strideW2, p.F, p.H);
         const long long steps1 = ceil_div_ll(row_bytes(p.H), 64);
         const long long steps2 = ceil_div_ll(row_bytes(p.F), 64);
-        // (Refused before the device is asked: narrower tiles are for fewer of them.)
+        // (Refused before the device is asked: narrower tiles are for fewer of them,
+        // too few to be more than a launch holds.)
         const LayerStep least1 = layer_step(nullptr, p.F, even1 ? 32 : 16, reached, most, steps1);
         const LayerStep least2 = layer_step(nullptr, p.H, even2 ? 64 : 32, reached, most, steps2);
         if (!fits_launch((double)least1.blocks, kLayerThreads) ||
@@ -902,17 +903,19 @@ template <typename X, typename W> int launch_layer(LayerParams p, hipStream_t s)
         // would, 16.2 us, 768 of half the rows 13.5); but not of narrow weights, of
         // which the activations' share grows (2 tokens, 2880 x 2880 in 4 bits: 29 us
         // against 34).
-        auto tile = [&](bool even, int total, int rows) {
+        auto tile = [&](bool even, bool narrow, int total, int rows) {
             const double n = reached * ceil_div_ll(total, rows);
             if (!even)
                 return 2;
             if (n / 2 * kLayerWaves >= 3000)
                 return 4;
             auto rounds = [&](double tiles) { return (double)(long long)(tiles / cus + 0.999); };
-            return !M::MX4 && !M::I8 && n <= 3.0 * cus && rounds(2 * n) < 2 * rounds(n) ? 1 : 2;
+            return narrow && !M::MX4 && !M::I8 && n <= 3.0 * cus && rounds(2 * n) < 2 * rounds(n) ? 1
+                                                                                              : 2;
         };
-        const int nt1 = tile(even1 && (p.F + 64LL) * p.ldw1 < INT32_MAX, p.F, 16);
-        const int nt2 = tile(even2, p.H, 32);
+        // (The narrowest tile of W1 reaches both its parts by one offset of 32 bits.)
+        const int nt1 = tile(even1, (p.F + 64LL) * p.ldw1 < INT32_MAX, p.F, 16);
+        const int nt2 = tile(even2, true, p.H, 32);
         constexpr int NARROW = M::MX4 || M::I8 ? 2 : 1; // the narrowest tile
         const LayerFn up = !even1     ? layer_up_kernel<X, W, 2, false>
                            : nt1 == 4 ? layer_up_kernel<X, W, 4, true>
