@@ -439,10 +439,13 @@ products(const typename std::conditional<EVEN, Even<NT>, Ragged<NT>>::type &rows
                 if constexpr (M::MX4)
                     to.word[t] = __builtin_amdgcn_raw_buffer_load_b32(
                         rows.sc, rows.offs[t] + s * rows.ldsc, 0, 0);
+            } else if constexpr (M::MX4) {
+                // (An element behind an odd K would meet a zero, but with a large scale
+                // as an infinity.)
+                to.w[t] = mx4_chunk(rows.w[t], 16 * c, K);
+                to.word[t] = rows.sc[t][s * rows.ldsc];
             } else {
                 to.w[t] = row_chunk(rows.w[t], 16 * c, rows.wbytes);
-                if constexpr (M::MX4)
-                    to.word[t] = rows.sc[t][s * rows.ldsc];
             }
         }
     };

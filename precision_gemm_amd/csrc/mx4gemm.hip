@@ -342,21 +342,6 @@ __device__ __forceinline__ i32x8 operand(i32x4 v)
 
 constexpr int kFp4 = 4; // the instructions' number of the element type
 
-// The 16 bytes of a row of K elements from its byte k on (row_chunk), without
-// what the last byte holds beyond an odd K.
-__device__ __forceinline__ i32x4 mx4_chunk(const signed char *row, int k, int K)
-{
-    i32x4 v = row_chunk(row, k, (K + 1) >> 1);
-    const int last = (K >> 1) - k; // the byte that an odd K ends in
-    if ((K & 1) && last >= 0 && last < 16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i == last >> 2)
-                v[i] &= ~(0xf0 << (8 * (last & 3)));
-    }
-    return v;
-}
-
 // The bytes of a word of scales that belong to blocks: all but in a row's last.
 __device__ __forceinline__ uint32_t scale_mask(int word, int K)
 {

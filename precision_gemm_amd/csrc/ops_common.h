@@ -247,6 +247,24 @@ __device__ __forceinline__ i32x4 row_chunk(const signed char *row, int k, int K)
     return i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
 }
 
+// The 16 bytes of a row of K 4-bit elements from its byte k on (row_chunk), without
+// what the last byte of an odd K holds beyond it. (Whole chunks first: a lane that
+// clears has to wait for what it has loaded.)
+__device__ __forceinline__ i32x4 mx4_chunk(const signed char *row, int k, int K)
+{
+    if (k + 16 <= K >> 1)
+        return load16(row + k);
+    i32x4 v = row_chunk(row, k, (K + 1) >> 1);
+    const int last = (K >> 1) - k; // the byte that an odd K ends in
+    if ((K & 1) && last >= 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i == last >> 2)
+                v[i] &= ~(0xf0 << (8 * (last & 3)));
+    }
+    return v;
+}
+
 constexpr uint32_t kOutside = 0x80000000u;
 constexpr int kMaxTileLd = 1 << 22;
 

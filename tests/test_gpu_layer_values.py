@@ -87,3 +87,141 @@ def test_inner_values_keep_24_bits(env, T, k, E, H, F, dtype, kind):
     dt = getattr(torch, dtype)
     got = run(env, x.to(dt), ids, E, w1, w2, kind)
     assert torch.equal(got, want.to(dt))
+
+
+class Blocks:
+    """A 4-bit layer: random codes, and a scale byte of all blocks of W1's gate, its
+    other part and W2."""
+
+    def __init__(self, torch, g, E, H, F, gate=126, other=126, down=126):
+        self.torch, self.E, self.H, self.F = torch, E, H, F
+        self.c1 = torch.randint(0, 16, (E, 2 * F, H + H % 2), generator=g)
+        self.c2 = torch.randint(0, 16, (E, H, F + F % 2), generator=g)
+        self.s1 = torch.full((E, (H + 127) // 128, 2 * F, 4), gate, dtype=torch.uint8)
+        self.s1[:, :, F:] = other
+        self.s2 = torch.full((E, (F + 127) // 128, H, 4), down, dtype=torch.uint8)
+
+    def run(self, pg, x, ids, mix=None):
+        torch, E, H, F = self.torch, self.E, self.H, self.F
+        w1, w2 = ((c[..., 0::2] + 16 * c[..., 1::2]).to(torch.uint8).cuda()
+                  for c in (self.c1, self.c2))
+        d1, d2 = w1.shape[2], w2.shape[2]
+        T, k = ids.shape
+        out = torch.full((T, H), 7.0, dtype=x.dtype).cuda()
+        ws = torch.full((pg.expert_layer_workspace_size(T, k, H, F, x.dtype),), 255,
+                        dtype=torch.uint8).cuda()
+        pg.expert_layer(T, k, E, H, F, x.cuda(), H, ids.int().cuda(),
+                        None if mix is None else mix.cuda(), w1, d1, 2 * F * d1, self.s1.cuda(), w2,
+                        d2, H * d2, self.s2.cuda(), out, H, ws)
+        return out.cpu()
+
+
+def some_tokens(torch, g, T, H, dt):
+    """Tokens of 0.5 to 2 (either sign), each a bf16 number, so that they can be scaled."""
+    x = 0.5 + 1.5 * torch.rand(T, H, generator=g)
+    return (x * (1 - 2 * torch.randint(0, 2, (T, H), generator=g))).bfloat16().to(dt)
+
+
+# even rows of one and of several words, the whole-sum kernel, ragged rows
+BLOCK_SIZES = [(1, 2, 4, 64, 96), (1, 8, 16, 4160, 96), (20, 2, 3, 320, 160), (5, 2, 3, 130, 75)]
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T,k,E,H,F", BLOCK_SIZES)
+def test_ends_of_the_scales(env, T, k, E, H, F, dtype):
+    """Blocks of 2^-127 (whose elements are subnormal bf16) and of 2^125, the largest
+    that the rounding writes, give what blocks of about 1 give with the other
+    operand scaled by the inverse power of two. To the bit, but where W2's are
+    subnormal: an instruction drops what lies below 2^-22 of the largest of what it
+    adds, whose size it takes from the exponents' fields, and a subnormal factor's
+    field, that of 2^-126, is up to four times its value of 2^-128 and more. So each
+    of the instructions, three of 32 k, drops up to 2^-20 of the magnitudes' sum on
+    either side. (W1's products, of 8 and 2 bits, lose nothing at all: they are
+    multiples of 2^-9 of the scales, and all sums below 2^15 of them.)"""
+    torch, pg = env
+    g = torch.Generator().manual_seed(H)
+    dt = getattr(torch, dtype)
+    x = some_tokens(torch, g, T, H, dt)
+    ids = torch.rand(T, E, generator=g).argsort(1)[:, :k]
+    log(f"[ends of the scales] T={T} k={k} E={E} H={H} F={F} {dtype}")
+    b = Blocks(torch, g, E, H, F, 120, 120)
+    want = b.run(pg, x, ids)
+    assert bool(want.isfinite().all()) and bool((want != 0).any(1).all())
+    for byte, power in ((0, 120), (1, 119)):
+        b.s1[:] = byte
+        assert torch.equal(b.run(pg, x * 2.0 ** power, ids), want)
+    b.s1[:] = 252
+    want = b.run(pg, x * 2.0 ** -125, ids)
+    b.s1[:] = 127
+    assert torch.equal(b.run(pg, x, ids), want) and bool(want.isfinite().all())
+    # W2, with inner values scaled by W1's other part: by 2^126 from those of 2^-18 and less
+    b.s1[:, :, :F] = 120
+    b.s1[:, :, F:] = 100
+    b.s2[:] = 126
+    want = b.run(pg, x, ids)
+    b.s1[:, :, F:] = 226
+    b.s2[:] = 0
+    level = torch.tensor(LEVELS + [-v for v in LEVELS], dtype=torch.float64)
+    w1, w2 = level[b.c1[..., :H]], level[b.c2[..., :F]] / 2
+    size = torch.zeros(T, H, dtype=torch.float64)
+    for t in range(T):
+        for e in ids[t].tolist():
+            s = w1[e] @ x[t].double()
+            gate, up = s[:F] * 2.0 ** -7, s[F:] * 2.0 ** -27
+            size[t] += w2[e].abs() @ (gate * torch.sigmoid(gate) * up).abs()
+    allowed = 2 * 3 * -(-F // 32) * 2.0 ** -20 * size + want.double().abs() * torch.finfo(dt).eps
+    got = b.run(pg, x, ids)
+    assert bool(((got.double() - want.double()).abs() <= allowed).all())
+    assert bool((want != 0).any(1).all())
+    b.s1[:, :, F:] = 100
+    b.s2[:] = 252
+    assert torch.equal(b.run(pg, x, ids, torch.full((T, k), 2.0 ** -126)), want)
+
+
+@pytest.mark.parametrize("T,k,E,H,F", BLOCK_SIZES)
+def test_blocks_of_nan(env, T, k, E, H, F):
+    """A block with the scale NaN spoils the outputs it is part of: all of the tokens
+    that name its expert, of W2 their row's, and no others."""
+    torch, pg = env
+    g = torch.Generator().manual_seed(F)
+    x = some_tokens(torch, g, T, H, torch.bfloat16)
+    ids = torch.rand(T, E, generator=g).argsort(1)[:, :k]
+    e = ids[0, 0].item()
+    named = (ids == e).any(1)
+    b = Blocks(torch, g, E, H, F, 120, 120)
+    want = b.run(pg, x, ids)
+    assert bool(want.isfinite().all())
+    for row in (F // 2, F + F // 3):
+        b.s1[e, 0, row, 1] = 255
+        got = b.run(pg, x, ids)
+        assert bool(got[named].isnan().all()) and torch.equal(got[~named], want[~named])
+        b.s1[e, 0, row, 1] = 120
+    b.s2[e, 0, H // 2, 1] = 255
+    got = b.run(pg, x, ids)
+    bad = torch.zeros(T, H, dtype=torch.bool)
+    bad[named, H // 2] = True
+    assert torch.equal(got.isnan(), bad) and torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H,F", [(33, 48), (64, 65), (161, 97)])
+def test_unused_halves_of_bytes(env, H, F, dtype):
+    """The high half of an odd row's last byte is no element: whatever it and a large
+    scale would make, it counts for nothing."""
+    torch, pg = env
+    g = torch.Generator().manual_seed(H + F)
+    T, k, E = 4, 2, 3
+    x = some_tokens(torch, g, T, H, getattr(torch, dtype))
+    ids = torch.rand(T, E, generator=g).argsort(1)[:, :k]
+    b = Blocks(torch, g, E, H, F, 122, 122)
+    for c, s, K in ((b.c1, b.s1, H), (b.c2, b.s2, F)):
+        if K % 2:  # the last block holds one element, a zero
+            c[:, :, K - 1] = 0
+            s[:, -1, :, K // 32 % 4] = 254
+            c[:, :, K] = 0
+    want = b.run(pg, x, ids)
+    assert bool(want.isfinite().all()) and bool(want.any())
+    for c, K in ((b.c1, H), (b.c2, F)):
+        if K % 2:
+            c[:, :, K] = torch.randint(5, 8, c[:, :, K].shape, generator=g)
+    assert torch.equal(b.run(pg, x, ids), want)
