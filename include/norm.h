@@ -16,9 +16,14 @@
  * inputs, but where it says that one may be an input itself: the same address
  * and leading dimension.
  *
- * A sum of squares beyond fp32's range (elements of 2^63 and more) makes rstd 0,
- * an infinity in h too: its own element of Y is NaN then, the row's others are 0.
- * A NaN in h makes the row NaN.
+ * The squares are added in fp32 before they are divided by K. A sum beyond its
+ * range (a root mean square of 2^64 / sqrt(K) and more) makes rstd 0, and an
+ * infinity in h does: its own element of Y is NaN then, the row's others are 0. A
+ * NaN in h makes the row NaN. With eps 0, a sum that is 0 (a row of zeros, or of
+ * nothing but elements below 2^-75) makes rstd infinite: Y is NaN where h is 0
+ * and infinite elsewhere, the scale of rms_norm_i8 is infinite, and rms_norm_grad
+ * gives no finite number in that row of dX nor in dweight. (With rstd 0 and a
+ * finite row its dX is dH.)
  *
  * Status codes: 0 success, a positive hipError_t, or minus (a base for the
  * call + the position of the first invalid argument): 1000 for rms_norm, 1100
