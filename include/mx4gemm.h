@@ -59,8 +59,9 @@ int mx4_quantize_rows(int M, int K, const void *X, int x_type, int ldx, unsigned
                       unsigned char *scale, int lds, sgemm_stream_t stream);
 
 /*
- * And back: Y[m,k] = element * scale, rounded once to Y's type (exact in F32 and
- * BF16; beyond F16's range infinite).
+ * And back: Y[m,k] = element * scale, rounded once to Y's type: exact in F32 and
+ * BF16, but infinite beyond the type's range (of F32 and BF16: elements of 4 and
+ * more with the byte 253, of 2 and more with 254, which the rounding never writes).
  * Positions: M 1, K 2, Q 3, ldq 4, scale 5, lds 6, Y 7, y_type 8, ldy 9.
  */
 int mx4_dequantize_rows(int M, int K, const unsigned char *Q, int ldq, const unsigned char *scale,

@@ -17,8 +17,9 @@ namespace {
 // small and comes from the caches. Each workgroup finds its expert and that
 // expert's slots from the ids itself, so nothing has to be sorted first.
 //
-// Weights of 8 and 4 bits and the scales of the latter are exact in bf16, so
-// those products run in bf16 (8-bit weights of fp16 tokens: in fp16) on as many
+// Weights of 8 bits are exact in bf16, and so are those of 4 bits times their scale,
+// from 2^-128 to below 2^128 (the scale bytes 253 and 254 make infinities of some),
+// so those products run in bf16 (8-bit weights of fp16 tokens: in fp16) on as many
 // terms as the other operand needs to lose nothing: fp16 tokens are two bf16
 // numbers, fp32 ones three. The layer's inner values, fp32 in memory, are three
 // terms (with fp32 weights fp32 themselves): all 24 bits. Two, 16 bits, would take

@@ -225,3 +225,31 @@ def test_unused_halves_of_bytes(env, H, F, dtype):
         if K % 2:
             c[:, :, K] = torch.randint(5, 8, c[:, :, K].shape, generator=g)
     assert torch.equal(b.run(pg, x, ids), want)
+
+
+@pytest.mark.parametrize("T,k,E,H,F", BLOCK_SIZES)
+def test_blocks_beyond_the_range(env, T, k, E, H, F):
+    """An element whose value is 2^128 counts as an infinity; 3 * 2^126, which both of
+    the last scale bytes can make, as what it is."""
+    torch, pg = env
+    g = torch.Generator().manual_seed(H)
+    x = some_tokens(torch, g, T, H, torch.bfloat16)
+    ids = torch.rand(T, E, generator=g).argsort(1)[:, :k]
+    e = ids[0, 0].item()
+    named = (ids == e).any(1)
+    b = Blocks(torch, g, E, H, F, 120, 120)
+    f = F + F // 2  # a row whose second block is one element; no other row sees it
+    b.c1[:, :, 40] = b.c1[:, f, 32:64] = 0
+
+    def with_element(byte, code, token):
+        b.s1[e, 0, f, 1], b.c1[e, f, 40] = byte, code
+        x[:, 40] = token
+        return b.run(pg, x, ids)
+
+    want = with_element(127, 5, 1.0)
+    assert bool(want.isfinite().all())
+    for byte, code in ((253, 5), (254, 3)):
+        assert torch.equal(with_element(byte, code, 2.0 ** -126), want)
+    for byte, code in ((253, 6), (254, 4)):
+        got = with_element(byte, code, 2.0 ** -126)
+        assert not bool(got[named].isfinite().any()) and torch.equal(got[~named], want[~named])

@@ -77,3 +77,22 @@ def test_sums_of_groups(env, K):
         if hi > lo:
             want[lo:hi] = torch.mm(a[lo:hi], b[e * N:(e + 1) * N].t().contiguous())
     assert torch.equal(C.double(), want)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+def test_every_element_with_every_scale(env, dtype):
+    """The way back of all 16 codes and 256 scale bytes; beyond the type's range it
+    is infinite."""
+    torch, pg = env
+    from test_gpu_mx4gemm import value
+    dt = getattr(torch, dtype)
+    code = torch.arange(16).repeat(256, 2)
+    byte = torch.arange(256)[:, None]
+    scale = torch.zeros(1, 256, 4, dtype=torch.uint8)
+    scale[0, :, 0] = byte[:, 0].to(torch.uint8)
+    Y = torch.zeros(256, 32, dtype=dt).cuda()
+    pg.mx4_dequantize_rows(256, 32, packed(torch, code).cuda(), 16, scale.cuda(), 256, Y, 32)
+    want = value(torch, code, byte, 32).to(dt)
+    assert torch.equal(Y.cpu().isnan(), want.isnan()) and bool(want[255].isnan().all())
+    assert torch.equal(Y.cpu()[:255], want[:255])
+    assert bool(want[253, [6, 7]].isinf().all()) and bool(want[254, 4:8].isinf().all())

@@ -1,5 +1,5 @@
-"""The norms at the ends of fp32's range, and over more rows than one launch
-takes."""
+"""The norms at the ends of fp32's range, over more rows than one launch takes, and
+gradients whose sums are exact."""
 import sys
 
 import pytest
@@ -109,3 +109,27 @@ def test_many_rows(env, i8):
             assert torch.equal(scale[lo:lo + n], s) and bool(s.any())
     assert bool((H[M:] == 7).all()) and bool((out[M:] == 77).all()) and bool((scale[M:] == 7).all())
     assert not bool((H[:M] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("M,K", [(1, 1), (33, 64), (300, 1024), (1030, 8192), (2, 16384), (5000, 2048),
+                                 (20000, 300), (16385, 40), (70, 129)])
+def test_exact_gradients(env, M, K, dtype):
+    """Rows of 1 and -1 with eps = 0 have rstd 1, and whole dY and dH make every sum a
+    whole number (below 2^24): dweight, and dX where K is a power of two, are
+    compared for equality, so that no row or column can be lost or taken twice."""
+    torch, pg = env
+    log(f"[exact gradients] {M}x{K} {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    dt = getattr(torch, dtype)
+    h = 1 - 2 * torch.randint(0, 2, (M, K), generator=g, device="cuda").double()
+    dy, dh = (torch.randint(-8, 9, (M, K), generator=g, device="cuda").double() for _ in range(2))
+    w = torch.exp2(torch.randint(-1, 2, (K,), generator=g, device="cuda").float())
+    dX, dw = torch.full((M, K), 7.0, dtype=dt).cuda(), torch.full((K,), 7.0).cuda()
+    ws = torch.full((pg.rms_norm_grad_workspace_size(M, K, dt),), 255, dtype=torch.uint8).cuda()
+    pg.rms_norm_grad(M, K, dy.to(dt), K, h.to(dt), K, w, 0.0, dh.to(dt), K, dX, K, dw, ws)
+    assert torch.equal(dw.double(), (dy * h).sum(0))
+    if K & (K - 1) == 0:
+        wdy = dy * w.double()
+        want = dh + wdy - h * (wdy * h).sum(1, keepdim=True) / K
+        assert torch.equal(dX, want.to(dt))
