@@ -28,10 +28,10 @@ namespace {
 // rounding. The terms are made once a workgroup, as its columns of activations
 // are brought to LDS.
 //
-// 64 tokens through 8 of 128 experts, 2048 x 768, in bf16 with 4-bit weights: 45
-// us for W1 (4.2 TB/s), 28 for W2, 5 for the sums; 16 through 4 of 64, 2048 x 1024,
-// fp16 with 8-bit weights: 27, 17 and 4.7; one through 8 of 128 in bf16: 13.4 (of
-// 50 MB; 6 without the weights' loads), 8.7 and 4.
+// 64 tokens through 8 of 128 experts, 2048 x 768, in bf16 with 4-bit weights: 46
+// us for W1 (4.2 TB/s), 32 for W2, 5 for the sums; 16 through 4 of 64, 2048 x 1024,
+// fp16 with 8-bit weights: 28, 18 and 4.7; one through 8 of 128 in bf16: 13.4 (of
+// 50 MB; 6 without the weights' loads), 9 and 4.
 
 struct Mx4 {};
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));

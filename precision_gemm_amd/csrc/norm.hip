@@ -115,7 +115,7 @@ struct NormParams {
 // one pass over memory. CH = 0: rows of any length, read twice (h from H where
 // it is kept, which each thread wrote itself). Bound by memory: 16384 x 4096 in
 // bf16 to 8 bits takes 92 us (5.1 TB/s, a large copy's rate), 16384 x 2048 in
-// bf16 40 us (a part of it cached); 4 x 4096 3.5 us, a launch, one trip to
+// bf16 45 us (a part of it cached); 4 x 4096 3.5 us, a launch, one trip to
 // memory and one meeting of the row's waves, with the sum and the largest value
 // at once.
 template <typename T, typename Out, int NT, int CH>
