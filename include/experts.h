@@ -116,9 +116,9 @@ int expert_combine_grad(int tokens, int topk, int cols, const void *dout, int ty
  * Slots whose id is outside [0, experts) take part in nothing; a token without
  * any gets 0. A token may name an expert twice. weights may be NULL (1
  * everywhere).
- * Sums run in fp32, and so is a held and multiplied, in all its 24 bits (with
- * weights of 16 bits and less down to 2^-133); out is rounded once, after the sum
- * over j in its order. An infinity among the weights or the values of a may give
+ * Sums run in fp32, and so are tokens and a held and multiplied, in all their bits
+ * (24 of F32 tokens and of a, with narrower weights down to 2^-133); out is rounded
+ * once, after the sum over j in its order. An infinity among the weights or the values of a may give
  * NaN where it would give an infinity; a 4-bit weight of 2^128 or more (scale bytes
  * 253 and 254, which mx4_quantize_rows never writes) counts as one, and a block
  * with the scale NaN makes what it is part of NaN.
