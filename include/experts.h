@@ -118,10 +118,10 @@ int expert_combine_grad(int tokens, int topk, int cols, const void *dout, int ty
  * everywhere).
  * Sums run in fp32, and so are tokens and a held and multiplied, in all their bits
  * (24 of F32 tokens and of a, with narrower weights down to 2^-133); out is rounded
- * once, after the sum over j in its order. An infinity among the weights or the values of a may give
- * NaN where it would give an infinity; a 4-bit weight of 2^128 or more (scale bytes
- * 253 and 254, which mx4_quantize_rows never writes) counts as one, and a block
- * with the scale NaN makes what it is part of NaN.
+ * once, after the sum over j in its order. An infinity among the weights or the
+ * values of a may give NaN where it would give an infinity; a 4-bit weight of 2^128
+ * or more (scale bytes 253 and 254, which mx4_quantize_rows never writes) counts as
+ * one, and a block with the scale NaN makes what it is part of NaN.
  * Only the experts that the tokens name are read, each once for up to 16 of its
  * slots; beyond that the sorted path of expert_sort to expert_combine is the
  * faster one. Rows on 16-byte boundaries that hold a multiple of 16 bytes (MX4:
